@@ -422,6 +422,67 @@ rb_status rb_qat_autotune(const void* X, const void* dY, rb_dtype a_dtype, int64
                           int64_t ldy, float* dW, int64_t lddw, void* dX, rb_dtype dx_dtype, int64_t lddx,
                           void* stream);
 
+/* ---------------------------------------------------------------------------------------
+ * rb_adamw_* -- one AdamW step over many tensors at once (the shared weights and the scales of
+ * coupled-training layers: rb_qat_backward gives their gradients), in one launch.
+ *     g' = g grad_scale;  m <- beta1 m + (1 - beta1) g';  v <- beta2 v + (1 - beta2) g'^2
+ *     p <- p (1 - lr_t wd) - lr_t / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ *   with lr_t = lr * lr_mult of the tensor and wd its weight_decay; the arithmetic is fp32.
+ *   state_bits = 32: m and v are fp32 [n].
+ *   state_bits = 8: m and v are bytes [n] with one fp32 scale per 256 elements each (m_scale and
+ *   v_scale, [ceil(n / 256)]; the last group may be short). An element of m is
+ *   e4m3(byte) / 256 * scale, of sqrt(v) (the root is what is held) likewise; e4m3 is the 8-bit
+ *   float of 4 exponent (bias 7) and 3 fraction bits without infinities. A scale is the power of
+ *   two above its group's largest finite magnitude (within 2^-99 .. 2^126). Rounding is
+ *   stochastic: the 20 fraction bits cut off (of the fp32 number that stands for the quotient
+ *   with its scale) are rounded up when they exceed 16 random bits, a hash of seed, step and the
+ *   element's position in the plan, the low half of a 32-bit hash for m and the high half for
+ *   sqrt(v). The same call on the same inputs gives the same result. A nonzero sqrt(v) keeps
+ *   the smallest nonzero code at least; what is not finite becomes NaN. All-zero bytes are the
+ *   state before the first step, whatever the scales.
+ *   A NaN or infinity in a gradient makes that element's parameter and states NaN or infinite and
+ *   no other's.
+ *
+ * The plan. rb_adamw_plan checks the tensors and writes an image of them (host memory,
+ * rb_adamw_plan_bytes bytes) that the caller copies to the device once; steps then read it there.
+ * Gradients are read from the same addresses at every step. It makes no HIP call.
+ *   n        elements, >= 0, contiguous (0: the tensor is skipped and its pointers are not used)
+ *   p_dtype, g_dtype   RB_F32, RB_F16, RB_BF16; equal, or one of them RB_F32
+ *   p, g     aligned to their element; m and v to 4 bytes with state_bits 32; scales to 4 bytes
+ *            (NULL with state_bits 32). Pointers at 16 bytes (8 for 2-byte types) make the
+ *            accesses wide; others only cost time.
+ *   count    0 .. 2^20; chunks receives the number of 4096-element chunks (below 2^31), which
+ *            the steps take. Tensors must not overlap.
+ * rb_adamw_plan_bytes: 0 if t is NULL with count > 0, count is out of range or an n is negative.
+ *
+ * rb_adamw_step
+ *   plan        the image in device memory, 16-byte aligned;  chunks, state_bits as planned (a step
+ *               whose state_bits are not the plan's changes nothing)
+ *   step        1, 2, ...: the number of this step;  lr, eps finite, lr >= 0, eps > 0;
+ *               0 <= beta1, beta2 < 1
+ *   grad_scale  optional device fp32, multiplied into every gradient (a clip factor, an inverse
+ *               loss scale);  skip  optional device int32: the step changes nothing if it is not 0
+ * --------------------------------------------------------------------------------------- */
+typedef struct rb_adamw_tensor {
+  void* p;
+  const void* g;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  int64_t n;
+  float lr_mult;       /* finite, >= 0 */
+  float weight_decay;  /* finite, >= 0 */
+  int32_t p_dtype;
+  int32_t g_dtype;
+} rb_adamw_tensor;
+size_t rb_adamw_plan_bytes(const rb_adamw_tensor* t, int64_t count);
+rb_status rb_adamw_plan(const rb_adamw_tensor* t, int64_t count, int32_t state_bits, void* image,
+                        size_t image_bytes, int64_t* chunks);
+rb_status rb_adamw_step(const void* plan, int64_t chunks, int32_t state_bits, int64_t step, double lr, double beta1,
+                        double beta2, double eps, const float* grad_scale, const int32_t* skip, uint32_t seed,
+                        void* stream);
+
 #ifdef __cplusplus
 }
 #endif

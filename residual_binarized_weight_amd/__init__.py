@@ -16,6 +16,7 @@ return CUDA (HIP) tensors on the current device and enqueue on the current strea
   Y, planes, What = qat_forward(W, g, h, X)      ... and the layer's product Y = X What^T
   dW, dX, dg, dh = qat_backward(dY, X, What, planes, g, h)   straight-through backward
   qat_autotune(X, dY, What, Y, dW, dX)           pick the fastest GEMM kernels for a shape
+  adamw_step(plan, step, lr)                     AdamW over many tensors (adamw_plan), states in 32 or 8 bits
 """
 from __future__ import annotations
 
@@ -30,7 +31,7 @@ from ._lib import (RB_F16, RB_F32, RB_BF16, RB_OP_CODEBOOK_GEMV, RB_OP_GEMM_SMAL
 
 __all__ = ["pack", "gemv", "gemv_variant", "gemm_small", "codebook_encode", "codebook_gemv", "codebook_mstep",
            "codebook_distinct", "codebook_learn", "svid_init", "qat_derive",
-           "qat_forward", "qat_matmul", "qat_backward", "qat_autotune", "workspace",
+           "qat_forward", "qat_matmul", "qat_backward", "qat_autotune", "adamw_plan", "adamw_step", "AdamWPlan", "workspace",
            "workspace_bytes", "storage_bits_per_weight", "version", "RbError", "lib"]
 
 _DT = {torch.float32: RB_F32, torch.float16: RB_F16, torch.bfloat16: RB_BF16}
@@ -337,3 +338,71 @@ def qat_autotune(X: torch.Tensor, dY: torch.Tensor, What: torch.Tensor, Y: torch
                                                  _dt(Y.dtype), Y.stride(0), _ptr_rows(dW), dW.stride(0),
                                                  _ptr_rows(dX), _dt(dX.dtype), dX.stride(0), _stream()))
 
+
+
+class AdamWPlan:
+    """The tensors of an optimizer, as adamw_step reads them: keeps the parameters, gradients and
+    states alive and their table on the device. m, v (and m_scale, v_scale with 8-bit states) are
+    lists in the parameters' order."""
+
+    def __init__(self, params, grads, state_bits, m, v, m_scale, v_scale, table, chunks):
+        self.params, self.grads, self.state_bits = params, grads, state_bits
+        self.m, self.v, self.m_scale, self.v_scale = m, v, m_scale, v_scale
+        self.table, self.chunks = table, chunks
+
+
+def adamw_plan(params, grads, state_bits: int = 32, m=None, v=None, m_scale=None, v_scale=None, weight_decay=0.0,
+               lr_mult=1.0) -> AdamWPlan:
+    """Lay out one AdamW step over `params` and their `grads` (lists of contiguous device tensors,
+    fp32 / fp16 / bf16). States are made, zero, unless given: fp32 with state_bits 32, with 8
+    torch.float8_e4m3fn (m, and sqrt(v) in v) and an fp32 scale per 256 elements. `weight_decay` and
+    `lr_mult` are numbers or lists of one per tensor. The gradients are read from these tensors at
+    every step: write new ones into them."""
+    params, grads, n = list(params), list(grads), len(params)
+    if state_bits not in (8, 32):
+        raise ValueError("state_bits must be 8 or 32")
+    if n == 0:
+        raise ValueError("adamw_plan needs a tensor at least")
+    sdt = torch.float32 if state_bits == 32 else torch.float8_e4m3fn
+    each = lambda x: list(x) if isinstance(x, (list, tuple)) else [x] * n  # noqa: E731
+    wd, lm = each(weight_decay), each(lr_mult)
+    m = [torch.zeros(p.shape, dtype=sdt, device=p.device) for p in params] if m is None else list(m)
+    v = [torch.zeros(p.shape, dtype=sdt, device=p.device) for p in params] if v is None else list(v)
+    rows = [(p.numel() + 255) // 256 for p in params]
+    if state_bits == 8:
+        m_scale, v_scale = ([torch.ones(r, device=p.device) for r, p in zip(rows, params)] if s is None else list(s)
+                            for s in (m_scale, v_scale))
+    else:
+        m_scale, v_scale = [None] * n, [None] * n
+    if not all(len(x) == n for x in (grads, wd, lm, m, v, m_scale, v_scale)):
+        raise ValueError("adamw_plan takes as many of each as there are parameters")
+    t = (_lib.AdamwTensor * n)()
+    for i in range(n):
+        p, g = params[i], grads[i]
+        if any(x.numel() != p.numel() for x in (g, m[i], v[i])) or m[i].dtype != sdt or v[i].dtype != sdt:
+            raise ValueError(f"tensor {i}: gradient and states must match the parameter, states in {sdt}")
+        if any(x.device != p.device for x in (g, m[i], v[i], params[0])):
+            raise ValueError(f"tensor {i}: all tensors of a plan live on one device")
+        if state_bits == 8 and any(s.numel() != rows[i] or s.dtype != torch.float32 or s.device != p.device
+                                   for s in (m_scale[i], v_scale[i])):
+            raise ValueError(f"tensor {i}: scales are fp32, one per 256 elements")
+        t[i] = _lib.AdamwTensor(_ptr(p), _ptr(g), _ptr(m[i]), _ptr(v[i]), _ptr(m_scale[i]), _ptr(v_scale[i]),
+                                p.numel(), lm[i], wd[i], _dt(p.dtype), _dt(g.dtype))
+    image = torch.zeros(lib.rb_adamw_plan_bytes(ctypes.byref(t), n), dtype=torch.uint8)
+    chunks = ctypes.c_int64()
+    check("rb_adamw_plan", lib.rb_adamw_plan(ctypes.byref(t), n, state_bits, ctypes.c_void_p(image.data_ptr()),
+                                             image.numel(), ctypes.byref(chunks)))
+    return AdamWPlan(params, grads, state_bits, m, v, m_scale, v_scale, image.to(params[0].device), chunks.value)
+
+
+def adamw_step(plan: AdamWPlan, step: int, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+               grad_scale: torch.Tensor | None = None, skip: torch.Tensor | None = None, seed: int = 0) -> None:
+    """Step number `step` (1, 2, ...) of AdamW over the plan's tensors, in place, in one launch.
+    `grad_scale` (device fp32) multiplies the gradients; the step changes nothing where `skip`
+    (device int32) is not 0; `seed` feeds the rounding of 8-bit states."""
+    if grad_scale is not None and grad_scale.dtype != torch.float32:
+        raise TypeError("grad_scale is a device fp32")
+    if skip is not None and skip.dtype != torch.int32:
+        raise TypeError("skip is a device int32")
+    check("rb_adamw_step", lib.rb_adamw_step(_ptr(plan.table), plan.chunks, plan.state_bits, step, lr, beta1, beta2,
+                                             eps, _ptr(grad_scale), _ptr(skip), seed & 0xFFFFFFFF, _stream()))

@@ -20,6 +20,12 @@ _i32 = ctypes.c_int32
 _i64 = ctypes.c_int64
 _sz = ctypes.c_size_t
 
+class AdamwTensor(ctypes.Structure):
+    """rb_adamw_tensor"""
+    _fields_ = [("p", _vp), ("g", _vp), ("m", _vp), ("v", _vp), ("m_scale", _vp), ("v_scale", _vp), ("n", _i64),
+                ("lr_mult", ctypes.c_float), ("weight_decay", ctypes.c_float), ("p_dtype", _i32), ("g_dtype", _i32)]
+
+
 # name -> (restype, argtypes); mirrors include/rb.h
 SIGNATURES = {
     "rb_version": (ctypes.c_int, []),
@@ -58,6 +64,10 @@ SIGNATURES = {
                                        _vp, _sz, _vp]),
     "rb_qat_autotune": (ctypes.c_int, [_vp, _vp, ctypes.c_int, _i64, _i64, _i64, _vp, _i64, _i64, _i64, _vp,
                                        ctypes.c_int, _i64, _vp, _i64, _vp, ctypes.c_int, _i64, _vp]),
+    "rb_adamw_plan_bytes": (_sz, [_vp, _i64]),
+    "rb_adamw_plan": (ctypes.c_int, [_vp, _i64, _i32, _vp, _sz, _vp]),
+    "rb_adamw_step": (ctypes.c_int, [_vp, _i64, _i32, _i64, ctypes.c_double, ctypes.c_double, ctypes.c_double,
+                                     ctypes.c_double, _vp, _vp, ctypes.c_uint32, _vp]),
     # streaming-read probe used by the bench (not part of the method)
     "rb_bench_stream_read": (ctypes.c_int, [_vp, _i64, _vp, _i32, _vp]),
     "rb_bench_gather": (ctypes.c_int, [_vp, ctypes.c_uint32, _i32, _vp, _i32, _vp]),

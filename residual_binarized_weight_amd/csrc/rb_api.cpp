@@ -425,4 +425,58 @@ rb_status rb_qat_autotune(const void* X, const void* dY, rb_dtype a_dtype, int64
                                           dX, dx_dtype, lddx, static_cast<hipStream_t>(stream)));
 }
 
+static bool adamw_counts_ok(const rb_adamw_tensor* t, int64_t count) {
+  if (count < 0 || count > (int64_t(1) << 20) || (count > 0 && !t)) return false;
+  int64_t chunks = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    if (t[i].n < 0) return false;
+    chunks += t[i].n / 4096 + 1;
+    if (chunks > kMaxDim) return false;
+  }
+  return true;
+}
+
+size_t rb_adamw_plan_bytes(const rb_adamw_tensor* t, int64_t count) {
+  return adamw_counts_ok(t, count) ? rb::adamw_plan_bytes(t, count) : 0;
+}
+
+rb_status rb_adamw_plan(const rb_adamw_tensor* t, int64_t count, int32_t state_bits, void* image, size_t image_bytes,
+                        int64_t* chunks) {
+  if (!image || !chunks || !adamw_counts_ok(t, count)) return RB_ERR_INVALID_ARG;
+  if (state_bits != 32 && state_bits != 8) return RB_ERR_INVALID_ARG;
+  for (int64_t i = 0; i < count; ++i) {
+    const rb_adamw_tensor& x = t[i];
+    const rb_dtype pd = static_cast<rb_dtype>(x.p_dtype), gd = static_cast<rb_dtype>(x.g_dtype);
+    if (!valid_dtype(pd) || !valid_dtype(gd)) return RB_ERR_INVALID_ARG;
+    if (!std::isfinite(x.lr_mult) || x.lr_mult < 0.f || !std::isfinite(x.weight_decay) || x.weight_decay < 0.f)
+      return RB_ERR_INVALID_ARG;
+    if (pd != gd && pd != RB_F32 && gd != RB_F32) return RB_ERR_UNSUPPORTED;
+    if (x.n == 0) continue;
+    if (!x.p || !x.g || !x.m || !x.v) return RB_ERR_INVALID_ARG;
+    if (state_bits == 8 && (!x.m_scale || !x.v_scale)) return RB_ERR_INVALID_ARG;
+    if (!elem_aligned(x.p, pd) || !elem_aligned(x.g, gd)) return RB_ERR_MISALIGNED;
+    if (state_bits == 32 ? !aligned(x.m, 4) || !aligned(x.v, 4) : !aligned(x.m_scale, 4) || !aligned(x.v_scale, 4))
+      return RB_ERR_MISALIGNED;
+  }
+  if (!aligned(image, 8)) return RB_ERR_MISALIGNED;
+  if (image_bytes < rb::adamw_plan_bytes(t, count)) return RB_ERR_WORKSPACE;
+  rb::adamw_fill_plan(t, count, state_bits, image);
+  *chunks = rb::adamw_chunks(t, count);
+  return RB_OK;
+}
+
+rb_status rb_adamw_step(const void* plan, int64_t chunks, int32_t state_bits, int64_t step, double lr, double beta1,
+                        double beta2, double eps, const float* grad_scale, const int32_t* skip, uint32_t seed,
+                        void* stream) {
+  if (!plan || chunks < 0 || chunks > kMaxDim || step < 1) return RB_ERR_INVALID_ARG;
+  if (state_bits != 32 && state_bits != 8) return RB_ERR_INVALID_ARG;
+  if (!std::isfinite(lr) || lr < 0.0 || !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0))
+    return RB_ERR_INVALID_ARG;
+  if (!std::isfinite(eps) || !(static_cast<float>(eps) > 0.f)) return RB_ERR_INVALID_ARG;
+  if (!aligned(plan, 16) || !aligned(grad_scale, 4) || !aligned(skip, 4)) return RB_ERR_MISALIGNED;
+  log_call("rb_adamw_step", chunks, state_bits, 0, 0);
+  return from_hip(rb::launch_adamw_step(plan, chunks, state_bits, step, lr, beta1, beta2, eps, grad_scale, skip, seed,
+                                        static_cast<hipStream_t>(stream)));
+}
+
 }  // extern "C"

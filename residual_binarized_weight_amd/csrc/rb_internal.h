@@ -113,4 +113,12 @@ hipError_t launch_qat_autotune(const void* X, const void* dY, rb_dtype a_dtype, 
                                int64_t ldy, float* dW, int64_t lddw, void* dX, rb_dtype dx_dtype, int64_t lddx,
                                hipStream_t stream);
 
+// multi-tensor optimizer step (rb_adamw.hip)
+int64_t adamw_chunks(const rb_adamw_tensor* t, int64_t count);
+size_t adamw_plan_bytes(const rb_adamw_tensor* t, int64_t count);
+void adamw_fill_plan(const rb_adamw_tensor* t, int64_t count, int state_bits, void* image);
+hipError_t launch_adamw_step(const void* plan, int64_t chunks, int state_bits, int64_t step, double lr, double beta1,
+                             double beta2, double eps, const float* grad_scale, const int32_t* skip, uint32_t seed,
+                             hipStream_t s);
+
 }  // namespace rb
