@@ -65,7 +65,8 @@ typedef enum rb_op {
   RB_OP_CODEBOOK_ENCODE = 3,
   RB_OP_CODEBOOK_GEMV = 4,
   RB_OP_SVID_INIT = 5,
-  RB_OP_QAT_BACKWARD = 6
+  RB_OP_QAT_BACKWARD = 6,
+  RB_OP_RESNORM_BACKWARD = 7 /* k = K = 1, N = D */
 } rb_op;
 
 /* Version of this ABI (major*10000 + minor*100 + patch). */
@@ -79,7 +80,7 @@ const char* rb_status_string(rb_status s);
  * 64-bit accumulator per output row), which rb_gemv and rb_gemv_variant need all-zero on
  * entry and return to all-zero before their last kernel ends; the bytes after it are
  * scratch. rb_gemm_small, rb_svid_init and rb_qat_backward use only bytes after the zero
- * region and never write it. So: zero-fill a workspace once after allocation, and one
+ * region and never write it; so does rb_resnorm_backward. So: zero-fill a workspace once after allocation, and one
  * buffer of the largest size its calls need can serve all of them (calls on one stream;
  * calls that overlap in time need separate workspaces). */
 size_t rb_workspace_bytes(rb_op op, int32_t k, int64_t N, int64_t K, int64_t M);
@@ -421,6 +422,52 @@ rb_status rb_qat_autotune(const void* X, const void* dY, rb_dtype a_dtype, int64
                           const void* What, int64_t ldwh, int64_t N, int64_t K, void* Y, rb_dtype y_dtype,
                           int64_t ldy, float* dW, int64_t lddw, void* dX, rb_dtype dx_dtype, int64_t lddx,
                           void* stream);
+
+/* ---------------------------------------------------------------------------------------
+ * rb_resnorm_* -- the norms between two blocks, in one pass: the norm after a block, its gate, the
+ * scaled residual stream, and the norm before the next block.
+ *     u = norm_post(Y);  S = alpha R + gate (.) u;  X = norm_pre(S)
+ *   row by row over D columns, norm(x) = (x - mu) rstd (.) w + b with rstd = (mean((x - mu)^2) +
+ *   eps)^(-1/2), mu = the row's mean for RB_NORM_LAYER and 0 for RB_NORM_RMS. Arithmetic and sums
+ *   are fp32; X is computed from the unrounded S.
+ * Shapes and types
+ *   M rows (>= 1, below 2^31), D columns (1 .. 16384); every leading dimension >= D, below 2^31
+ *   a_dtype   type of Y, X and a gate of rows: RB_F32, RB_F16, RB_BF16
+ *   s_dtype   type of the stream R, S: a_dtype or RB_F32
+ *   gate      NULL (ones); with ldg = 0 an fp32 [D] vector; otherwise [M][ldg] in a_dtype
+ *   post, pre rb_norm; w_*, b_* fp32 [D] (w needed where the norm is not RB_NORM_NONE; b NULL = 0)
+ *   stats     fp32 [M][4]: post mean, post rstd, pre mean, pre rstd (0 for RB_NORM_NONE)
+ *   Buffers are aligned to their element; rows need no other alignment. Elements past D of a row
+ *   are not touched.
+ *
+ * rb_resnorm_forward -- R may be NULL (no residual), S may be NULL (not kept), stats too; X must be
+ *   given where pre is not RB_NORM_NONE. alpha finite, eps finite and > 0. S may be R and X may be
+ *   Y (same leading dimension); other overlaps are not allowed.
+ *
+ * rb_resnorm_backward -- gradients from those of X (dX, needed where pre is not RB_NORM_NONE, as
+ *   are S and w_pre) and of S (dS, NULL = 0), with the forward's Y (may be NULL if post is
+ *   RB_NORM_NONE and there is no gate), S and stats; with d = dy (.) w and xh = (x - mu) rstd a
+ *   norm gives rstd (d - xh mean(d xh) - [layer] mean(d)):
+ *     T = dS + norm_pre's gradient;  dR = alpha T;  dgate = u (.) T;  dY = norm_post's gradient of gate (.) T
+ *   dY       output [M][lddy] in a_dtype;  dR  output [M][lddr] in s_dtype, NULL: not written
+ *   dgate    NULL, or like the gate: fp32 [D] summed over the rows (ldg = 0), else [M][lddg] a_dtype
+ *   dw_*, db_*   outputs fp32 [D], summed over the rows, NULL: not written. The sums are in a fixed
+ *            order: deterministic. Those of an RB_NORM_NONE must be NULL.
+ *   ws       rb_workspace_bytes(RB_OP_RESNORM_BACKWARD, 1, D, 1, M) bytes, 16-byte aligned; no
+ *            zero-filling needed. dY may be Y or dX, dR may be dS (same leading dimension).
+ * --------------------------------------------------------------------------------------- */
+typedef enum rb_norm { RB_NORM_NONE = 0, RB_NORM_RMS = 1, RB_NORM_LAYER = 2 } rb_norm;
+rb_status rb_resnorm_forward(const void* Y, rb_dtype a_dtype, int64_t M, int64_t D, int64_t ldy, const void* R,
+                             rb_dtype s_dtype, int64_t ldr, const void* gate, int64_t ldg, float alpha, int32_t post,
+                             const float* w_post, const float* b_post, int32_t pre, const float* w_pre,
+                             const float* b_pre, float eps, void* S, int64_t lds, void* X, int64_t ldx, float* stats,
+                             void* stream);
+rb_status rb_resnorm_backward(const void* dX, rb_dtype a_dtype, int64_t M, int64_t D, int64_t lddx, const void* dS,
+                              rb_dtype s_dtype, int64_t ldds, const void* Y, int64_t ldy, const void* S, int64_t lds,
+                              const float* stats, const void* gate, int64_t ldg, float alpha, int32_t post,
+                              const float* w_post, const float* b_post, int32_t pre, const float* w_pre, void* dY,
+                              int64_t lddy, void* dR, int64_t lddr, void* dgate, int64_t lddg, float* dw_post,
+                              float* db_post, float* dw_pre, float* db_pre, void* ws, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------------------
  * rb_adamw_* -- one AdamW step over many tensors at once (the shared weights and the scales of

@@ -16,6 +16,8 @@ return CUDA (HIP) tensors on the current device and enqueue on the current strea
   Y, planes, What = qat_forward(W, g, h, X)      ... and the layer's product Y = X What^T
   dW, dX, dg, dh = qat_backward(dY, X, What, planes, g, h)   straight-through backward
   qat_autotune(X, dY, What, Y, dW, dX)           pick the fastest GEMM kernels for a shape
+  S, X, stats = resnorm_forward(Y, R, w_pre)     S = alpha R + gate norm_post(Y), X = norm_pre(S)
+  grads = resnorm_backward(dX, dS, Y, S, stats, w_pre)   ... and its gradients
   adamw_step(plan, step, lr)                     AdamW over many tensors (adamw_plan), states in 32 or 8 bits
 """
 from __future__ import annotations
@@ -26,12 +28,13 @@ import torch
 
 from . import _lib
 from ._lib import (RB_F16, RB_F32, RB_BF16, RB_OP_CODEBOOK_GEMV, RB_OP_GEMM_SMALL, RB_OP_GEMV,
-                   RB_OP_QAT_BACKWARD, RB_OP_SVID_INIT, RB_QAT_ENGINE_AUTO, RB_QAT_ENGINE_MFMA,
+                   RB_OP_QAT_BACKWARD, RB_OP_RESNORM_BACKWARD, RB_OP_SVID_INIT, RB_QAT_ENGINE_AUTO, RB_QAT_ENGINE_MFMA,
                    RB_QAT_ENGINE_ROCBLAS, RbError, check, lib)
 
 __all__ = ["pack", "gemv", "gemv_variant", "gemm_small", "codebook_encode", "codebook_gemv", "codebook_mstep",
            "codebook_distinct", "codebook_learn", "svid_init", "qat_derive",
-           "qat_forward", "qat_matmul", "qat_backward", "qat_autotune", "adamw_plan", "adamw_step", "AdamWPlan", "workspace",
+           "qat_forward", "qat_matmul", "qat_backward", "qat_autotune", "resnorm_forward",
+           "resnorm_backward", "adamw_plan", "adamw_step", "AdamWPlan", "workspace",
            "workspace_bytes", "storage_bits_per_weight", "version", "RbError", "lib"]
 
 _DT = {torch.float32: RB_F32, torch.float16: RB_F16, torch.bfloat16: RB_BF16}
@@ -338,6 +341,105 @@ def qat_autotune(X: torch.Tensor, dY: torch.Tensor, What: torch.Tensor, Y: torch
                                                  _dt(Y.dtype), Y.stride(0), _ptr_rows(dW), dW.stride(0),
                                                  _ptr_rows(dX), _dt(dX.dtype), dX.stride(0), _stream()))
 
+
+
+_NORM = {"none": _lib.RB_NORM_NONE, "rms": _lib.RB_NORM_RMS, "layer": _lib.RB_NORM_LAYER}
+
+
+def _vec(name: str, t: torch.Tensor | None, n: int):
+    """A contiguous fp32 device vector of n elements, or None."""
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or t.numel() != n:
+        raise ValueError(f"{name} is an fp32 vector of {n} elements")
+    return _ptr(t)
+
+
+def _rows(name: str, t: torch.Tensor | None, shape, dtype):
+    """(pointer, row stride) of a matrix of this shape and type, or (None, 0)."""
+    if t is None:
+        return None, 0
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{name} is a {dtype} matrix of shape {tuple(shape)}")
+    return _ptr_rows(t), t.stride(0) if shape[0] > 1 else max(t.stride(0), shape[1])
+
+
+def _gate_rows(gate, shape, dtype):
+    """(pointer, row stride) of a gate: an fp32 vector (stride 0) or rows."""
+    if gate is not None and gate.dim() == 1:
+        return _vec("gate", gate, shape[1]), 0
+    return _rows("gate", gate, shape, dtype)
+
+
+def resnorm_forward(Y: torch.Tensor, R: torch.Tensor | None, w_pre: torch.Tensor | None, w_post=None, b_pre=None,
+                    b_post=None, gate=None, alpha: float = 1.0, eps: float = 1e-6, pre: str = "rms",
+                    post: str | None = None, S: torch.Tensor | None = None, X: torch.Tensor | None = None,
+                    stats: torch.Tensor | None = None):
+    """Between two blocks: S = alpha R + gate * norm_post(Y), X = norm_pre(S). Y [M][D] is the block's
+    output, R [M][D] the stream (Y's type or fp32; None: no residual), `gate` an fp32 vector [D], rows
+    [M][D] of Y's type or None; `pre` and `post` name the norms ("none", "rms", "layer"; post
+    defaults to "rms" where w_post is given), w_* and b_* are fp32 [D]. Returns (S, X, stats): S in
+    R's type, X in Y's (None for pre "none"), stats [M][4] fp32 for the backward."""
+    M, D = Y.shape
+    post = post or ("none" if w_post is None else "rms")
+    sdt = R.dtype if R is not None else S.dtype if S is not None else Y.dtype
+    if S is None:
+        S = torch.empty((M, D), dtype=sdt, device=Y.device)
+    if X is None and pre != "none":
+        X = torch.empty((M, D), dtype=Y.dtype, device=Y.device)
+    if stats is None:
+        stats = torch.empty((M, 4), dtype=torch.float32, device=Y.device)
+    shape, dt = Y.shape, Y.dtype
+    yp, ldy = _rows("Y", Y, shape, dt)
+    rp, ldr = _rows("R", R, shape, sdt)
+    gp, ldg = _gate_rows(gate, shape, dt)
+    sp, lds = _rows("S", S, shape, sdt)
+    xp, ldx = _rows("X", X, shape, dt)
+    check("rb_resnorm_forward", lib.rb_resnorm_forward(
+        yp, _dt(dt), M, D, ldy, rp, _dt(sdt), ldr, gp, ldg, alpha, _NORM[post], _vec("w_post", w_post, D),
+        _vec("b_post", b_post, D), _NORM[pre], _vec("w_pre", w_pre, D), _vec("b_pre", b_pre, D), eps, sp, lds, xp, ldx,
+        _vec("stats", stats, 4 * M), _stream()))
+    return S, X, stats
+
+
+def resnorm_backward(dX: torch.Tensor | None, dS: torch.Tensor | None, Y: torch.Tensor, S: torch.Tensor,
+                     stats: torch.Tensor, w_pre: torch.Tensor | None, w_post=None, b_post=None, gate=None,
+                     alpha: float = 1.0, pre: str = "rms", post: str | None = None, bias: bool = False,
+                     dY: torch.Tensor | None = None, dR: torch.Tensor | None = None, ws: torch.Tensor | None = None):
+    """Gradients of resnorm_forward's inputs from those of X (dX) and S (dS; None: zero), in a dict:
+    dY, dR, dgate (like the gate), dw_pre, dw_post and, with `bias`, db_pre, db_post (fp32 [D]); None
+    where there is no such input. Other arguments as in the forward call."""
+    M, D = Y.shape
+    dev, dt, sdt, shape = Y.device, Y.dtype, S.dtype, Y.shape
+    post = post or ("none" if w_post is None else "rms")
+    has_pre, has_post = pre != "none", post != "none"
+    if dY is None:
+        dY = torch.empty(shape, dtype=dt, device=dev)
+    if dR is None:
+        dR = torch.empty(shape, dtype=sdt, device=dev)
+    # the vectors' gradients lie in one buffer
+    names = [n for n, there in (("dw_pre", has_pre), ("db_pre", has_pre and bias), ("dw_post", has_post),
+                                ("db_post", has_post and bias), ("dgate", gate is not None and gate.dim() == 1)) if there]
+    vec = dict(zip(names, torch.empty((len(names), D), dtype=torch.float32, device=dev).unbind(0))) if names else {}
+    out = {"dY": dY, "dR": dR, "dgate": None, "dw_pre": None, "dw_post": None, "db_pre": None, "db_post": None, **vec}
+    if gate is not None and gate.dim() != 1:
+        out["dgate"] = torch.empty(shape, dtype=dt, device=dev)
+    if ws is None:
+        ws = torch.empty(workspace_bytes(RB_OP_RESNORM_BACKWARD, 1, D, 1, M), dtype=torch.uint8, device=dev)
+    dxp, lddx = _rows("dX", dX, shape, dt)
+    dsp, ldds = _rows("dS", dS, shape, sdt)
+    yp, ldy = _rows("Y", Y, shape, dt)
+    sp, lds = _rows("S", S, shape, sdt)
+    gp, ldg = _gate_rows(gate, shape, dt)
+    dyp, lddy = _rows("dY", dY, shape, dt)
+    drp, lddr = _rows("dR", dR, shape, sdt)
+    dg = out["dgate"]
+    check("rb_resnorm_backward", lib.rb_resnorm_backward(
+        dxp, _dt(dt), M, D, lddx, dsp, _dt(sdt), ldds, yp, ldy, sp, lds, _vec("stats", stats, 4 * M), gp, ldg, alpha,
+        _NORM[post], _vec("w_post", w_post, D), _vec("b_post", b_post, D), _NORM[pre], _vec("w_pre", w_pre, D), dyp,
+        lddy, drp, lddr, _ptr(dg), D, _ptr(out["dw_post"]), _ptr(out["db_post"]), _ptr(out["dw_pre"]),
+        _ptr(out["db_pre"]), _ptr(ws), ws.numel(), _stream()))
+    return out
 
 
 class AdamWPlan:

@@ -13,7 +13,8 @@ RB_OK, RB_ERR_INVALID_ARG, RB_ERR_UNSUPPORTED, RB_ERR_MISALIGNED, RB_ERR_WORKSPA
 RB_F32, RB_F16, RB_BF16 = 0, 1, 2
 RB_QAT_ENGINE_AUTO, RB_QAT_ENGINE_MFMA, RB_QAT_ENGINE_ROCBLAS = 0, 1, 2
 (RB_OP_PACK, RB_OP_GEMV, RB_OP_GEMM_SMALL, RB_OP_CODEBOOK_ENCODE, RB_OP_CODEBOOK_GEMV, RB_OP_SVID_INIT,
- RB_OP_QAT_BACKWARD) = range(7)
+ RB_OP_QAT_BACKWARD, RB_OP_RESNORM_BACKWARD) = range(8)
+RB_NORM_NONE, RB_NORM_RMS, RB_NORM_LAYER = 0, 1, 2
 
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
@@ -64,6 +65,12 @@ SIGNATURES = {
                                        _vp, _sz, _vp]),
     "rb_qat_autotune": (ctypes.c_int, [_vp, _vp, ctypes.c_int, _i64, _i64, _i64, _vp, _i64, _i64, _i64, _vp,
                                        ctypes.c_int, _i64, _vp, _i64, _vp, ctypes.c_int, _i64, _vp]),
+    "rb_resnorm_forward": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, ctypes.c_int, _i64, _vp, _i64,
+                                          ctypes.c_float, _i32, _vp, _vp, _i32, _vp, _vp, ctypes.c_float, _vp, _i64,
+                                          _vp, _i64, _vp, _vp]),
+    "rb_resnorm_backward": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, ctypes.c_int, _i64, _vp, _i64,
+                                           _vp, _i64, _vp, _vp, _i64, ctypes.c_float, _i32, _vp, _vp, _i32, _vp, _vp,
+                                           _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "rb_adamw_plan_bytes": (_sz, [_vp, _i64]),
     "rb_adamw_plan": (ctypes.c_int, [_vp, _i64, _i32, _vp, _sz, _vp]),
     "rb_adamw_step": (ctypes.c_int, [_vp, _i64, _i32, _i64, ctypes.c_double, ctypes.c_double, ctypes.c_double,

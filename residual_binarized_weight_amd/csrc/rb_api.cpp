@@ -25,6 +25,8 @@ bool is_pow2_in(int32_t v, int32_t lo, int32_t hi) {
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
 constexpr int64_t kQatMaxDim = int64_t(1) << 28;  // N and K of the training layer (32-bit byte offsets)
 
+constexpr int64_t kResnormMaxD = 16384;  // a row is held in one block's registers
+
 bool act_dtype(rb_dtype d) { return d == RB_F16 || d == RB_BF16; }
 bool elem_aligned(const void* p, rb_dtype d) { return aligned(p, d == RB_F32 ? 4 : 2); }
 
@@ -101,6 +103,8 @@ size_t rb_workspace_bytes(rb_op op, int32_t k, int64_t N, int64_t K, int64_t M) 
     case RB_OP_SVID_INIT: return (N > kMaxDim || K > kMaxDim) ? 0 : rb::zero_region_bytes(N) + rb::svid_workspace_bytes(k, N, K);
     case RB_OP_QAT_BACKWARD:
       return (N > kQatMaxDim || K > kQatMaxDim) ? 0 : rb::zero_region_bytes(N) + rb::qat_backward_workspace_bytes(k, N, K);
+    case RB_OP_RESNORM_BACKWARD:
+      return (N > kResnormMaxD || M > kMaxDim) ? 0 : rb::zero_region_bytes(N) + rb::resnorm_backward_workspace_bytes(N, M);
     default: return 0;
   }
 }
@@ -423,6 +427,75 @@ rb_status rb_qat_autotune(const void* X, const void* dY, rb_dtype a_dtype, int64
   log_call("rb_qat_autotune", N, K, M, 0);
   return from_hip(rb::launch_qat_autotune(X, dY, a_dtype, M, ldx, lddy, What, ldwh, N, K, Y, y_dtype, ldy, dW, lddw,
                                           dX, dx_dtype, lddx, static_cast<hipStream_t>(stream)));
+}
+
+static bool norm_kind(int32_t k) { return k >= RB_NORM_NONE && k <= RB_NORM_LAYER; }
+static bool row_ld(int64_t ld, int64_t D) { return ld >= D && ld <= kMaxDim; }
+
+// shapes, types and vectors shared by the two directions
+static rb_status check_resnorm(rb_dtype a_dtype, rb_dtype s_dtype, int64_t M, int64_t D, const void* gate, int64_t ldg,
+                               float alpha, int32_t post, const float* w_post, const float* b_post, int32_t pre,
+                               const float* w_pre) {
+  if (!valid_dtype(a_dtype) || !valid_dtype(s_dtype) || !norm_kind(post) || !norm_kind(pre)) return RB_ERR_INVALID_ARG;
+  if (M < 1 || D < 1 || M > kMaxDim || D > kMaxDim || !std::isfinite(alpha)) return RB_ERR_INVALID_ARG;
+  if (gate && ldg != 0 && !row_ld(ldg, D)) return RB_ERR_INVALID_ARG;
+  if ((post != RB_NORM_NONE && !w_post) || (pre != RB_NORM_NONE && !w_pre)) return RB_ERR_INVALID_ARG;
+  if (s_dtype != a_dtype && s_dtype != RB_F32) return RB_ERR_UNSUPPORTED;
+  if (D > kResnormMaxD) return RB_ERR_UNSUPPORTED;
+  if (!elem_aligned(gate, ldg ? a_dtype : RB_F32) || !aligned(w_post, 4) || !aligned(b_post, 4) || !aligned(w_pre, 4))
+    return RB_ERR_MISALIGNED;
+  return RB_OK;
+}
+
+rb_status rb_resnorm_forward(const void* Y, rb_dtype a_dtype, int64_t M, int64_t D, int64_t ldy, const void* R,
+                             rb_dtype s_dtype, int64_t ldr, const void* gate, int64_t ldg, float alpha, int32_t post,
+                             const float* w_post, const float* b_post, int32_t pre, const float* w_pre,
+                             const float* b_pre, float eps, void* S, int64_t lds, void* X, int64_t ldx, float* stats,
+                             void* stream) {
+  if (!Y || (pre != RB_NORM_NONE && !X) || (!S && !X)) return RB_ERR_INVALID_ARG;
+  rb_status st = check_resnorm(a_dtype, s_dtype, M, D, gate, ldg, alpha, post, w_post, b_post, pre, w_pre);
+  if (st != RB_OK) return st;
+  if (!row_ld(ldy, D) || (R && !row_ld(ldr, D)) || (S && !row_ld(lds, D)) || (X && !row_ld(ldx, D)))
+    return RB_ERR_INVALID_ARG;
+  if (!std::isfinite(eps) || !(eps > 0.f)) return RB_ERR_INVALID_ARG;
+  if (!elem_aligned(Y, a_dtype) || !elem_aligned(R, s_dtype) || !elem_aligned(S, s_dtype) ||
+      !elem_aligned(X, a_dtype) || !aligned(b_pre, 4) || !aligned(stats, 4))
+    return RB_ERR_MISALIGNED;
+  log_call("rb_resnorm_forward", D, 0, M, 0);
+  return from_hip(rb::launch_resnorm_forward(Y, a_dtype, M, D, ldy, R, s_dtype, ldr, gate, ldg, alpha, post, w_post,
+                                             b_post, pre, w_pre, b_pre, eps, S, lds, X, ldx, stats,
+                                             static_cast<hipStream_t>(stream)));
+}
+
+rb_status rb_resnorm_backward(const void* dX, rb_dtype a_dtype, int64_t M, int64_t D, int64_t lddx, const void* dS,
+                              rb_dtype s_dtype, int64_t ldds, const void* Y, int64_t ldy, const void* S, int64_t lds,
+                              const float* stats, const void* gate, int64_t ldg, float alpha, int32_t post,
+                              const float* w_post, const float* b_post, int32_t pre, const float* w_pre, void* dY,
+                              int64_t lddy, void* dR, int64_t lddr, void* dgate, int64_t lddg, float* dw_post,
+                              float* db_post, float* dw_pre, float* db_pre, void* ws, size_t ws_bytes, void* stream) {
+  if (!stats || !dY || (pre != RB_NORM_NONE && (!dX || !S)) || (pre == RB_NORM_NONE && !dS)) return RB_ERR_INVALID_ARG;
+  if (!Y && (post != RB_NORM_NONE || gate)) return RB_ERR_INVALID_ARG;
+  if ((post == RB_NORM_NONE && (dw_post || db_post)) || (pre == RB_NORM_NONE && (dw_pre || db_pre)) || (!gate && dgate))
+    return RB_ERR_INVALID_ARG;
+  rb_status st = check_resnorm(a_dtype, s_dtype, M, D, gate, ldg, alpha, post, w_post, b_post, pre, w_pre);
+  if (st != RB_OK) return st;
+  if ((dX && !row_ld(lddx, D)) || (dS && !row_ld(ldds, D)) || (Y && !row_ld(ldy, D)) || (S && !row_ld(lds, D)) ||
+      !row_ld(lddy, D) || (dR && !row_ld(lddr, D)) || (dgate && ldg && !row_ld(lddg, D)))
+    return RB_ERR_INVALID_ARG;
+  if (!elem_aligned(dX, a_dtype) || !elem_aligned(dS, s_dtype) || !elem_aligned(Y, a_dtype) ||
+      !elem_aligned(S, s_dtype) || !aligned(stats, 4) || !elem_aligned(dY, a_dtype) || !elem_aligned(dR, s_dtype) ||
+      !elem_aligned(dgate, ldg ? a_dtype : RB_F32) || !aligned(dw_post, 4) || !aligned(db_post, 4) ||
+      !aligned(dw_pre, 4) || !aligned(db_pre, 4))
+    return RB_ERR_MISALIGNED;
+  const size_t need = rb::zero_region_bytes(D) + rb::resnorm_backward_workspace_bytes(D, M);
+  if (!ws || ws_bytes < need) return RB_ERR_WORKSPACE;
+  if (!aligned(ws, 16)) return RB_ERR_MISALIGNED;
+  log_call("rb_resnorm_backward", D, 0, M, 0);
+  return from_hip(rb::launch_resnorm_backward(dX, a_dtype, M, D, lddx, dS, s_dtype, ldds, Y, ldy, S, lds, stats, gate,
+                                              ldg, alpha, post, w_post, b_post, pre, w_pre, dY, lddy, dR, lddr, dgate,
+                                              lddg, dw_post, db_post, dw_pre, db_pre,
+                                              static_cast<char*>(ws) + rb::zero_region_bytes(D),
+                                              static_cast<hipStream_t>(stream)));
 }
 
 static bool adamw_counts_ok(const rb_adamw_tensor* t, int64_t count) {

@@ -1,0 +1,79 @@
+// rb_elem.hpp -- 8 consecutive elements of a row in registers, for rows of any alignment.
+#pragma once
+
+#include "rb_device.hpp"
+
+namespace rb {
+
+// The storage types of activations and streams. 8 elements are moved by 16-byte accesses whatever
+// the row's alignment (gfx950 global accesses need none beyond the element's) and stay packed, two
+// 16-bit elements a register, until they are widened.
+template <typename T> struct Vec8;
+
+template <> struct Vec8<float> {
+  struct __attribute__((packed, aligned(4))) Raw { uint32_t w[8]; };
+  __device__ static __forceinline__ float get(const Raw& r, int j) { return __uint_as_float(r.w[j]); }
+  __device__ static __forceinline__ void set2(Raw& r, int j, float a, float b) {
+    r.w[j] = __float_as_uint(a), r.w[j + 1] = __float_as_uint(b);
+  }
+  __device__ static __forceinline__ float narrow(float v) { return v; }
+};
+template <> struct Vec8<_Float16> {
+  struct __attribute__((packed, aligned(2))) Raw { uint32_t w[4]; };
+  __device__ static __forceinline__ float get(const Raw& r, int j) {
+    return (float)__builtin_bit_cast(_Float16, (uint16_t)(r.w[j >> 1] >> (16 * (j & 1))));
+  }
+  __device__ static __forceinline__ void set2(Raw& r, int j, float a, float b) {
+    typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+    r.w[j >> 1] = __builtin_bit_cast(uint32_t, (h2){(_Float16)a, (_Float16)b});
+  }
+  __device__ static __forceinline__ _Float16 narrow(float v) { return (_Float16)v; }
+};
+template <> struct Vec8<__bf16> {
+  struct __attribute__((packed, aligned(2))) Raw { uint32_t w[4]; };
+  __device__ static __forceinline__ float get(const Raw& r, int j) {
+    return __uint_as_float(j & 1 ? r.w[j >> 1] & 0xffff0000u : r.w[j >> 1] << 16);
+  }
+  __device__ static __forceinline__ void set2(Raw& r, int j, float a, float b) {
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    r.w[j >> 1] = __builtin_bit_cast(uint32_t, (b2){(__bf16)a, (__bf16)b});
+  }
+  __device__ static __forceinline__ __bf16 narrow(float v) { return (__bf16)v; }
+};
+
+// elements c .. c+7 of a row of n; those past n read as 0
+template <typename T>
+__device__ __forceinline__ typename Vec8<T>::Raw load8(const T* row, int c, int n) {
+  typename Vec8<T>::Raw r;
+  if (c + 8 <= n) {
+    r = *reinterpret_cast<const typename Vec8<T>::Raw*>(row + c);
+  } else {
+    const T zero = Vec8<T>::narrow(0.f);
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      const T a = c + j < n ? row[c + j] : zero, b = c + j + 1 < n ? row[c + j + 1] : zero;
+      Vec8<T>::set2(r, j, (float)a, (float)b);  // widened and narrowed again: the same value
+    }
+  }
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* row, int c, int n, const float (&v)[8]) {
+  if (c + 8 <= n) {
+    typename Vec8<T>::Raw r;
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) Vec8<T>::set2(r, j, v[j], v[j + 1]);
+    *reinterpret_cast<typename Vec8<T>::Raw*>(row + c) = r;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c + j < n) row[c + j] = Vec8<T>::narrow(v[j]);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void widen8(const typename Vec8<T>::Raw& r, float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = Vec8<T>::get(r, j);
+}
+
+}  // namespace rb

@@ -113,6 +113,21 @@ hipError_t launch_qat_autotune(const void* X, const void* dY, rb_dtype a_dtype, 
                                int64_t ldy, float* dW, int64_t lddw, void* dX, rb_dtype dx_dtype, int64_t lddx,
                                hipStream_t stream);
 
+// norms between blocks (rb_resnorm.hip)
+size_t resnorm_backward_workspace_bytes(int64_t D, int64_t M);
+hipError_t launch_resnorm_forward(const void* Y, rb_dtype a_dtype, int64_t M, int64_t D, int64_t ldy, const void* R,
+                                  rb_dtype s_dtype, int64_t ldr, const void* gate, int64_t ldg, float alpha, int post,
+                                  const float* w_post, const float* b_post, int pre, const float* w_pre,
+                                  const float* b_pre, float eps, void* S, int64_t lds, void* X, int64_t ldx,
+                                  float* stats, hipStream_t s);
+hipError_t launch_resnorm_backward(const void* dX, rb_dtype a_dtype, int64_t M, int64_t D, int64_t lddx, const void* dS,
+                                   rb_dtype s_dtype, int64_t ldds, const void* Y, int64_t ldy, const void* S,
+                                   int64_t lds, const float* stats, const void* gate, int64_t ldg, float alpha,
+                                   int post, const float* w_post, const float* b_post, int pre, const float* w_pre,
+                                   void* dY, int64_t lddy, void* dR, int64_t lddr, void* dgate, int64_t lddg,
+                                   float* dw_post, float* db_post, float* dw_pre, float* db_pre, void* ws,
+                                   hipStream_t s);
+
 // multi-tensor optimizer step (rb_adamw.hip)
 int64_t adamw_chunks(const rb_adamw_tensor* t, int64_t count);
 size_t adamw_plan_bytes(const rb_adamw_tensor* t, int64_t count);
