@@ -66,7 +66,9 @@ typedef enum rb_op {
   RB_OP_CODEBOOK_GEMV = 4,
   RB_OP_SVID_INIT = 5,
   RB_OP_QAT_BACKWARD = 6,
-  RB_OP_RESNORM_BACKWARD = 7 /* k = K = 1, N = D */
+  RB_OP_RESNORM_BACKWARD = 7,      /* k = K = 1, N = D */
+  RB_OP_QAT_LINEAR = 8,            /* k = 1 */
+  RB_OP_QAT_LINEAR_BACKWARD = 9    /* k = K = 1 */
 } rb_op;
 
 /* Version of this ABI (major*10000 + minor*100 + patch). */
@@ -80,7 +82,7 @@ const char* rb_status_string(rb_status s);
  * 64-bit accumulator per output row), which rb_gemv and rb_gemv_variant need all-zero on
  * entry and return to all-zero before their last kernel ends; the bytes after it are
  * scratch. rb_gemm_small, rb_svid_init and rb_qat_backward use only bytes after the zero
- * region and never write it; so does rb_resnorm_backward. So: zero-fill a workspace once after allocation, and one
+ * region and never write it; so do the calls listed after them in rb_op. So: zero-fill a workspace once after allocation, and one
  * buffer of the largest size its calls need can serve all of them (calls on one stream;
  * calls that overlap in time need separate workspaces). */
 size_t rb_workspace_bytes(rb_op op, int32_t k, int64_t N, int64_t K, int64_t M);
@@ -422,6 +424,37 @@ rb_status rb_qat_autotune(const void* X, const void* dY, rb_dtype a_dtype, int64
                           const void* What, int64_t ldwh, int64_t N, int64_t K, void* Y, rb_dtype y_dtype,
                           int64_t ldy, float* dW, int64_t lddw, void* dX, rb_dtype dx_dtype, int64_t lddx,
                           void* stream);
+
+/* rb_qat_linear -- the forward's product with a bias, an activation and a residual in its epilogue.
+ *     Z = X What^T + bias;  Y = act(Z) + R
+ *   computed on the library's matrix-core kernels with fp32 sums; Y is computed from the fp32 Z.
+ *   X [M][ldx], What [N][ldwh] in a_dtype (RB_F16 or RB_BF16), any alignment of rows (16-byte aligned
+ *   operands with leading dimensions and K multiples of 8 are the fast case)
+ *   1 <= M, N, K; N, K <= 2^28, M below 2^31; leading dimensions as rb_qat_matmul
+ *   bias     fp32 [N] or NULL;  act  rb_act: RELU max(z, 0), GELU z Phi(z), GELU_TANH its tanh form
+ *            z / 2 (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))), SILU z / (1 + exp(-z))
+ *   R        [M][ldr] in y_dtype or NULL; may be Y (same leading dimension)
+ *   Z        [M][ldz] in a_dtype or NULL: Z rounded, for rb_qat_linear_backward
+ *   Y        [M][ldy] in y_dtype, RB_F32 or a_dtype
+ *   ws       rb_workspace_bytes(RB_OP_QAT_LINEAR, 1, N, K, M) bytes (may be 0: NULL), 16-byte aligned: the
+ *            partial sums of a product with few output tiles, whose columns are split over the GPU
+ *            and joined in a fixed order (deterministic); no zero-filling needed.
+ *
+ * rb_qat_linear_backward -- from dY = the gradient of Y: dZ = dY (.) act'(Z) (relu's slope at 0 is
+ *   0) and db = the column sums of the unrounded dZ in fp32, in a fixed order. dZ is what
+ *   rb_qat_backward takes as its dY; R's gradient is dY itself.
+ *   dY       [M][lddy] in dy_dtype, RB_F32 or a_dtype;  Z  [M][ldz] in a_dtype (may be NULL for RB_ACT_NONE)
+ *   dZ       [M][lddz] in a_dtype, or NULL with a db; may be dY or Z (same type and leading dimension)
+ *   db       fp32 [N] or NULL
+ *   ws       rb_workspace_bytes(RB_OP_QAT_LINEAR_BACKWARD, 1, N, 1, M) bytes, 16-byte aligned (NULL if
+ *            db is NULL); no zero-filling needed. */
+typedef enum rb_act { RB_ACT_NONE = 0, RB_ACT_RELU = 1, RB_ACT_GELU = 2, RB_ACT_GELU_TANH = 3, RB_ACT_SILU = 4 } rb_act;
+rb_status rb_qat_linear(const void* X, rb_dtype a_dtype, int64_t M, int64_t ldx, const void* What, int64_t ldwh,
+                        int64_t N, int64_t K, const float* bias, int32_t act, const void* R, int64_t ldr, void* Z,
+                        int64_t ldz, void* Y, rb_dtype y_dtype, int64_t ldy, void* ws, size_t ws_bytes, void* stream);
+rb_status rb_qat_linear_backward(const void* dY, rb_dtype dy_dtype, int64_t M, int64_t N, int64_t lddy, const void* Z,
+                                 rb_dtype a_dtype, int64_t ldz, int32_t act, void* dZ, int64_t lddz, float* db, void* ws,
+                                 size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------------------
  * rb_resnorm_* -- the norms between two blocks, in one pass: the norm after a block, its gate, the

@@ -16,6 +16,8 @@ return CUDA (HIP) tensors on the current device and enqueue on the current strea
   Y, planes, What = qat_forward(W, g, h, X)      ... and the layer's product Y = X What^T
   dW, dX, dg, dh = qat_backward(dY, X, What, planes, g, h)   straight-through backward
   qat_autotune(X, dY, What, Y, dW, dX)           pick the fastest GEMM kernels for a shape
+  Y, Z = qat_linear(X, What, bias, act, residual)   Y = act(X What^T + bias) + residual
+  dZ, db = qat_linear_backward(dY, Z, act)       ... and its epilogue's gradients
   S, X, stats = resnorm_forward(Y, R, w_pre)     S = alpha R + gate norm_post(Y), X = norm_pre(S)
   grads = resnorm_backward(dX, dS, Y, S, stats, w_pre)   ... and its gradients
   adamw_step(plan, step, lr)                     AdamW over many tensors (adamw_plan), states in 32 or 8 bits
@@ -28,12 +30,12 @@ import torch
 
 from . import _lib
 from ._lib import (RB_F16, RB_F32, RB_BF16, RB_OP_CODEBOOK_GEMV, RB_OP_GEMM_SMALL, RB_OP_GEMV,
-                   RB_OP_QAT_BACKWARD, RB_OP_RESNORM_BACKWARD, RB_OP_SVID_INIT, RB_QAT_ENGINE_AUTO, RB_QAT_ENGINE_MFMA,
+                   RB_OP_QAT_BACKWARD, RB_OP_QAT_LINEAR, RB_OP_QAT_LINEAR_BACKWARD, RB_OP_RESNORM_BACKWARD, RB_OP_SVID_INIT, RB_QAT_ENGINE_AUTO, RB_QAT_ENGINE_MFMA,
                    RB_QAT_ENGINE_ROCBLAS, RbError, check, lib)
 
 __all__ = ["pack", "gemv", "gemv_variant", "gemm_small", "codebook_encode", "codebook_gemv", "codebook_mstep",
            "codebook_distinct", "codebook_learn", "svid_init", "qat_derive",
-           "qat_forward", "qat_matmul", "qat_backward", "qat_autotune", "resnorm_forward",
+           "qat_forward", "qat_matmul", "qat_backward", "qat_autotune", "qat_linear", "qat_linear_backward", "resnorm_forward",
            "resnorm_backward", "adamw_plan", "adamw_step", "AdamWPlan", "workspace",
            "workspace_bytes", "storage_bits_per_weight", "version", "RbError", "lib"]
 
@@ -343,7 +345,8 @@ def qat_autotune(X: torch.Tensor, dY: torch.Tensor, What: torch.Tensor, Y: torch
 
 
 
-_NORM = {"none": _lib.RB_NORM_NONE, "rms": _lib.RB_NORM_RMS, "layer": _lib.RB_NORM_LAYER}
+_ACT = {"none": _lib.RB_ACT_NONE, "relu": _lib.RB_ACT_RELU, "gelu": _lib.RB_ACT_GELU,
+        "gelu_tanh": _lib.RB_ACT_GELU_TANH, "silu": _lib.RB_ACT_SILU}
 
 
 def _vec(name: str, t: torch.Tensor | None, n: int):
@@ -362,6 +365,63 @@ def _rows(name: str, t: torch.Tensor | None, shape, dtype):
     if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{name} is a {dtype} matrix of shape {tuple(shape)}")
     return _ptr_rows(t), t.stride(0) if shape[0] > 1 else max(t.stride(0), shape[1])
+
+
+def qat_linear(X: torch.Tensor, What: torch.Tensor, bias: torch.Tensor | None = None, act: str = "none",
+               residual: torch.Tensor | None = None, y_dtype=None, save_z: bool = False,
+               Y: torch.Tensor | None = None, Z: torch.Tensor | None = None, ws: torch.Tensor | None = None):
+    """The layer's product with its epilogue: Z = X What^T + bias, Y = act(Z) + residual, for X [M][K]
+    and What [N][K] (fp16 or bf16, rows may be strided), an fp32 `bias` [N], `act` one of "none",
+    "relu", "gelu", "gelu_tanh", "silu" and a `residual` [M][N] in Y's type (fp32 or X's, the default;
+    it may be Y itself). Returns (Y, Z); Z, in X's type, is kept for the backward if `save_z` or
+    given, else None."""
+    M, K = X.shape
+    N = What.shape[0]
+    dt = X.dtype
+    if Y is None:
+        Y = torch.empty((M, N), dtype=y_dtype or (dt if residual is None else residual.dtype), device=X.device)
+    if Z is None and save_z:
+        Z = torch.empty((M, N), dtype=dt, device=X.device)
+    n = workspace_bytes(RB_OP_QAT_LINEAR, 1, N, K, M)
+    if ws is None and n:
+        ws = torch.empty(n, dtype=torch.uint8, device=X.device)
+    xp, ldx = _rows("X", X, (M, K), dt)
+    wp, ldw = _rows("What", What, (N, K), dt)
+    yp, ldy = _rows("Y", Y, (M, N), Y.dtype)
+    rp, ldr = _rows("residual", residual, (M, N), Y.dtype)
+    zp, ldz = _rows("Z", Z, (M, N), dt)
+    check("rb_qat_linear", lib.rb_qat_linear(xp, _dt(dt), M, ldx, wp, ldw, N, K, _vec("bias", bias, N), _ACT[act], rp, ldr,
+                                             zp, ldz, yp, _dt(Y.dtype), ldy, _ptr(ws), 0 if ws is None else ws.numel(),
+                                             _stream()))
+    return Y, Z
+
+
+def qat_linear_backward(dY: torch.Tensor, Z: torch.Tensor | None, act: str = "none", bias: bool = True, a_dtype=None,
+                        dZ: torch.Tensor | None = None, db: torch.Tensor | None = None,
+                        ws: torch.Tensor | None = None):
+    """The epilogue's gradients from dY [M][N] (fp32 or the activation type) and the forward's Z (not
+    needed for act "none"): (dZ, db), dZ = dY act'(Z) in the activation type (Z's, or `a_dtype`; what
+    qat_backward takes as its dY) and, with `bias`, db = its column sums, fp32 [N]."""
+    M, N = dY.shape
+    dt = a_dtype or (Z.dtype if Z is not None else dZ.dtype if dZ is not None else dY.dtype)
+    if dZ is None:
+        dZ = torch.empty((M, N), dtype=dt, device=dY.device)
+    if not bias:
+        db = None
+    elif db is None:
+        db = torch.empty(N, dtype=torch.float32, device=dY.device)
+    if ws is None and bias:
+        ws = torch.empty(workspace_bytes(RB_OP_QAT_LINEAR_BACKWARD, 1, N, 1, M), dtype=torch.uint8, device=dY.device)
+    dyp, lddy = _rows("dY", dY, (M, N), dY.dtype)
+    zp, ldz = _rows("Z", Z, (M, N), dt)
+    dzp, lddz = _rows("dZ", dZ, (M, N), dt)
+    check("rb_qat_linear_backward", lib.rb_qat_linear_backward(dyp, _dt(dY.dtype), M, N, lddy, zp, _dt(dt), ldz, _ACT[act],
+                                                               dzp, lddz, _vec("db", db, N), _ptr(ws),
+                                                               0 if ws is None else ws.numel(), _stream()))
+    return dZ, db
+
+
+_NORM = {"none": _lib.RB_NORM_NONE, "rms": _lib.RB_NORM_RMS, "layer": _lib.RB_NORM_LAYER}
 
 
 def _gate_rows(gate, shape, dtype):

@@ -13,7 +13,8 @@ RB_OK, RB_ERR_INVALID_ARG, RB_ERR_UNSUPPORTED, RB_ERR_MISALIGNED, RB_ERR_WORKSPA
 RB_F32, RB_F16, RB_BF16 = 0, 1, 2
 RB_QAT_ENGINE_AUTO, RB_QAT_ENGINE_MFMA, RB_QAT_ENGINE_ROCBLAS = 0, 1, 2
 (RB_OP_PACK, RB_OP_GEMV, RB_OP_GEMM_SMALL, RB_OP_CODEBOOK_ENCODE, RB_OP_CODEBOOK_GEMV, RB_OP_SVID_INIT,
- RB_OP_QAT_BACKWARD, RB_OP_RESNORM_BACKWARD) = range(8)
+ RB_OP_QAT_BACKWARD, RB_OP_RESNORM_BACKWARD, RB_OP_QAT_LINEAR, RB_OP_QAT_LINEAR_BACKWARD) = range(10)
+RB_ACT_NONE, RB_ACT_RELU, RB_ACT_GELU, RB_ACT_GELU_TANH, RB_ACT_SILU = range(5)
 RB_NORM_NONE, RB_NORM_RMS, RB_NORM_LAYER = 0, 1, 2
 
 _vp = ctypes.c_void_p
@@ -65,6 +66,10 @@ SIGNATURES = {
                                        _vp, _sz, _vp]),
     "rb_qat_autotune": (ctypes.c_int, [_vp, _vp, ctypes.c_int, _i64, _i64, _i64, _vp, _i64, _i64, _i64, _vp,
                                        ctypes.c_int, _i64, _vp, _i64, _vp, ctypes.c_int, _i64, _vp]),
+    "rb_qat_linear": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _vp, _i64, _i64, _i64, _vp, _i32, _vp, _i64, _vp,
+                                     _i64, _vp, ctypes.c_int, _i64, _vp, _sz, _vp]),
+    "rb_qat_linear_backward": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, ctypes.c_int, _i64, _i32, _vp,
+                                              _i64, _vp, _vp, _sz, _vp]),
     "rb_resnorm_forward": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, ctypes.c_int, _i64, _vp, _i64,
                                           ctypes.c_float, _i32, _vp, _vp, _i32, _vp, _vp, ctypes.c_float, _vp, _i64,
                                           _vp, _i64, _vp, _vp]),

@@ -105,6 +105,13 @@ size_t rb_workspace_bytes(rb_op op, int32_t k, int64_t N, int64_t K, int64_t M) 
       return (N > kQatMaxDim || K > kQatMaxDim) ? 0 : rb::zero_region_bytes(N) + rb::qat_backward_workspace_bytes(k, N, K);
     case RB_OP_RESNORM_BACKWARD:
       return (N > kResnormMaxD || M > kMaxDim) ? 0 : rb::zero_region_bytes(N) + rb::resnorm_backward_workspace_bytes(N, M);
+    case RB_OP_QAT_LINEAR: {
+      if (N > kQatMaxDim || K > kQatMaxDim || M > kMaxDim) return 0;
+      const size_t p = rb::linear_workspace_bytes(N, K, M);
+      return p > 0 ? rb::zero_region_bytes(N) + p : 0;
+    }
+    case RB_OP_QAT_LINEAR_BACKWARD:
+      return (N > kQatMaxDim || M > kMaxDim) ? 0 : rb::zero_region_bytes(N) + rb::linear_backward_workspace_bytes(N, M);
     default: return 0;
   }
 }
@@ -427,6 +434,49 @@ rb_status rb_qat_autotune(const void* X, const void* dY, rb_dtype a_dtype, int64
   log_call("rb_qat_autotune", N, K, M, 0);
   return from_hip(rb::launch_qat_autotune(X, dY, a_dtype, M, ldx, lddy, What, ldwh, N, K, Y, y_dtype, ldy, dW, lddw,
                                           dX, dx_dtype, lddx, static_cast<hipStream_t>(stream)));
+}
+
+static bool act_kind(int32_t a) { return a >= RB_ACT_NONE && a <= RB_ACT_SILU; }
+
+rb_status rb_qat_linear(const void* X, rb_dtype a_dtype, int64_t M, int64_t ldx, const void* What, int64_t ldwh,
+                        int64_t N, int64_t K, const float* bias, int32_t act, const void* R, int64_t ldr, void* Z,
+                        int64_t ldz, void* Y, rb_dtype y_dtype, int64_t ldy, void* ws, size_t ws_bytes, void* stream) {
+  if (!X || !What || !Y) return RB_ERR_INVALID_ARG;
+  if (N < 1 || K < 1 || M < 1 || N > kQatMaxDim || K > kQatMaxDim || M > kMaxDim) return RB_ERR_INVALID_ARG;
+  if (ldx < K || ldx > kMaxDim || ldwh < K || ldwh > kMaxDim || ldy < N || ldy > kMaxDim) return RB_ERR_INVALID_ARG;
+  if ((R && (ldr < N || ldr > kMaxDim)) || (Z && (ldz < N || ldz > kMaxDim)) || !act_kind(act))
+    return RB_ERR_INVALID_ARG;
+  if (!valid_dtype(a_dtype) || !valid_dtype(y_dtype)) return RB_ERR_INVALID_ARG;
+  if (!act_dtype(a_dtype) || (y_dtype != RB_F32 && y_dtype != a_dtype)) return RB_ERR_UNSUPPORTED;
+  if (!elem_aligned(X, a_dtype) || !elem_aligned(What, a_dtype) || !elem_aligned(Y, y_dtype) ||
+      !elem_aligned(R, y_dtype) || !elem_aligned(Z, a_dtype) || !aligned(bias, 4))
+    return RB_ERR_MISALIGNED;
+  const size_t part = rb::linear_workspace_bytes(N, K, M);
+  if (part > 0 && (!ws || ws_bytes < rb::zero_region_bytes(N) + part)) return RB_ERR_WORKSPACE;
+  if (!aligned(ws, 16)) return RB_ERR_MISALIGNED;
+  log_call("rb_qat_linear", N, K, M, act);
+  return from_hip(rb::launch_linear(X, a_dtype, M, ldx, What, ldwh, N, K, bias, act, R, ldr, Z, ldz, Y, y_dtype, ldy,
+                                    part > 0 ? static_cast<char*>(ws) + rb::zero_region_bytes(N) : nullptr,
+                                    static_cast<hipStream_t>(stream)));
+}
+
+rb_status rb_qat_linear_backward(const void* dY, rb_dtype dy_dtype, int64_t M, int64_t N, int64_t lddy, const void* Z,
+                                 rb_dtype a_dtype, int64_t ldz, int32_t act, void* dZ, int64_t lddz, float* db, void* ws,
+                                 size_t ws_bytes, void* stream) {
+  if (!dY || (!dZ && !db) || !act_kind(act) || (!Z && act != RB_ACT_NONE)) return RB_ERR_INVALID_ARG;
+  if (N < 1 || M < 1 || N > kQatMaxDim || M > kMaxDim || lddy < N || lddy > kMaxDim) return RB_ERR_INVALID_ARG;
+  if ((Z && (ldz < N || ldz > kMaxDim)) || (dZ && (lddz < N || lddz > kMaxDim))) return RB_ERR_INVALID_ARG;
+  if (!valid_dtype(a_dtype) || !valid_dtype(dy_dtype)) return RB_ERR_INVALID_ARG;
+  if (!act_dtype(a_dtype) || (dy_dtype != RB_F32 && dy_dtype != a_dtype)) return RB_ERR_UNSUPPORTED;
+  if (!elem_aligned(dY, dy_dtype) || !elem_aligned(Z, a_dtype) || !elem_aligned(dZ, a_dtype) || !aligned(db, 4))
+    return RB_ERR_MISALIGNED;
+  const size_t need = rb::zero_region_bytes(N) + rb::linear_backward_workspace_bytes(N, M);
+  if (db && (!ws || ws_bytes < need)) return RB_ERR_WORKSPACE;
+  if (!aligned(ws, 16)) return RB_ERR_MISALIGNED;
+  log_call("rb_qat_linear_backward", N, 0, M, act);
+  return from_hip(rb::launch_linear_backward(dY, dy_dtype, M, N, lddy, Z, a_dtype, ldz, act, dZ, lddz, db,
+                                             db ? static_cast<char*>(ws) + rb::zero_region_bytes(N) : nullptr,
+                                             static_cast<hipStream_t>(stream)));
 }
 
 static bool norm_kind(int32_t k) { return k >= RB_NORM_NONE && k <= RB_NORM_LAYER; }

@@ -113,6 +113,16 @@ hipError_t launch_qat_autotune(const void* X, const void* dY, rb_dtype a_dtype, 
                                int64_t ldy, float* dW, int64_t lddw, void* dX, rb_dtype dx_dtype, int64_t lddx,
                                hipStream_t stream);
 
+// the layer's product with its epilogue, and the epilogue's backward (rb_linear.hip)
+size_t linear_workspace_bytes(int64_t N, int64_t K, int64_t M);
+hipError_t launch_linear(const void* X, rb_dtype a_dtype, int64_t M, int64_t ldx, const void* W, int64_t ldw, int64_t N,
+                         int64_t K, const float* bias, int act, const void* R, int64_t ldr, void* Z, int64_t ldz,
+                         void* Y, rb_dtype y_dtype, int64_t ldy, void* ws, hipStream_t s);
+size_t linear_backward_workspace_bytes(int64_t N, int64_t M);
+hipError_t launch_linear_backward(const void* dY, rb_dtype dy_dtype, int64_t M, int64_t N, int64_t lddy, const void* Z,
+                                  rb_dtype a_dtype, int64_t ldz, int act, void* dZ, int64_t lddz, float* db, void* ws,
+                                  hipStream_t s);
+
 // norms between blocks (rb_resnorm.hip)
 size_t resnorm_backward_workspace_bytes(int64_t D, int64_t M);
 hipError_t launch_resnorm_forward(const void* Y, rb_dtype a_dtype, int64_t M, int64_t D, int64_t ldy, const void* R,

@@ -1,0 +1,251 @@
+"""GPU parity of the layer's product with its epilogue (rb_qat_linear) and of the epilogue's backward
+(rb_qat_linear_backward) against the oracle.
+
+Comparison rules, u = 2^-24:
+* Z: the products of fp16/bf16 numbers are exact in fp32; they are added 32 to a matrix instruction and
+  K / 32 instructions deep, the halves of a step's columns and the K chunks joined after: at most
+  (K / 32 + 48) u of S = sum |x w| + |b|, for the K here below 2e-5 S;
+* Y: every activation's slope is below 1.13, its own evaluation (exp and erf of the device, a reciprocal)
+  within 16 u of |z| + |act(z)|, plus the residual's and the sum's rounding;
+* dZ: the slope's evaluation within 24 u (1 + |z|) of |dY|; db: those errors and M u of sum |dZ|;
+* rounded outputs add half a unit of their type.
+"""
+import numpy as np
+import pytest
+import torch
+
+import residual_binarized_weight_amd as rb
+from oracle import block_oracle as BO
+from tests.gpu_util import dev
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs the GPU")]
+
+U = 2.0 ** -24
+DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+UNIT = {torch.float32: U, torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}
+TINY = {torch.float32: 2.0 ** -149, torch.float16: 2.0 ** -25, torch.bfloat16: 2.0 ** -134}
+ACTS = ["none", "relu", "gelu", "gelu_tanh", "silu"]
+
+
+def n64(t):
+    return None if t is None else t.detach().float().cpu().numpy().astype(np.float64)
+
+
+def mat(r, M, N, dt, std=1.0, pad=0, off=0):
+    """M rows of N, pad elements between them and off before; what lies between is NaN: a kernel that
+    reads it shows."""
+    buf = torch.full((M * (N + pad) + off,), float("nan"), dtype=DT[dt], device=dev())
+    v = buf[off:].view(M, N + pad)[:, :N]
+    v.copy_(torch.from_numpy((r.standard_normal((M, N)) * std).astype(np.float32)).to(DT[dt]).to(dev()))
+    return v
+
+
+def near(got, ref, lim, what):
+    lim = lim + UNIT[got.dtype] * np.abs(ref) + TINY[got.dtype]
+    err = np.abs(n64(got) - ref)
+    assert np.all(err <= lim), f"{what}: {np.nanmax(err / lim):.3g} x the bound, {np.isnan(err).sum()} NaN"
+
+
+def case(seed, M, N, K, dt, act="none", bias=False, res=False, ydt=None, save_z=False, pad=0, off=0):
+    r = np.random.default_rng([920, seed])
+    ydt = ydt or dt
+    X, W = mat(r, M, K, dt, 1.0, pad, off), mat(r, N, K, dt, 0.03, pad, off)
+    b = torch.from_numpy(r.standard_normal(N).astype(np.float32)).to(dev()) if bias else None
+    R = mat(r, M, N, ydt, 1.0, pad, off) if res else None
+    Y, Z = rb.qat_linear(X, W, bias=b, act=act, residual=R, y_dtype=DT[ydt], save_z=save_z)
+    torch.cuda.synchronize()
+    check(X, W, b, act, R, Y, Z)
+    assert (Z is not None) == save_z and Y.dtype == DT[ydt]
+    return X, W, b, R, Y, Z
+
+
+def check(X, W, b, act, R, Y, Z):
+    x, w = n64(X), n64(W)
+    yo, zo = BO.linear(x, w, n64(b), act, n64(R))
+    S = np.abs(x) @ np.abs(w).T + (0 if b is None else np.abs(n64(b)))
+    if Z is not None:
+        near(Z, zo, 2e-5 * S, "Z")
+    lim = 1.13 * 2e-5 * S + 16 * U * (np.abs(zo) + np.abs(BO.activation(zo, act)[0]))
+    near(Y, yo, lim + 2 * U * (np.abs(yo) + (0 if R is None else np.abs(n64(R)))), "Y")
+
+
+# sizes around every tile edge: 16, 32, 64 and 128 batch rows, 64 and 256 weight rows, 32, 64 and 128 columns
+@pytest.mark.parametrize("M", [1, 2, 15, 16, 17, 32, 33, 64, 65, 127, 128, 129, 200])
+@pytest.mark.parametrize("N,K", [(1, 8), (63, 64), (256, 72), (257, 128), (300, 136), (65, 1000)])
+def test_tile_edges(M, N, K):
+    case(1, M, N, K, "bf16", bias=True, ydt="f32")
+
+
+@pytest.mark.parametrize("M", [1, 3, 16, 31, 64, 100, 130])
+@pytest.mark.parametrize("N,K", [(1, 1), (5, 3), (64, 63), (255, 65), (258, 129), (100, 997)])
+def test_tile_edges_unaligned(M, N, K):
+    case(2, M, N, K, "f16", bias=True, ydt="f32")
+
+
+@pytest.mark.parametrize("pad,off", [(8, 0), (8, 8), (3, 0), (0, 1), (1, 5)])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_strides_and_offsets(pad, off, dt):
+    """Rows further apart than their length, with NaN between them, at aligned and odd addresses."""
+    for M, K in ((1, 200), (40, 264), (150, 328)):
+        case(3, M, 70, K, dt, act="silu", bias=True, res=True, save_z=True, pad=pad, off=off)
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("dt,ydt", [("bf16", "bf16"), ("bf16", "f32"), ("f16", "f16"), ("f16", "f32")])
+@pytest.mark.parametrize("bias,res,save_z", [(False, False, False), (True, True, True), (False, True, False), (True, False, True)])
+def test_epilogues(act, dt, ydt, bias, res, save_z):
+    case(4, 37, 130, 160, dt, act, bias, res, ydt, save_z)
+    case(5, 37, 2050, 2048, dt, act, bias, res, ydt, save_z)      # split columns: the join's epilogue
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 4096, 4096), (5, 1000, 9000), (17, 520, 8192), (300, 700, 4100), (1100, 4100, 520),
+                                   (2048, 4096, 1024), (700, 11008, 640)])
+def test_long_and_wide(M, N, K):
+    case(6, M, N, K, "bf16", "gelu_tanh", True, True, "f32")
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 2000, 4099), (40, 1500, 3001), (513, 1030, 1027)])
+def test_long_and_wide_unaligned(M, N, K):
+    case(7, M, N, K, "f16", "gelu", True, True, "f16", True)
+
+
+def test_training_shape_sampled():
+    """2048 tokens through the 4096 x 11008 layer: sampled rows, first and last included. K = 11008 adds
+    (344 + 48) u, still below 2.4e-5: the bound here is 2.4e-5 of S."""
+    r = np.random.default_rng(8)
+    M, N, K = 2048, 4096, 11008
+    X, W = mat(r, M, K, "bf16"), mat(r, N, K, "bf16", 0.03)
+    Y, _ = rb.qat_linear(X, W, y_dtype=torch.float32)
+    torch.cuda.synchronize()
+    rows = [0, 1, 127, 128, 1000, 1531, 2046, 2047]
+    x, w = n64(X[rows]), n64(W)
+    near(Y[rows], x @ w.T, 2.4e-5 * (np.abs(x) @ np.abs(w).T), "Y")
+
+
+def test_writes_stay_inside_and_residual_in_place():
+    r = np.random.default_rng(9)
+    M, N, K = 67, 131, 96
+    X, W = mat(r, M, K, "bf16"), mat(r, N, K, "bf16", 0.1)
+    Yb, Zb = (torch.full((M + 2, N + 9), 7.0, dtype=torch.bfloat16, device=dev()) for _ in range(2))
+    Y, Z = Yb[1:M + 1, 3:N + 3], Zb[1:M + 1, 5:N + 5]
+    R = Y.clone()
+    rb.qat_linear(X, W, residual=Y, Y=Y, Z=Z)
+    torch.cuda.synchronize()
+    check(X, W, None, "none", R, Y, Z)
+    for b, o in ((Yb, 3), (Zb, 5)):
+        assert torch.all(b[0] == 7) and torch.all(b[M + 1:] == 7) and torch.all(b[:, :o] == 7) and torch.all(b[:, o + N:] == 7)
+
+
+def test_non_finite_values_stay_in_their_row_and_column():
+    r = np.random.default_rng(10)
+    X, W = mat(r, 50, 200, "f16"), mat(r, 300, 200, "f16")
+    X[7, 3], W[11, 199] = float("nan"), float("inf")
+    Y, _ = rb.qat_linear(X, W, y_dtype=torch.float32)
+    torch.cuda.synchronize()
+    bad = ~torch.isfinite(Y)
+    want = torch.zeros_like(bad)
+    want[7], want[:, 11] = True, True
+    assert torch.equal(bad, want)
+
+
+@pytest.mark.parametrize("M,N,K", [(300, 520, 1600), (3, 4096, 4096), (33, 100, 3001)])
+def test_deterministic_and_in_a_graph(M, N, K):
+    r = np.random.default_rng(11)
+    X, W = mat(r, M, K, "bf16"), mat(r, N, K, "bf16", 0.1)
+    want, _ = rb.qat_linear(X, W, y_dtype=torch.float32)
+    n = rb.workspace_bytes(rb.RB_OP_QAT_LINEAR, 1, N, K, M)
+    ws = torch.empty(max(n, 16), dtype=torch.uint8, device=dev())
+    Y = torch.empty_like(want)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        rb.qat_linear(X, W, Y=Y, ws=ws)
+    for _ in range(3):
+        ws.fill_(255)
+        Y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(Y, want)
+
+
+def test_on_another_stream():
+    r = np.random.default_rng(12)
+    X, W = mat(r, 100, 512, "bf16"), mat(r, 600, 512, "bf16", 0.1)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        Y, Z = rb.qat_linear(X, W, act="silu", save_z=True)
+        dZ, db = rb.qat_linear_backward(Y, Z, act="silu")
+    s.synchronize()
+    check(X, W, None, "silu", None, Y, Z)
+
+
+# ---------------------------------------------------------------------------------------------
+# the epilogue's backward
+# ---------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("dt,ydt", [("bf16", "bf16"), ("bf16", "f32"), ("f16", "f16"), ("f16", "f32")])
+@pytest.mark.parametrize("M,N", [(1, 1), (1, 700), (3, 512), (4, 513), (130, 7), (1000, 1030)])
+def test_backward(act, dt, ydt, M, N):
+    r = np.random.default_rng([921, M, N])
+    dY, Z = mat(r, M, N, ydt, 0.1, 3, 1), mat(r, M, N, dt, 2.0, 2, 3)
+    dZ, db = rb.qat_linear_backward(dY, Z, act=act)
+    torch.cuda.synchronize()
+    z, d = n64(Z), n64(dY)
+    zo, bo = BO.linear_backward(d, z, act)
+    lim = 24 * U * (1 + np.abs(z)) * np.abs(d)
+    near(dZ, zo, lim, "dZ")
+    near(db, bo, lim.sum(axis=0) + M * U * np.abs(zo).sum(axis=0), "db")
+
+
+def test_backward_without_bias_or_z_and_in_place():
+    r = np.random.default_rng(13)
+    dY, Z = mat(r, 60, 200, "bf16"), mat(r, 60, 200, "bf16")
+    want, db = rb.qat_linear_backward(dY, Z, act="silu")
+    same, none = rb.qat_linear_backward(dY, Z, act="silu", bias=False)
+    assert none is None and torch.equal(same, want)
+    d = dY.clone()
+    rb.qat_linear_backward(d, Z, act="silu", dZ=d, db=db)
+    assert torch.equal(d, want)
+    f = dY.float()
+    dZ, db = rb.qat_linear_backward(f, None, a_dtype=torch.bfloat16)
+    torch.cuda.synchronize()
+    assert torch.equal(dZ, f.to(torch.bfloat16))
+    near(db, n64(f).sum(axis=0), 60 * U * np.abs(n64(f)).sum(axis=0), "db")
+
+
+@pytest.mark.parametrize("act", ACTS[2:])
+def test_slope_is_the_difference_quotient(act):
+    """The slope against central differences of the oracle's activation: truncation h^2 / 6 of a third
+    derivative below 4."""
+    z = torch.linspace(-9, 9, 4001, device=dev()).to(torch.float16).reshape(1, -1)
+    one = torch.ones_like(z, dtype=torch.float32)
+    dZ, db = rb.qat_linear_backward(one, z, act=act)
+    torch.cuda.synchronize()
+    zz, h = n64(z), 1e-4
+    diff = (BO.activation(zz + h, act)[0] - BO.activation(zz - h, act)[0]) / (2 * h)
+    assert np.max(np.abs(n64(db) - diff[0])) <= h * h + 24 * U * 10 + 1e-10 / h
+
+
+def test_refusals():
+    r = np.random.default_rng(14)
+    X, W = mat(r, 4, 64, "bf16"), mat(r, 8, 64, "bf16")
+    with pytest.raises(ValueError):
+        rb.qat_linear(X, W[:, :32])
+    with pytest.raises(ValueError):
+        rb.qat_linear(X, W, bias=torch.zeros(9, device=dev()))
+    with pytest.raises(ValueError):
+        rb.qat_linear(X, W, residual=torch.zeros((4, 8), device=dev()), Y=torch.zeros((4, 8), dtype=torch.bfloat16, device=dev()))
+    with pytest.raises(KeyError):
+        rb.qat_linear(X, W, act="tanh")
+    with pytest.raises(ValueError):
+        rb.qat_linear(X.cpu(), W.cpu())
+    with pytest.raises(rb.RbError):
+        rb.qat_linear(X.float(), W.float())
+    with pytest.raises(rb.RbError):
+        rb.qat_linear(X, W, y_dtype=torch.float16)
+    with pytest.raises(rb.RbError):
+        rb.qat_linear(mat(r, 1, 8192, "bf16"), mat(r, 64, 8192, "bf16"), ws=torch.empty(16, dtype=torch.uint8, device=dev()))
+    with pytest.raises(rb.RbError):
+        rb.qat_linear_backward(X, None, act="relu", a_dtype=torch.bfloat16)
