@@ -4,8 +4,9 @@
 //   dZ = dY act'(Z),   db = column sums of dZ
 //
 // Kernels of this file:
-//   linear_tile_kernel    a tile of 16 MT batch rows by 256 weight rows per block, on the matrix cores
+//   linear_tile_kernel    a tile of batch rows by weight rows per block, on the matrix cores
 //   linear_join_kernel    the sums of K chunks, where a tile's columns are split, and the epilogue
+//   linear_rows_kernel    up to 4 batch rows, on the vector units: a wave streams whole weight rows
 //   linear_grad_kernel    dZ and, per strip of rows, partial column sums; linear_grad_sum_kernel adds them
 #include "rb_elem.hpp"
 #include "rb_internal.h"
@@ -102,10 +103,8 @@ __device__ __forceinline__ l_u4 load_16(__amdgpu_buffer_rsrc_t r, uint32_t voff,
   return __builtin_amdgcn_raw_buffer_load_b128(r, (int)voff, soff, 0);
 }
 
-constexpr int kTN = 256;           // weight rows per tile: 64 per wave
 constexpr int kTK = 64;            // columns per step
 constexpr int kRowB = kTK * 2;     // bytes of a staged row
-constexpr int kStages = 4;         // steps held in LDS: two being read, two arriving
 constexpr uint32_t kOob = 0x80000000u;
 constexpr int kXcds = 8;
 constexpr int kPadRow = 68;        // floats of a row in the epilogue's LDS transposition
@@ -124,235 +123,180 @@ struct TileArgs {
   Epilogue e;
 };
 
-constexpr int tile_lds(int MT, int KG) {
-  const int stage = kStages * 16 * MT * kRowB * KG, turn = 4 * KG * 16 * kPadRow * 4;
-  const int swap = KG == 2 ? 8 * (MT > 1 ? MT / 2 : 1) * 4096 : 0;
-  const int most = stage > turn ? stage : turn;
-  return most > swap ? most : swap;
-}
-
-// Tile. 4 KG waves; wave w of a group owns weight rows 64 w .. +63 and all 16 MT batch rows (4 x MT
-// accumulators of v_mfma_f32_16x16x32). With KG = 2 the two groups take alternate 64-column steps
-// of the same tile and join at the end, so that two waves per SIMD share a CU's single tile.
-// A weight element is needed by one wave only: it goes straight from L2 to that wave's
-// registers (two steps ahead), and LDS carries only the batch rows, which all 4 waves read.
-// AL: rows of both operands are 16-byte aligned and K is a multiple of 8, so batch rows go to LDS
-// directly. Otherwise they pass through registers, and a step that holds the end of the columns is
-// read element by element.
-template <typename TA, typename TY, int MT, int KG, bool AL>
-__global__ __launch_bounds__(256 * KG, 2) void linear_tile_kernel(TileArgs a) {
+// WM x WN waves, each TM x TN accumulators of v_mfma_f32_16x16x32: a tile of 16 WM TM batch rows by
+// 16 WN TN weight rows. A step of 64 columns of the tile's rows is one LDS stage of a ring of kS. A
+// step is two phases of 32 columns; a phase's fragments are read while the phase before it multiplies.
+// In the middle of step s (the second phase's fragments are then in registers, so its stage is free) a
+// wave waits for its own loads of step s + 1, the barrier makes everyone's visible, and the loads of
+// step s + kS go into the freed stage.
+//
+// AL: rows of both operands are 16-byte aligned and K is a multiple of 8: the rows go to LDS directly
+// (buffer loads, out of range past a tile's rows and past the columns, where they give 0). Otherwise
+// they pass through registers one step ahead, by 16-byte loads at any address, and the step that holds
+// the end of the columns is read element by element.
+template <typename TA, typename TY, int WM, int WN, int TM, int TN, int kS, bool AL>
+__global__ __launch_bounds__(64 * WM * WN, 2) void linear_tile_kernel(TileArgs a) {
+  constexpr int kWaves = WM * WN;
+  constexpr int BM = 16 * WM * TM, BN = 16 * WN * TN;
+  constexpr int kStage = (BM + BN) * kRowB;
+  constexpr int kPer = (BM + BN) / 8 / kWaves;  // 1 KB groups a wave loads per step
+  constexpr int kPerX = BM / 8 / kWaves;
+  static_assert(BM / 8 % kWaves == 0 && BN / 8 % kWaves == 0, "a load instruction has one operand");
+  static_assert(AL || kS == 2, "through registers a step is written two steps ahead");
   extern __shared__ __align__(16) uint8_t l_smem[];
   const uint32_t blk = blockIdx.x;
   const uint32_t t = blk % kXcds * a.per_xcd + blk / kXcds;  // an XCD's blocks take one run of tiles
   if (t >= a.tiles) return;
-  const int64_t m0 = (int64_t)__builtin_amdgcn_readfirstlane(t % a.tiles_m) * (16 * MT);
-  const int n0 = __builtin_amdgcn_readfirstlane(t / a.tiles_m) * kTN;
+  const int64_t m0 = (int64_t)__builtin_amdgcn_readfirstlane(t % a.tiles_m) * BM;
+  const int n0 = __builtin_amdgcn_readfirstlane(t / a.tiles_m) * BN;
   const int kb = blockIdx.y * a.chunk_k;
   const int ke = kb + a.chunk_k < a.K ? kb + a.chunk_k : a.K;
 
   const int lane = threadIdx.x & 63;
-  const int wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int grp = wv >> 2, w = wv & 3;
+  const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int wm = w % WM, wn = w / WM;
   const int lr = lane & 15, lj = lane >> 4;
 
-  const int64_t mrows = a.M - m0 < 16 * MT ? a.M - m0 : 16 * MT;
-  const int nrows = a.N - n0 < kTN ? a.N - n0 : kTN;
-  const __amdgpu_buffer_rsrc_t rx =
-      buffer_rsrc(static_cast<const TA*>(a.X) + m0 * a.ldx, (uint32_t)(mrows * a.ldx * 2));
-  const __amdgpu_buffer_rsrc_t rw =
-      buffer_rsrc(static_cast<const TA*>(a.W) + (int64_t)n0 * a.ldw, (uint32_t)(nrows * a.ldw * 2));
+  const int mrows = (int)(a.M - m0 < BM ? a.M - m0 : BM);
+  const int nrows = a.N - n0 < BN ? a.N - n0 : BN;
 
-  uint32_t woff[4];
-  const TA* wrow[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 64 * w + 16 * i + lr;
-    woff[i] = (uint32_t)(r * a.ldw * 2) + 16u * lj;
-    // a row past the last one repeats it: its outputs are not stored
-    wrow[i] = static_cast<const TA*>(a.W) + (int64_t)(n0 + (r < nrows ? r : nrows - 1)) * a.ldw;
-  }
-
-  // batch rows into LDS: 1 KB groups of 8 rows; lane l fills slot l % 8 of row l / 8 with the 16-byte
-  // chunk (l % 8) ^ (row % 8), so that the 8 rows of a fragment read's phase lie in 8 bank groups
-  constexpr int kGroupsX = 2 * MT;
-  constexpr int kPer = kGroupsX >= 4 ? kGroupsX / 4 : 1;
+  // 1 KB groups of 8 rows; lane l fills slot l % 8 of row l / 8 with the 16-byte chunk (l % 8) ^ (row % 8),
+  // so that the 8 rows of a fragment read's phase lie in 8 bank groups
   const int xc = (lane & 7) ^ (lane >> 3);
-  uint32_t xoff[kPer];
+  const auto row_of = [&](int i) { return 8 * ((i < kPerX ? i : i - kPerX) * kWaves + w) + (lane >> 3); };
+  const __amdgpu_buffer_rsrc_t rx =
+      buffer_rsrc(static_cast<const TA*>(a.X) + m0 * a.ldx, AL ? (uint32_t)(mrows * a.ldx * 2) : 0u);
+  const __amdgpu_buffer_rsrc_t rw =
+      buffer_rsrc(static_cast<const TA*>(a.W) + (int64_t)n0 * a.ldw, AL ? (uint32_t)(nrows * a.ldw * 2) : 0u);
+  uint32_t off[kPer];
+  const TA* row[kPer];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) xoff[i] = (uint32_t)((8 * (w * kPer + i) + (lane >> 3)) * a.ldx * 2) + 16u * xc;
-  uint8_t* const area = l_smem + grp * (kStages * 16 * MT * kRowB);
-  const auto k_of = [&](int i) { return kb + (i * KG + grp) * kTK; };
-  const auto dma = [&](int i) {
-    const int k0 = k_of(i);
-    const bool ok = k0 + 8 * xc < ke;
-    uint8_t* const base = area + (i & (kStages - 1)) * (16 * MT * kRowB);
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      if (kGroupsX < 4 && w >= kGroupsX) break;
-      load_to_lds(rx, base + (w * kPer + j) * 1024, ok ? xoff[j] : kOob, k0 * 2);
-    }
-  };
-  // the same through registers: a thread holds chunk slots tid + 256 j of two steps
-  constexpr int kHold = MT >= 2 ? MT / 2 : 1;
-  l_u4 hold[2][kHold];
-  const int gtid = threadIdx.x & 255;
-  const auto fetch_x = [&](int i) {
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      const int k0 = k_of(i + p);
-#pragma unroll
-      for (int j = 0; j < kHold; ++j) {
-        const int q = gtid + 256 * j, r = q >> 3, c = k0 + 8 * (q & 7);
-        if (r >= 16 * MT) continue;
-        const TA* row = static_cast<const TA*>(a.X) + (m0 + (r < mrows ? r : (int)mrows - 1)) * a.ldx;
-        if (k0 + kTK <= ke)
-          hold[p][j] = __builtin_bit_cast(l_u4, *reinterpret_cast<const typename Vec8<TA>::Raw*>(row + c));
-        else
-          hold[p][j] = __builtin_bit_cast(l_u4, load8<TA>(row, c, ke));
-      }
-    }
-  };
-  const auto stage_x = [&](int i) {
-#pragma unroll
-    for (int p = 0; p < 2; ++p)
-#pragma unroll
-      for (int j = 0; j < kHold; ++j) {
-        const int q = gtid + 256 * j, r = q >> 3;
-        if (r >= 16 * MT) continue;
-        uint8_t* const base = area + ((i + p) & (kStages - 1)) * (16 * MT * kRowB);
-        *reinterpret_cast<l_u4*>(base + r * kRowB + 16 * ((q & 7) ^ (r & 7))) = hold[p][j];
-      }
-  };
-  l_u4 wf[2][2][4];  // step parity, half of the step, weight row tile
-  const auto load_w = [&](int p, int kh, int i) {
-    const int k0 = k_of(i) + 32 * kh;
-    if constexpr (!AL) {
-      const int c = k0 + 8 * lj;
-      if (k0 + 32 <= ke) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          wf[p][kh][j] = __builtin_bit_cast(l_u4, *reinterpret_cast<const typename Vec8<TA>::Raw*>(wrow[j] + c));
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) wf[p][kh][j] = __builtin_bit_cast(l_u4, load8<TA>(wrow[j], c, ke));
-      }
-      return;
-    }
-    const bool ok = k0 + 8 * lj < ke;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      wf[p][kh][j] = load_16(rw, ok ? woff[j] : kOob, k0 * 2);
-  };
-
-  l_f4 acc[MT][4];
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = (l_f4){0.f, 0.f, 0.f, 0.f};
-
-  const uint32_t lds0 = (uint32_t)(size_t)(__attribute__((address_space(3))) uint8_t*)area;
-  // fragment row lr + 16 i has lr % 8 in its swizzle whatever i
-  const uint32_t fo0 = lr * kRowB + 16u * ((uint32_t)lj ^ (lr & 7u)), fo1 = lr * kRowB + 16u * ((4u + lj) ^ (lr & 7u));
-  l_u4 xf[MT];
-  const auto read_x = [&](int i, int stage, int kh) {
-    xf[i] = *(l_lds_u4*)(size_t)(lds0 + stage * (16 * MT * kRowB) + i * 16 * kRowB + (kh ? fo1 : fo0));
-  };
-
-  const int steps = ((ke - kb + kTK - 1) / kTK + KG - 1) / KG;
-  const int halves = (steps + 1) / 2;
-  if constexpr (AL) {
-    dma(0);
-    dma(1);
-  } else {
-    fetch_x(0);
-    stage_x(0);
-  }
-  load_w(0, 0, 0);
-  load_w(0, 1, 0);
-  load_w(1, 0, 1);
-  load_w(1, 1, 1);
-  __builtin_amdgcn_sched_barrier(0);
-  for (int h = 0; h < halves; ++h) {
-    // the 16 weight loads issued after this half's batch rows may still be in flight
-    __builtin_amdgcn_s_waitcnt(AL ? wait_vmcnt(16) : kWaitLds);
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_barrier();  // every wave's rows are in; every wave is done with the other two stages
-    asm volatile("" ::: "memory");
+  for (int i = 0; i < kPer; ++i) {
+    const int r = row_of(i);
     if constexpr (AL) {
-      dma(2 * h + 2);
-      dma(2 * h + 3);
+      off[i] = (uint32_t)(r * (i < kPerX ? a.ldx : a.ldw) * 2) + 16u * xc;
     } else {
-      fetch_x(2 * h + 2);
+      // a row past the last one repeats it: its outputs are not stored
+      row[i] = i < kPerX ? static_cast<const TA*>(a.X) + (m0 + (r < mrows ? r : mrows - 1)) * a.ldx
+                         : static_cast<const TA*>(a.W) + (int64_t)(n0 + (r < nrows ? r : nrows - 1)) * a.ldw;
+    }
+  }
+  const auto dma = [&](int s, int stage) {
+    const int k0 = kb + s * kTK;
+    const bool ok = k0 + 8 * xc < ke;
+    uint8_t* const base = l_smem + stage * kStage;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      load_to_lds(i < kPerX ? rx : rw, base + (i * kWaves + w) * 1024, ok ? off[i] : kOob, k0 * 2);
+  };
+  l_u4 hold[kPer];
+  const auto fetch = [&](int s) {
+    const int k0 = kb + s * kTK, c = k0 + 8 * xc;
+    if (k0 + kTK <= ke) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        hold[i] = __builtin_bit_cast(l_u4, *reinterpret_cast<const typename Vec8<TA>::Raw*>(row[i] + c));
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) hold[i] = __builtin_bit_cast(l_u4, load8<TA>(row[i], c, ke));
+    }
+  };
+  const auto put = [&](int stage) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      *reinterpret_cast<l_u4*>(l_smem + stage * kStage + (i * kWaves + w) * 1024 + lane * 16) = hold[i];
+  };
+
+  l_f4 acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = (l_f4){0.f, 0.f, 0.f, 0.f};
+
+  const uint32_t lds0 = (uint32_t)(size_t)(__attribute__((address_space(3))) uint8_t*)l_smem;
+  const uint32_t f0 = lr * kRowB + 16u * ((uint32_t)lj ^ (lr & 7u)), f1 = lr * kRowB + 16u * ((4u + lj) ^ (lr & 7u));
+  const uint32_t ax = lds0 + wm * TM * 16 * kRowB, aw = lds0 + (BM + wn * TN * 16) * kRowB;
+  l_u4 xf[2][TM], wf[2][TN];
+  const auto read = [&](int kh, int stage) {  // the fragments of half kh of a stage
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+      wf[kh][j] = *(l_lds_u4*)(size_t)(aw + stage * kStage + j * 16 * kRowB + (kh ? f1 : f0));
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+      xf[kh][i] = *(l_lds_u4*)(size_t)(ax + stage * kStage + i * 16 * kRowB + (kh ? f1 : f0));
+  };
+  const auto multiply = [&](int kh) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[i][j] = mfma(TA(0), wf[kh][j], xf[kh][i], acc[i][j]);
+  };
+  constexpr int kR = TM + TN, kM = TM * TN;
+  const auto barrier = [] {  // the raw barrier: __syncthreads would also wait for every load in flight
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+
+  const int steps = (ke - kb + kTK - 1) / kTK;
+  if constexpr (AL) {
+#pragma unroll
+    for (int s = 0; s < kS; ++s) dma(s, s);
+    __builtin_amdgcn_s_waitcnt(wait_vmcnt((kS - 1) * kPer));
+  } else {
+    fetch(0);
+    put(0);
+    fetch(1);
+    put(1);
+    fetch(2);
+    __builtin_amdgcn_s_waitcnt(kWaitLds);
+  }
+  barrier();
+  read(0, 0);
+  __builtin_amdgcn_sched_barrier(0);
+  int st = 0;
+  for (int s = 0; s < steps; ++s) {
+    read(1, st);
+    multiply(0);
+    // the reads spread over the first products
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // MFMA
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // LDS read
     }
     __builtin_amdgcn_sched_barrier(0);
-    const int st = (h & 1) * 2;
-#pragma unroll
-    for (int i = 0; i < MT; ++i) read_x(i, st, 0);
+    const int next = st + 1 == kS ? 0 : st + 1;
+    __builtin_amdgcn_s_waitcnt(AL ? wait_vmcnt((kS - 2) * kPer) & kWaitLds : kWaitLds);
+    barrier();
+    if constexpr (AL) {
+      dma(s + kS, st);
+    } else {
+      put(st);
+      fetch(s + 3);
+    }
     __builtin_amdgcn_sched_barrier(0);
+    read(0, next);
+    multiply(1);
 #pragma unroll
-    for (int p = 0; p < 2; ++p)
-#pragma unroll
-      for (int kh = 0; kh < 2; ++kh) {
-        const bool more = p == 0 || kh == 0;  // the other stages' rows are only safe after the next barrier
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] = mfma(TA(0), wf[p][kh][j], xf[i], acc[i][j]);
-          if (more) read_x(i, st + p + kh, kh ^ 1);
-        }
-        load_w(p, kh, 2 * h + p + 2);
-        // as written: a fragment is read again as soon as its 4 products are issued, the weights once
-        // all are, and neither is moved next to its use
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);             // MFMA
-          if (more) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // LDS read
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    if constexpr (!AL) stage_x(2 * h + 2);
+    for (int r = 0; r < kR; ++r) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
     __builtin_amdgcn_sched_barrier(0);
+    st = next;
   }
   // loads past the last step (out of range, zeros) end before LDS is used again
   __builtin_amdgcn_s_waitcnt(wait_vmcnt(0));
   __syncthreads();
 
-  int i0 = 0, i1 = MT;
-  if constexpr (KG == 2) {
-    // the groups swap halves of the batch rows' tiles and add: group 0 keeps the first half (for MT = 1
-    // group 1 gives all to group 0)
-    constexpr int kHalf = MT > 1 ? MT / 2 : 1;
-    float* const mine = reinterpret_cast<float*>(l_smem) + (size_t)wv * (kHalf * 4 * 256);
-    const float* const other = reinterpret_cast<float*>(l_smem) + (size_t)(wv ^ 4) * (kHalf * 4 * 256);
-#pragma unroll
-    for (int i = 0; i < kHalf; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const l_f4 v = grp == 0 ? acc[MT > 1 ? i + kHalf : i][j] : acc[i][j];
-        *reinterpret_cast<l_f4*>(mine + ((i * 4 + j) * 64 + lane) * 4) = v;
-      }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kHalf; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const l_f4 o = *reinterpret_cast<const l_f4*>(other + ((i * 4 + j) * 64 + lane) * 4);
-        if (grp == 0) acc[i][j] = acc[i][j] + o;
-        if (MT > 1 && grp == 1) acc[i + kHalf][j] = o + acc[i + kHalf][j];
-      }
-    __syncthreads();
-    i0 = grp == 0 ? 0 : kHalf;
-    i1 = grp == 0 ? kHalf : MT;
-  }
-
-  // 16 rows at a time through the wave's own LDS area, so that 8 lanes hold 64 consecutive columns of
-  // a row and whole 128-byte lines are read and written. D of the product: lane l holds weight rows
+  // 16 rows by 64 columns at a time through the wave's own LDS area, so that 8 lanes hold 64 consecutive
+  // columns of a row and whole lines are read and written. D of the product: lane l holds weight rows
   // 4 (l / 16) .. +3 of batch row l % 16.
-  float* const turn = reinterpret_cast<float*>(l_smem) + wv * (16 * kPadRow);
+  float* const turn = reinterpret_cast<float*>(l_smem) + w * (16 * kPadRow);
 #pragma unroll 1
-  for (int i = i0; i < i1; ++i) {
+  for (int i = 0; i < TM; ++i) {
 #pragma unroll
-    for (int q = 0; q < MT; ++q)
+    for (int q = 0; q < TM; ++q)
       if (q == i) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) *reinterpret_cast<l_f4*>(turn + lr * kPadRow + 16 * j + 4 * lj) = acc[q][j];
@@ -366,8 +310,8 @@ __global__ __launch_bounds__(256 * KG, 2) void linear_tile_kernel(TileArgs a) {
       const l_f4 hi = *reinterpret_cast<const l_f4*>(turn + r * kPadRow + c + 4);
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[j] = lo[j], v[4 + j] = hi[j];
-      const int64_t m = m0 + 16 * i + r;
-      const int n = n0 + 64 * w + c;
+      const int64_t m = m0 + (wm * TM + i) * 16 + r;
+      const int n = n0 + wn * 64 + c;
       if (m < a.M && n < a.N) {
         if (a.part)
           store8<float>(a.part + ((int64_t)blockIdx.y * a.M + m) * a.N, n, a.N, v);
@@ -377,6 +321,7 @@ __global__ __launch_bounds__(256 * KG, 2) void linear_tile_kernel(TileArgs a) {
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
+  static_assert(TN == 4, "a wave's 64 columns");
 }
 
 struct JoinArgs {
@@ -400,6 +345,66 @@ __global__ __launch_bounds__(256) void linear_join_kernel(JoinArgs a) {
     for (int j = 0; j < 8; ++j) v[j] += p[j];
   }
   finish8<TA, TY>(a.e, v, m, n, a.N);
+}
+
+// ---------------------------------------------------------------------------------------------
+// up to 4 batch rows: HBM's rate for the weights is the bound, and the vector units' products are far
+// below it. A wave owns kRows weight rows, its lanes 8 columns each of a 512-column step; kRows x kSteps
+// loads of 1 KB are in flight per wave. One launch, no partial sums in memory.
+// ---------------------------------------------------------------------------------------------
+template <typename TA, typename TY, int MR, int kRows, int kSteps>
+__global__ __launch_bounds__(256) void linear_rows_kernel(TileArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int n0 = (blockIdx.x * 4 + w) * kRows;
+  if (n0 >= a.N) return;
+  const TA* const X = static_cast<const TA*>(a.X);
+  const TA* row[kRows];
+#pragma unroll
+  for (int r = 0; r < kRows; ++r)  // a row past the last one repeats it: its sums are not stored
+    row[r] = static_cast<const TA*>(a.W) + (int64_t)(n0 + r < a.N ? n0 + r : a.N - 1) * a.ldw;
+  float sum[MR][kRows];
+#pragma unroll
+  for (int m = 0; m < MR; ++m)
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) sum[m][r] = 0.f;
+  for (int k0 = 0; k0 < a.K; k0 += 512 * kSteps) {
+    typename Vec8<TA>::Raw wr[kSteps][kRows], xr[kSteps][MR];
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const int c = k0 + 512 * s + 8 * lane;
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) wr[s][r] = load8<TA>(row[r], c, a.K);
+#pragma unroll
+      for (int m = 0; m < MR; ++m) xr[s][m] = load8<TA>(X + (m < a.M ? m : 0) * a.ldx, c, a.K);
+    }
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+      for (int m = 0; m < MR; ++m)
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            sum[m][r] = fmaf(Vec8<TA>::get(wr[s][r], j), Vec8<TA>::get(xr[s][m], j), sum[m][r]);
+  }
+  // lane r + kRows m takes sum (m, r)
+  float mine = 0.f;
+#pragma unroll
+  for (int m = 0; m < MR; ++m)
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const float v = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(wave_sum_dpp(sum[m][r])), 63));
+      mine = lane == m * kRows + r ? v : mine;
+    }
+  const int m = lane / kRows, n = n0 + lane % kRows;
+  if (m >= MR || m >= a.M || n >= a.N) return;
+  const Epilogue& e = a.e;
+  if (e.bias) mine += e.bias[n];
+  if (e.Z) static_cast<TA*>(e.Z)[m * e.ldz + n] = Vec8<TA>::narrow(mine);
+  if (e.act != RB_ACT_NONE) mine = act_value(mine, e.act);
+  if (e.R) mine += (float)static_cast<const TY*>(e.R)[m * e.ldr + n];
+  static_cast<TY*>(e.Y)[m * e.ldy + n] = Vec8<TY>::narrow(mine);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -465,18 +470,29 @@ __global__ __launch_bounds__(512) void linear_grad_sum_kernel(const float* part,
   }
 }
 
+bool tile_aligned(const void* X, int64_t ldx, const void* W, int64_t ldw, int64_t K) {
+  const auto a16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
+  // a tile's rows lie within 2^31 bytes, the out-of-range marker
+  return a16(X) && a16(W) && ldx % 8 == 0 && ldw % 8 == 0 && K % 8 == 0 && ldx < (1 << 21) && ldw < (1 << 21);
+}
+
+// How a product is laid over the GPU's 256 compute units: `bm` batch rows by 256 weight rows per tile
+// (32, 64, 128; 256 for the first `big_n` weight rows), the columns in `chunks`.
 struct Plan {
-  int mt, chunks, chunk_k;
-  bool two;  // two wave groups per tile
+  int bm, chunks, chunk_k, big_n;
 };
-// see launch: how many blocks a shape gives
 Plan plan_tiles(int64_t M, int64_t N, int64_t K, bool aligned) {
-  Plan p;
-  p.mt = M <= 16 ? 1 : M <= 32 ? 2 : M <= 64 || !aligned ? 4 : 8;
-  const int64_t tiles = (M + 16 * p.mt - 1) / (16 * p.mt) * ((N + kTN - 1) / kTN);
-  p.two = p.mt == 8 && tiles < 512;
+  Plan p{};
+  p.bm = M <= 32 ? 32 : M <= 64 ? 64 : 128;
+  const int64_t tn = (N + 255) / 256;
+  if (aligned && M > 128) {
+    const int64_t tm2 = (M + 255) / 256, rounds = tm2 * tn / 256;
+    if (rounds > 0) p.big_n = (int)(rounds * 256 / tm2 * 256);
+    if (p.big_n >= N) p.big_n = (int)N;
+  }
+  const int64_t tiles = (M + p.bm - 1) / p.bm * ((N - p.big_n + 255) / 256);
   const int64_t steps = (K + kTK - 1) / kTK;
-  const int64_t want = tiles >= 192 ? 1 : (p.two ? 256 : 512) / tiles;
+  const int64_t want = tiles == 0 || tiles > 128 ? 1 : 256 / tiles;
   const int64_t most = steps / 8 > 1 ? steps / 8 : 1;
   const int64_t chunks = want < most ? want : most;
   p.chunk_k = (int)((steps + chunks - 1) / chunks) * kTK;
@@ -484,47 +500,61 @@ Plan plan_tiles(int64_t M, int64_t N, int64_t K, bool aligned) {
   return p;
 }
 
-bool tile_aligned(const void* X, int64_t ldx, const void* W, int64_t ldw, int64_t K) {
-  const auto a16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
-  // a tile's rows lie within 2^31 bytes, the out-of-range marker
-  return a16(X) && a16(W) && ldx % 8 == 0 && ldw % 8 == 0 && K % 8 == 0 && ldx < (1 << 21) && ldw < (1 << 21);
-}
-
-template <typename TA, typename TY, int MT, int KG, bool AL>
-hipError_t launch_tile(const TileArgs& a, int chunks, hipStream_t s) {
-  constexpr int lds = tile_lds(MT, KG);
-  static const hipError_t attr = hipFuncSetAttribute((const void*)linear_tile_kernel<TA, TY, MT, KG, AL>,
+template <typename TA, typename TY, int WM, int WN, int TM, int kS, bool AL>
+hipError_t launch_tile(TileArgs a, int chunks, hipStream_t s) {
+  constexpr int BM = 16 * WM * TM, BN = 64 * WN;
+  constexpr int stage = kS * (BM + BN) * kRowB, turn = WM * WN * 16 * kPadRow * 4;
+  constexpr int lds = stage > turn ? stage : turn;
+  static const hipError_t attr = hipFuncSetAttribute((const void*)linear_tile_kernel<TA, TY, WM, WN, TM, 4, kS, AL>,
                                                      hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (attr != hipSuccess) return attr;
-  linear_tile_kernel<TA, TY, MT, KG, AL>
-      <<<dim3(a.per_xcd * kXcds, (uint32_t)chunks), 256 * KG, lds, s>>>(a);
+  const int64_t tm = (a.M + BM - 1) / BM, tiles = tm * ((a.N + BN - 1) / BN);
+  if (tiles > 0x70000000) return hipErrorInvalidConfiguration;
+  a.tiles_m = (uint32_t)tm;
+  a.tiles = (uint32_t)tiles;
+  a.per_xcd = (uint32_t)((tiles + kXcds - 1) / kXcds);
+  linear_tile_kernel<TA, TY, WM, WN, TM, 4, kS, AL>
+      <<<dim3(a.per_xcd * kXcds, (uint32_t)chunks), 64 * WM * WN, lds, s>>>(a);
+  return hipGetLastError();
+}
+
+template <typename TA, typename TY, int MR>
+hipError_t launch_rows(const TileArgs& a, hipStream_t s) {
+  if (a.N >= 4096)
+    linear_rows_kernel<TA, TY, MR, 4, 4><<<dim3((uint32_t)((a.N + 15) / 16)), 256, 0, s>>>(a);
+  else
+    linear_rows_kernel<TA, TY, MR, 1, 8><<<dim3((uint32_t)((a.N + 3) / 4)), 256, 0, s>>>(a);
   return hipGetLastError();
 }
 
 template <typename TA, typename TY>
 hipError_t launch_product(TileArgs a, void* ws, hipStream_t s) {
+  if (a.M == 1) return launch_rows<TA, TY, 1>(a, s);
+  if (a.M <= 4) return launch_rows<TA, TY, 4>(a, s);
   const bool al = tile_aligned(a.X, a.ldx, a.W, a.ldw, a.K);
   const Plan p = plan_tiles(a.M, a.N, a.K, al);
-  const int64_t tm = (a.M + 16 * p.mt - 1) / (16 * p.mt), tiles = tm * ((a.N + kTN - 1) / kTN);
-  if (tiles > 0x70000000) return hipErrorInvalidConfiguration;
-  a.tiles_m = (uint32_t)tm;
-  a.tiles = (uint32_t)tiles;
-  a.per_xcd = (uint32_t)((tiles + kXcds - 1) / kXcds);
+  a.chunk_k = (a.K + kTK - 1) / kTK * kTK;
+  if (p.big_n > 0) {
+    TileArgs b = a;
+    b.N = p.big_n;
+    const hipError_t e = launch_tile<TA, TY, 2, 4, 8, 2, true>(b, 1, s);
+    if (e != hipSuccess || p.big_n == a.N) return e;
+    a.N -= p.big_n;
+    a.W = static_cast<const TA*>(a.W) + (int64_t)p.big_n * a.ldw;
+    if (a.e.bias) a.e.bias += p.big_n;
+    if (a.e.R) a.e.R = static_cast<const TY*>(a.e.R) + p.big_n;
+    if (a.e.Z) a.e.Z = static_cast<TA*>(a.e.Z) + p.big_n;
+    a.e.Y = static_cast<TY*>(a.e.Y) + p.big_n;
+  }
   a.chunk_k = p.chunk_k;
   a.part = p.chunks > 1 ? static_cast<float*>(ws) : nullptr;
   hipError_t e;
-  if (!al)
-    e = p.mt == 1 ? launch_tile<TA, TY, 1, 1, false>(a, p.chunks, s)
-                  : p.mt == 2 ? launch_tile<TA, TY, 2, 1, false>(a, p.chunks, s)
-                              : launch_tile<TA, TY, 4, 1, false>(a, p.chunks, s);
-  else if (p.mt == 1)
-    e = launch_tile<TA, TY, 1, 1, true>(a, p.chunks, s);
-  else if (p.mt == 2)
-    e = launch_tile<TA, TY, 2, 1, true>(a, p.chunks, s);
-  else if (p.mt == 4)
-    e = launch_tile<TA, TY, 4, 1, true>(a, p.chunks, s);
+  if (p.bm == 32)
+    e = al ? launch_tile<TA, TY, 1, 4, 2, 3, true>(a, p.chunks, s) : launch_tile<TA, TY, 1, 4, 2, 2, false>(a, p.chunks, s);
+  else if (p.bm == 64)
+    e = al ? launch_tile<TA, TY, 1, 4, 4, 3, true>(a, p.chunks, s) : launch_tile<TA, TY, 1, 4, 4, 2, false>(a, p.chunks, s);
   else
-    e = p.two ? launch_tile<TA, TY, 8, 2, true>(a, p.chunks, s) : launch_tile<TA, TY, 8, 1, true>(a, p.chunks, s);
+    e = al ? launch_tile<TA, TY, 2, 4, 4, 3, true>(a, p.chunks, s) : launch_tile<TA, TY, 2, 4, 4, 2, false>(a, p.chunks, s);
   if (e != hipSuccess || p.chunks == 1) return e;
   const JoinArgs j{a.part, a.M, a.N, p.chunks, a.e};
   linear_join_kernel<TA, TY><<<dim3((uint32_t)((a.N + 2047) / 2048), (uint32_t)a.M), 256, 0, s>>>(j);
@@ -542,10 +572,11 @@ int grad_strip(int64_t M, int64_t N) {
 }  // namespace
 
 size_t linear_workspace_bytes(int64_t N, int64_t K, int64_t M) {
+  if (M <= 4) return 0;
   size_t most = 0;
   for (int al = 0; al < 2; ++al) {
     const Plan p = plan_tiles(M, N, K, al != 0);
-    const size_t b = p.chunks > 1 ? (size_t)p.chunks * (size_t)M * (size_t)N * 4 : 0;
+    const size_t b = p.chunks > 1 ? (size_t)p.chunks * (size_t)M * (size_t)(N - p.big_n) * 4 : 0;
     most = b > most ? b : most;
   }
   return most;

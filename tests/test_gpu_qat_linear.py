@@ -246,6 +246,6 @@ def test_refusals():
     with pytest.raises(rb.RbError):
         rb.qat_linear(X, W, y_dtype=torch.float16)
     with pytest.raises(rb.RbError):
-        rb.qat_linear(mat(r, 1, 8192, "bf16"), mat(r, 64, 8192, "bf16"), ws=torch.empty(16, dtype=torch.uint8, device=dev()))
+        rb.qat_linear(mat(r, 40, 8192, "bf16"), mat(r, 64, 8192, "bf16"), ws=torch.empty(16, dtype=torch.uint8, device=dev()))
     with pytest.raises(rb.RbError):
         rb.qat_linear_backward(X, None, act="relu", a_dtype=torch.bfloat16)
