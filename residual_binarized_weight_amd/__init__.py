@@ -25,6 +25,7 @@ return CUDA (HIP) tensors on the current device and enqueue on the current strea
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -55,7 +56,7 @@ def _ptr(t: torch.Tensor | None):
         raise ValueError("librb takes device tensors")
     if not t.is_contiguous():
         raise ValueError("librb takes contiguous tensors")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _ptr_rows(t: torch.Tensor | None):
@@ -69,11 +70,17 @@ def _ptr_rows(t: torch.Tensor | None):
         raise ValueError("librb takes matrices with unit stride along rows")
     if t.dim() == 3 and t.stride(0) != t.shape[1] * t.stride(1):
         raise ValueError("librb takes plane stacks with planes stored back to back")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
+
+
+# the handle alone costs a tenth of what a Stream object does (0.3 against 2.8 us per call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    if _raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch.cuda.current_device())
 
 
 def version() -> int:
@@ -107,7 +114,7 @@ def pack(W: torch.Tensor, k: int, h: torch.Tensor | None = None, group: int = 0,
     if planes is None:
         planes = torch.zeros((k, N, ldp), dtype=torch.int32, device=W.device)
     shape = (k, N) if group == 0 else (k, N, (K + group - 1) // group)
-    g = torch.empty(shape, dtype=scale_dtype, device=W.device)
+    g = torch.empty((M, D), dtype=scale_dtype, device=W.device)
     check("rb_pack", lib.rb_pack(_ptr(W), _dt(W.dtype), N, K, W.stride(0), k, group, _ptr(h),
                                  _dt(scale_dtype), _ptr(planes), ldp, _ptr(g), _ptr(d_status),
                                  _stream()))
@@ -353,18 +360,30 @@ def _vec(name: str, t: torch.Tensor | None, n: int):
     """A contiguous fp32 device vector of n elements, or None."""
     if t is None:
         return None
-    if t.dtype != torch.float32 or t.numel() != n:
+    if t.dtype is not torch.float32 or t.numel() != n:
         raise ValueError(f"{name} is an fp32 vector of {n} elements")
     return _ptr(t)
 
 
-def _rows(name: str, t: torch.Tensor | None, shape, dtype):
-    """(pointer, row stride) of a matrix of this shape and type, or (None, 0)."""
+def _rows(name: str, t: torch.Tensor | None, M: int, N: int, dtype):
+    """(pointer, row stride) of an M x N matrix of this type, or (None, 0)."""
     if t is None:
         return None, 0
-    if t.shape != shape or t.dtype != dtype:
-        raise ValueError(f"{name} is a {dtype} matrix of shape {tuple(shape)}")
-    return _ptr_rows(t), t.stride(0) if shape[0] > 1 else max(t.stride(0), shape[1])
+    if t.dtype is not dtype or t.shape != (M, N):
+        raise ValueError(f"{name} is a {dtype} matrix of shape {(M, N)}")
+    if not t.is_cuda:
+        raise ValueError("librb takes device tensors")
+    if t.is_contiguous():
+        return t.data_ptr(), N
+    ld, step = t.stride()
+    if (step != 1 and N > 1) or (ld < N and M > 1):
+        raise ValueError("librb takes matrices with unit stride along rows")
+    return t.data_ptr(), ld if M > 1 else max(ld, N)
+
+
+@functools.lru_cache(maxsize=4096)
+def _ws_bytes(op: int, N: int, K: int, M: int) -> int:
+    return workspace_bytes(op, 1, N, K, M)
 
 
 def qat_linear(X: torch.Tensor, What: torch.Tensor, bias: torch.Tensor | None = None, act: str = "none",
@@ -382,14 +401,14 @@ def qat_linear(X: torch.Tensor, What: torch.Tensor, bias: torch.Tensor | None = 
         Y = torch.empty((M, N), dtype=y_dtype or (dt if residual is None else residual.dtype), device=X.device)
     if Z is None and save_z:
         Z = torch.empty((M, N), dtype=dt, device=X.device)
-    n = workspace_bytes(RB_OP_QAT_LINEAR, 1, N, K, M)
+    n = _ws_bytes(RB_OP_QAT_LINEAR, N, K, M)
     if ws is None and n:
         ws = torch.empty(n, dtype=torch.uint8, device=X.device)
-    xp, ldx = _rows("X", X, (M, K), dt)
-    wp, ldw = _rows("What", What, (N, K), dt)
-    yp, ldy = _rows("Y", Y, (M, N), Y.dtype)
-    rp, ldr = _rows("residual", residual, (M, N), Y.dtype)
-    zp, ldz = _rows("Z", Z, (M, N), dt)
+    xp, ldx = _rows("X", X, M, K, dt)
+    wp, ldw = _rows("What", What, N, K, dt)
+    yp, ldy = _rows("Y", Y, M, N, Y.dtype)
+    rp, ldr = _rows("residual", residual, M, N, Y.dtype)
+    zp, ldz = _rows("Z", Z, M, N, dt)
     check("rb_qat_linear", lib.rb_qat_linear(xp, _dt(dt), M, ldx, wp, ldw, N, K, _vec("bias", bias, N), _ACT[act], rp, ldr,
                                              zp, ldz, yp, _dt(Y.dtype), ldy, _ptr(ws), 0 if ws is None else ws.numel(),
                                              _stream()))
@@ -411,10 +430,10 @@ def qat_linear_backward(dY: torch.Tensor, Z: torch.Tensor | None, act: str = "no
     elif db is None:
         db = torch.empty(N, dtype=torch.float32, device=dY.device)
     if ws is None and bias:
-        ws = torch.empty(workspace_bytes(RB_OP_QAT_LINEAR_BACKWARD, 1, N, 1, M), dtype=torch.uint8, device=dY.device)
-    dyp, lddy = _rows("dY", dY, (M, N), dY.dtype)
-    zp, ldz = _rows("Z", Z, (M, N), dt)
-    dzp, lddz = _rows("dZ", dZ, (M, N), dt)
+        ws = torch.empty(_ws_bytes(RB_OP_QAT_LINEAR_BACKWARD, N, 1, M), dtype=torch.uint8, device=dY.device)
+    dyp, lddy = _rows("dY", dY, M, N, dY.dtype)
+    zp, ldz = _rows("Z", Z, M, N, dt)
+    dzp, lddz = _rows("dZ", dZ, M, N, dt)
     check("rb_qat_linear_backward", lib.rb_qat_linear_backward(dyp, _dt(dY.dtype), M, N, lddy, zp, _dt(dt), ldz, _ACT[act],
                                                                dzp, lddz, _vec("db", db, N), _ptr(ws),
                                                                0 if ws is None else ws.numel(), _stream()))
@@ -424,11 +443,11 @@ def qat_linear_backward(dY: torch.Tensor, Z: torch.Tensor | None, act: str = "no
 _NORM = {"none": _lib.RB_NORM_NONE, "rms": _lib.RB_NORM_RMS, "layer": _lib.RB_NORM_LAYER}
 
 
-def _gate_rows(gate, shape, dtype):
+def _gate_rows(gate, M: int, D: int, dtype):
     """(pointer, row stride) of a gate: an fp32 vector (stride 0) or rows."""
     if gate is not None and gate.dim() == 1:
-        return _vec("gate", gate, shape[1]), 0
-    return _rows("gate", gate, shape, dtype)
+        return _vec("gate", gate, D), 0
+    return _rows("gate", gate, M, D, dtype)
 
 
 def resnorm_forward(Y: torch.Tensor, R: torch.Tensor | None, w_pre: torch.Tensor | None, w_post=None, b_pre=None,
@@ -449,12 +468,12 @@ def resnorm_forward(Y: torch.Tensor, R: torch.Tensor | None, w_pre: torch.Tensor
         X = torch.empty((M, D), dtype=Y.dtype, device=Y.device)
     if stats is None:
         stats = torch.empty((M, 4), dtype=torch.float32, device=Y.device)
-    shape, dt = Y.shape, Y.dtype
-    yp, ldy = _rows("Y", Y, shape, dt)
-    rp, ldr = _rows("R", R, shape, sdt)
-    gp, ldg = _gate_rows(gate, shape, dt)
-    sp, lds = _rows("S", S, shape, sdt)
-    xp, ldx = _rows("X", X, shape, dt)
+    dt = Y.dtype
+    yp, ldy = _rows("Y", Y, M, D, dt)
+    rp, ldr = _rows("R", R, M, D, sdt)
+    gp, ldg = _gate_rows(gate, M, D, dt)
+    sp, lds = _rows("S", S, M, D, sdt)
+    xp, ldx = _rows("X", X, M, D, dt)
     check("rb_resnorm_forward", lib.rb_resnorm_forward(
         yp, _dt(dt), M, D, ldy, rp, _dt(sdt), ldr, gp, ldg, alpha, _NORM[post], _vec("w_post", w_post, D),
         _vec("b_post", b_post, D), _NORM[pre], _vec("w_pre", w_pre, D), _vec("b_pre", b_pre, D), eps, sp, lds, xp, ldx,
@@ -470,29 +489,29 @@ def resnorm_backward(dX: torch.Tensor | None, dS: torch.Tensor | None, Y: torch.
     dY, dR, dgate (like the gate), dw_pre, dw_post and, with `bias`, db_pre, db_post (fp32 [D]); None
     where there is no such input. Other arguments as in the forward call."""
     M, D = Y.shape
-    dev, dt, sdt, shape = Y.device, Y.dtype, S.dtype, Y.shape
+    dev, dt, sdt = Y.device, Y.dtype, S.dtype
     post = post or ("none" if w_post is None else "rms")
     has_pre, has_post = pre != "none", post != "none"
     if dY is None:
-        dY = torch.empty(shape, dtype=dt, device=dev)
+        dY = torch.empty((M, D), dtype=dt, device=dev)
     if dR is None:
-        dR = torch.empty(shape, dtype=sdt, device=dev)
+        dR = torch.empty((M, D), dtype=sdt, device=dev)
     # the vectors' gradients lie in one buffer
     names = [n for n, there in (("dw_pre", has_pre), ("db_pre", has_pre and bias), ("dw_post", has_post),
                                 ("db_post", has_post and bias), ("dgate", gate is not None and gate.dim() == 1)) if there]
     vec = dict(zip(names, torch.empty((len(names), D), dtype=torch.float32, device=dev).unbind(0))) if names else {}
     out = {"dY": dY, "dR": dR, "dgate": None, "dw_pre": None, "dw_post": None, "db_pre": None, "db_post": None, **vec}
     if gate is not None and gate.dim() != 1:
-        out["dgate"] = torch.empty(shape, dtype=dt, device=dev)
+        out["dgate"] = torch.empty((M, D), dtype=dt, device=dev)
     if ws is None:
-        ws = torch.empty(workspace_bytes(RB_OP_RESNORM_BACKWARD, 1, D, 1, M), dtype=torch.uint8, device=dev)
-    dxp, lddx = _rows("dX", dX, shape, dt)
-    dsp, ldds = _rows("dS", dS, shape, sdt)
-    yp, ldy = _rows("Y", Y, shape, dt)
-    sp, lds = _rows("S", S, shape, sdt)
-    gp, ldg = _gate_rows(gate, shape, dt)
-    dyp, lddy = _rows("dY", dY, shape, dt)
-    drp, lddr = _rows("dR", dR, shape, sdt)
+        ws = torch.empty(_ws_bytes(RB_OP_RESNORM_BACKWARD, D, 1, M), dtype=torch.uint8, device=dev)
+    dxp, lddx = _rows("dX", dX, M, D, dt)
+    dsp, ldds = _rows("dS", dS, M, D, sdt)
+    yp, ldy = _rows("Y", Y, M, D, dt)
+    sp, lds = _rows("S", S, M, D, sdt)
+    gp, ldg = _gate_rows(gate, M, D, dt)
+    dyp, lddy = _rows("dY", dY, M, D, dt)
+    drp, lddr = _rows("dR", dR, M, D, sdt)
     dg = out["dgate"]
     check("rb_resnorm_backward", lib.rb_resnorm_backward(
         dxp, _dt(dt), M, D, lddx, dsp, _dt(sdt), ldds, yp, ldy, sp, lds, _vec("stats", stats, 4 * M), gp, ldg, alpha,

@@ -57,6 +57,35 @@ __device__ __forceinline__ typename Vec8<T>::Raw load8(const T* row, int c, int 
   }
   return r;
 }
+// The same for a uniform n of 8 or more, without element loads: the vector that holds the end of the
+// row is read 8 elements before it and, when it is used, shifted down by the (uniform) rest.
+__device__ __forceinline__ void shift_down(Vec8<float>::Raw& r, int by) {
+#pragma unroll
+  for (int bit = 4; bit >= 1; bit >>= 1)
+    if (by & bit) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) r.w[i] = i + bit < 8 ? r.w[i + bit] : 0u;
+    }
+}
+template <typename Raw>
+__device__ __forceinline__ void shift_down(Raw& r, int by) {
+#pragma unroll
+  for (int bit = 4; bit >= 2; bit >>= 1)
+    if (by & bit) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r.w[i] = i + bit / 2 < 4 ? r.w[i + bit / 2] : 0u;
+    }
+  if (by & 1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.w[i] = (r.w[i] >> 16) | (i < 3 ? r.w[i + 1] << 16 : 0u);
+  }
+}
+// elements c .. c+7 into r, or the row's last 8 where those pass its end (to be shifted down by
+// c + 8 - n before use); r is left alone from n on
+template <typename T>
+__device__ __forceinline__ void load8_long(typename Vec8<T>::Raw& r, const T* row, int c, int n) {
+  if (c < n) r = *reinterpret_cast<const typename Vec8<T>::Raw*>(row + (c + 8 <= n ? c : n - 8));
+}
 template <typename T>
 __device__ __forceinline__ void store8(T* row, int c, int n, const float (&v)[8]) {
   if (c + 8 <= n) {
