@@ -348,10 +348,12 @@ __global__ __launch_bounds__(256) void linear_join_kernel(JoinArgs a) {
 }
 
 // ---------------------------------------------------------------------------------------------
-// up to 4 batch rows: HBM's rate for the weights is the bound, and the vector units' products are far
+// up to kMaxRows batch rows: HBM's rate for the weights is the bound, and the vector units' products are far
 // below it. A wave owns kRows weight rows, its lanes 8 columns each of a 512-column step; kRows x kSteps
 // loads of 1 KB are in flight per wave. One launch, no partial sums in memory.
 // ---------------------------------------------------------------------------------------------
+constexpr int kMaxRows = 4;
+
 template <typename TA, typename TY, int MR, int kRows, int kSteps>
 __global__ __launch_bounds__(256) void linear_rows_kernel(TileArgs a) {
   const int lane = threadIdx.x & 63;
@@ -426,7 +428,7 @@ __global__ __launch_bounds__(256) void linear_grad_kernel(GradArgs a) {
   const int64_t r0 = (int64_t)blockIdx.y * a.strip;
   const int64_t r1 = r0 + a.strip < a.M ? r0 + a.strip : a.M;
   float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
+#pragma unroll 4
   for (int64_t m = r0 + w; m < r1; m += 4) {
     float d[8], z[8];
     widen8<TY>(load8<TY>(static_cast<const TY*>(a.dY) + m * a.lddy, n, a.N), d);
@@ -478,24 +480,45 @@ bool tile_aligned(const void* X, int64_t ldx, const void* W, int64_t ldw, int64_
 
 // How a product is laid over the GPU's 256 compute units: `bm` batch rows by 256 weight rows per tile
 // (32, 64, 128; 256 for the first `big_n` weight rows), the columns in `chunks`.
+//
+// 256-row tiles move two thirds of the bytes per product that 128-row ones do, but a round of 256 of
+// them must be full to pay: whole rounds go to them, the rest to the small tiles (2048 x 11008 x 4096:
+// 127 + 70 us; 128-row tiles alone 198 us, 256-row ones alone 196 us).
+// The rest, and every smaller product, is laid out by estimate, in us: a step of a tile costs `one` when
+// few units are busy and `all` when every unit loads at once; 5 for the launch and the ends of the
+// pipeline; a split costs its partial sums' way to memory and back (5 MB / us) and 2 for the join. The
+// figures are fits to measured runs (16..1024 rows, 1000..4096 weight rows and columns), where the choice
+// is within 10 % of the best of the 15 layouts; one layout for all would cost up to twice the time
+// (512 x 4096 x 4096: 32-row tiles 30.6 us, 128-row tiles 47.7 us and in 4 chunks 35.4 us; 64 x 4096 x
+// 4096: 28.7 us whole, 14.4 us in 4 chunks).
 struct Plan {
   int bm, chunks, chunk_k, big_n;
 };
 Plan plan_tiles(int64_t M, int64_t N, int64_t K, bool aligned) {
   Plan p{};
-  p.bm = M <= 32 ? 32 : M <= 64 ? 64 : 128;
   const int64_t tn = (N + 255) / 256;
   if (aligned && M > 128) {
     const int64_t tm2 = (M + 255) / 256, rounds = tm2 * tn / 256;
-    if (rounds > 0) p.big_n = (int)(rounds * 256 / tm2 * 256);
-    if (p.big_n >= N) p.big_n = (int)N;
+    if (rounds > 0) p.big_n = (int)(rounds * 256 / tm2 * 256 < N ? rounds * 256 / tm2 * 256 : N);
   }
-  const int64_t tiles = (M + p.bm - 1) / p.bm * ((N - p.big_n + 255) / 256);
-  const int64_t steps = (K + kTK - 1) / kTK;
-  const int64_t want = tiles == 0 || tiles > 128 ? 1 : 256 / tiles;
-  const int64_t most = steps / 8 > 1 ? steps / 8 : 1;
-  const int64_t chunks = want < most ? want : most;
-  p.chunk_k = (int)((steps + chunks - 1) / chunks) * kTK;
+  const int64_t n = N - p.big_n, steps = (K + kTK - 1) / kTK;
+  struct { int bm; double one, all; } const kinds[2][3] = {{{32, 0.79, 0.9}, {64, 1.0, 1.15}, {128, 1.07, 1.3}},
+                                                           {{32, 0.36, 0.38}, {64, 0.50, 0.65}, {128, 0.65, 0.95}}};
+  double best = 0.0;
+  for (const auto& k : kinds[aligned]) {
+    const int64_t tiles = (M + k.bm - 1) / k.bm * ((n + 255) / 256);
+    for (int64_t c = 1; c <= 16 && (c == 1 || (c * 2 <= steps && tiles * c <= 512)); c *= 2) {
+      const int64_t blocks = tiles * c, rounds = (blocks + 255) / 256, each = (steps + c - 1) / c;
+      const double load = blocks < 256 ? (double)blocks / 256 : 1.0;
+      const double est = 5.0 + (double)rounds * (double)(each + 2) * (k.one + (k.all - k.one) * load) +
+                         (c > 1 ? 2.0 + (double)c * (double)M * (double)n * 8 / 5e6 : 0.0);
+      if (p.bm == 0 || est < best) {
+        best = est;
+        p.bm = k.bm;
+        p.chunk_k = (int)each * kTK;
+      }
+    }
+  }
   p.chunks = (int)((K + p.chunk_k - 1) / p.chunk_k);
   return p;
 }
@@ -518,19 +541,24 @@ hipError_t launch_tile(TileArgs a, int chunks, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <typename TA, typename TY, int MR>
+// One batch row: a weight row per wave, 8 loads of it in flight (4096 x 4096 fp16: 6.9 us, 4.9 TB/s; 2 rows
+// by 4 loads 7.7, 4 by 4 8.1). Up to 4 batch rows: 2 weight rows per wave halve the reads of X (7.4 us;
+// 1 by 8 9.3), where that leaves enough waves.
+template <typename TA, typename TY>
 hipError_t launch_rows(const TileArgs& a, hipStream_t s) {
-  if (a.N >= 4096)
-    linear_rows_kernel<TA, TY, MR, 4, 4><<<dim3((uint32_t)((a.N + 15) / 16)), 256, 0, s>>>(a);
+  const dim3 ones((uint32_t)((a.N + 3) / 4)), twos((uint32_t)((a.N + 7) / 8));
+  if (a.M == 1)
+    linear_rows_kernel<TA, TY, 1, 1, 8><<<ones, 256, 0, s>>>(a);
+  else if (a.N < 2048)
+    linear_rows_kernel<TA, TY, 4, 1, 8><<<ones, 256, 0, s>>>(a);
   else
-    linear_rows_kernel<TA, TY, MR, 1, 8><<<dim3((uint32_t)((a.N + 3) / 4)), 256, 0, s>>>(a);
+    linear_rows_kernel<TA, TY, 4, 2, 4><<<twos, 256, 0, s>>>(a);
   return hipGetLastError();
 }
 
 template <typename TA, typename TY>
 hipError_t launch_product(TileArgs a, void* ws, hipStream_t s) {
-  if (a.M == 1) return launch_rows<TA, TY, 1>(a, s);
-  if (a.M <= 4) return launch_rows<TA, TY, 4>(a, s);
+  if (a.M <= kMaxRows) return launch_rows<TA, TY>(a, s);
   const bool al = tile_aligned(a.X, a.ldx, a.W, a.ldw, a.K);
   const Plan p = plan_tiles(a.M, a.N, a.K, al);
   a.chunk_k = (a.K + kTK - 1) / kTK * kTK;
@@ -572,7 +600,7 @@ int grad_strip(int64_t M, int64_t N) {
 }  // namespace
 
 size_t linear_workspace_bytes(int64_t N, int64_t K, int64_t M) {
-  if (M <= 4) return 0;
+  if (M <= kMaxRows) return 0;
   size_t most = 0;
   for (int al = 0; al < 2; ++al) {
     const Plan p = plan_tiles(M, N, K, al != 0);
