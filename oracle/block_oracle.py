@@ -133,7 +133,8 @@ def resnorm_backward(dX, dS, Y, S, stats, w_pre, w_post=None, b_post=None, gate=
 # ---------------------------------------------------------------------------------------------
 def adamw(p, g, m, v, step: int, lr: float, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, grad_scale=1.0):
     """(p, m, v) after one step."""
-    p, g, m, v = _f(p), _f(g) * grad_scale, _f(m), _f(v)
+    p, g = _f(p), _f(g) * grad_scale
+    m, v = _f(m), _f(v)
     m = beta1 * m + (1.0 - beta1) * g
     v = beta2 * v + (1.0 - beta2) * g * g
     hat = (m / (1.0 - beta1 ** step)) / (np.sqrt(v / (1.0 - beta2 ** step)) + eps)

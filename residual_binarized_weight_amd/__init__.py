@@ -484,10 +484,12 @@ def resnorm_forward(Y: torch.Tensor, R: torch.Tensor | None, w_pre: torch.Tensor
 def resnorm_backward(dX: torch.Tensor | None, dS: torch.Tensor | None, Y: torch.Tensor, S: torch.Tensor,
                      stats: torch.Tensor, w_pre: torch.Tensor | None, w_post=None, b_post=None, gate=None,
                      alpha: float = 1.0, pre: str = "rms", post: str | None = None, bias: bool = False,
-                     dY: torch.Tensor | None = None, dR: torch.Tensor | None = None, ws: torch.Tensor | None = None):
+                     dY: torch.Tensor | None = None, dR: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                     out: dict | None = None):
     """Gradients of resnorm_forward's inputs from those of X (dX) and S (dS; None: zero), in a dict:
     dY, dR, dgate (like the gate), dw_pre, dw_post and, with `bias`, db_pre, db_post (fp32 [D]); None
-    where there is no such input. Other arguments as in the forward call."""
+    where there is no such input. `out` holds buffers for any of the vectors' or the gate's gradients, by
+    these names. Other arguments as in the forward call."""
     M, D = Y.shape
     dev, dt, sdt = Y.device, Y.dtype, S.dtype
     post = post or ("none" if w_post is None else "rms")
@@ -496,13 +498,22 @@ def resnorm_backward(dX: torch.Tensor | None, dS: torch.Tensor | None, Y: torch.
         dY = torch.empty((M, D), dtype=dt, device=dev)
     if dR is None:
         dR = torch.empty((M, D), dtype=sdt, device=dev)
-    # the vectors' gradients lie in one buffer
+    # the vectors' gradients that are not given lie in one buffer
     names = [n for n, there in (("dw_pre", has_pre), ("db_pre", has_pre and bias), ("dw_post", has_post),
                                 ("db_post", has_post and bias), ("dgate", gate is not None and gate.dim() == 1)) if there]
     vec = dict(zip(names, torch.empty((len(names), D), dtype=torch.float32, device=dev).unbind(0))) if names else {}
-    out = {"dY": dY, "dR": dR, "dgate": None, "dw_pre": None, "dw_post": None, "db_pre": None, "db_post": None, **vec}
-    if gate is not None and gate.dim() != 1:
+    given, out = out, {"dY": dY, "dR": dR, "dgate": None, "dw_pre": None, "dw_post": None, "db_pre": None,
+                       "db_post": None, **vec}
+    if gate is not None and gate.dim() != 1 and not (given and "dgate" in given):
         out["dgate"] = torch.empty((M, D), dtype=dt, device=dev)
+    for k, t in (given or {}).items():
+        if k == "dgate" and gate is not None and gate.dim() != 1:
+            _rows(k, t, M, D, dt)
+        elif k not in vec:
+            raise ValueError(f"there is no gradient {k} to write")
+        else:
+            _vec(k, t, D)
+        out[k] = t
     if ws is None:
         ws = torch.empty(_ws_bytes(RB_OP_RESNORM_BACKWARD, D, 1, M), dtype=torch.uint8, device=dev)
     dxp, lddx = _rows("dX", dX, M, D, dt)
@@ -512,11 +523,15 @@ def resnorm_backward(dX: torch.Tensor | None, dS: torch.Tensor | None, Y: torch.
     gp, ldg = _gate_rows(gate, M, D, dt)
     dyp, lddy = _rows("dY", dY, M, D, dt)
     drp, lddr = _rows("dR", dR, M, D, sdt)
-    dg = out["dgate"]
+    dg, lddg = out["dgate"], D
+    if dg is not None and dg.dim() == 2:
+        dg, lddg = _rows("dgate", dg, M, D, dt)
+    else:
+        dg = _ptr(dg)
     check("rb_resnorm_backward", lib.rb_resnorm_backward(
         dxp, _dt(dt), M, D, lddx, dsp, _dt(sdt), ldds, yp, ldy, sp, lds, _vec("stats", stats, 4 * M), gp, ldg, alpha,
         _NORM[post], _vec("w_post", w_post, D), _vec("b_post", b_post, D), _NORM[pre], _vec("w_pre", w_pre, D), dyp,
-        lddy, drp, lddr, _ptr(dg), D, _ptr(out["dw_post"]), _ptr(out["db_post"]), _ptr(out["dw_pre"]),
+        lddy, drp, lddr, dg, lddg, _ptr(out["dw_post"]), _ptr(out["db_post"]), _ptr(out["dw_pre"]),
         _ptr(out["db_pre"]), _ptr(ws), ws.numel(), _stream()))
     return out
 
