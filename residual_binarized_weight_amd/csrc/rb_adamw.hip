@@ -105,11 +105,11 @@ template <> struct Elem4<__hip_bfloat16> {
   }
 };
 
-// 4 elements from e on; those past n read as 0 and are not written
-template <typename T>
+// 4 elements from e on; those past n read as 0 and are not written. FULL: all 4 are there and aligned.
+template <bool FULL, typename T>
 __device__ __forceinline__ float4 get4(const void* base, int64_t e, int64_t n, bool vec) {
   const T* p = static_cast<const T*>(base) + e;
-  if (vec && e + 4 <= n) return Elem4<T>::load(p);
+  if (FULL || (vec && e + 4 <= n)) return Elem4<T>::load(p);
   float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
   if (e < n) r.x = to_f32(p[0]);
   if (e + 1 < n) r.y = to_f32(p[1]);
@@ -117,10 +117,10 @@ __device__ __forceinline__ float4 get4(const void* base, int64_t e, int64_t n, b
   if (e + 3 < n) r.w = to_f32(p[3]);
   return r;
 }
-template <typename T>
+template <bool FULL, typename T>
 __device__ __forceinline__ void put4(void* base, int64_t e, int64_t n, bool vec, float4 v) {
   T* p = static_cast<T*>(base) + e;
-  if (vec && e + 4 <= n) {
+  if (FULL || (vec && e + 4 <= n)) {
     Elem4<T>::store(p, v);
     return;
   }
@@ -129,17 +129,19 @@ __device__ __forceinline__ void put4(void* base, int64_t e, int64_t n, bool vec,
   if (e + 2 < n) p[2] = Elem4<T>::narrow(v.z);
   if (e + 3 < n) p[3] = Elem4<T>::narrow(v.w);
 }
+template <bool FULL>
 __device__ __forceinline__ uint32_t get4_codes(const void* base, int64_t e, int64_t n, bool vec) {
   const uint8_t* p = static_cast<const uint8_t*>(base) + e;
-  if (vec && e + 4 <= n) return *reinterpret_cast<const uint32_t*>(p);
+  if (FULL || (vec && e + 4 <= n)) return *reinterpret_cast<const uint32_t*>(p);
   uint32_t r = 0;
   for (int j = 0; j < 4; ++j)
     if (e + j < n) r |= (uint32_t)p[j] << (8 * j);
   return r;
 }
+template <bool FULL>
 __device__ __forceinline__ void put4_codes(void* base, int64_t e, int64_t n, bool vec, uint32_t c) {
   uint8_t* p = static_cast<uint8_t*>(base) + e;
-  if (vec && e + 4 <= n) {
+  if (FULL || (vec && e + 4 <= n)) {
     *reinterpret_cast<uint32_t*>(p) = c;
     return;
   }
@@ -154,11 +156,9 @@ __device__ __forceinline__ float4 decode4(uint32_t c, float scale) {
   return make_float4(a.x * s, a.y * s, b.x * s, b.y * s);
 }
 
-__device__ __forceinline__ bool finite_f32(float x) { return (__float_as_uint(x) & 0x7fffffffu) < 0x7f800000u; }
-__device__ __forceinline__ uint32_t finite_mag(float x) {
-  const uint32_t a = __float_as_uint(x) & 0x7fffffffu;
-  return a < 0x7f800000u ? a : 0u;
-}
+constexpr uint32_t kInf = 0x7f800000u;
+__device__ __forceinline__ uint32_t mag_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+__device__ __forceinline__ uint32_t finite_mag(float x) { return mag_bits(x) < kInf ? mag_bits(x) : 0u; }
 // largest of the wave's non-negative values (as bits: the order is the same)
 __device__ __forceinline__ uint32_t wave_max_bits(uint32_t v) {
 #define RB_MAX_STEP(ctrl, rows) \
@@ -184,14 +184,36 @@ __device__ __forceinline__ uint32_t scale_bits(uint32_t top) {
 }
 // |x| / scale * 256 as an e4m3 code: times 2^-120 its exponent field is the code's, and the code
 // is the upper bits (numbers below 2^-6 become subnormal in both); 16 random bits over the 20 cut
-// ones decide the rounding
-__device__ __forceinline__ uint32_t encode(float x, float inv, uint32_t rnd16, uint32_t low) {
+// ones decide the rounding. ROOT: a nonzero x takes the smallest code at least.
+// PLAIN: every x of the group is finite and below its scale, so the code is at most 0x78.
+template <bool PLAIN, bool ROOT>
+__device__ __forceinline__ uint32_t encode(float x, float inv, uint32_t rnd16) {
   const float y = (fabsf(x) * inv) * 0x1p-112f;
   uint32_t c = (__float_as_uint(y) + rnd16 * 16u + 8u) >> 20;
-  c = c < low ? low : (c > 0x7eu ? 0x7eu : c);
-  if (x == 0.f) c = 0u;
-  if (!finite_f32(x)) c = 0x7fu;
-  return c | ((__float_as_uint(x) >> 24) & 0x80u);
+  if (ROOT) c = max(c, x != 0.f ? 1u : 0u);
+  if (!PLAIN) {
+    c = c > 0x7eu ? 0x7eu : c;
+    if (mag_bits(x) >= kInf) c = 0x7fu;
+  }
+  return ROOT && PLAIN ? c : c | ((__float_as_uint(x) >> 24) & 0x80u);
+}
+// the codes and scale bits of the lane's 4 values; h0..h3 hold the random bits from bit `shift` on
+template <bool ROOT>
+__device__ __forceinline__ uint32_t encode4(float x, float y, float z, float w, uint32_t h0, uint32_t h1, uint32_t h2,
+                                            uint32_t h3, uint32_t& scale) {
+  constexpr int shift = ROOT ? 16 : 0;
+  const uint32_t top = wave_max_bits(max(max(mag_bits(x), mag_bits(y)), max(mag_bits(z), mag_bits(w))));
+  const auto rnd = [](uint32_t h) { return ROOT ? h >> shift : h & 0xffffu; };
+  if (top < (127u + 126u) << 23) {  // the whole group, so the branch is uniform
+    scale = scale_bits(top);
+    const float inv = __uint_as_float((254u << 23) - scale);
+    return encode<true, ROOT>(x, inv, rnd(h0)) | encode<true, ROOT>(y, inv, rnd(h1)) << 8 |
+           encode<true, ROOT>(z, inv, rnd(h2)) << 16 | encode<true, ROOT>(w, inv, rnd(h3)) << 24;
+  }
+  scale = scale_bits(wave_max_bits(max(max(finite_mag(x), finite_mag(y)), max(finite_mag(z), finite_mag(w)))));
+  const float inv = __uint_as_float((254u << 23) - scale);
+  return encode<false, ROOT>(x, inv, rnd(h0)) | encode<false, ROOT>(y, inv, rnd(h1)) << 8 |
+         encode<false, ROOT>(z, inv, rnd(h2)) << 16 | encode<false, ROOT>(w, inv, rnd(h3)) << 24;
 }
 
 struct Updated {
@@ -212,11 +234,9 @@ __device__ __forceinline__ Updated update(float p, float g, float m, float v, co
   return o;
 }
 
-template <int BITS, typename TP, typename TG>
-__device__ __forceinline__ void chunk_step(const PlanTensor& t, int64_t chunk, const StepArgs& a, float gscale) {
+template <int BITS, typename TP, typename TG, bool FULL>
+__device__ __forceinline__ void wave_step(const PlanTensor& t, int64_t chunk, int wave, int64_t e0, const StepArgs& a, float gscale) {
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int64_t e0 = (chunk - t.first_chunk) * kChunk + wave * kPerWave;
   const bool vec = t.vec != 0;
   const float step_size = a.step_size * t.lr_mult;
   const float decay = 1.f - a.lr * t.lr_mult * t.weight_decay;
@@ -226,16 +246,16 @@ __device__ __forceinline__ void chunk_step(const PlanTensor& t, int64_t chunk, c
 #pragma unroll
   for (int i = 0; i < kGroups; ++i) {
     const int64_t e = e0 + i * kGroup + lane * 4;
-    g[i] = get4<TG>(t.g, e, t.n, vec);
-    p[i] = get4<TP>(t.p, e, t.n, vec);
+    g[i] = get4<FULL, TG>(t.g, e, t.n, vec);
+    p[i] = get4<FULL, TP>(t.p, e, t.n, vec);
     if (BITS == 32) {
-      m[i] = get4<float>(t.m, e, t.n, vec);
-      v[i] = get4<float>(t.v, e, t.n, vec);
+      m[i] = get4<FULL, float>(t.m, e, t.n, vec);
+      v[i] = get4<FULL, float>(t.v, e, t.n, vec);
     } else {
       const int64_t row = (e0 >> 8) + i;
-      const bool live = e0 + i * kGroup < t.n;
-      mc[i] = get4_codes(t.m, e, t.n, vec);
-      vc[i] = get4_codes(t.v, e, t.n, vec);
+      const bool live = FULL || e0 + i * kGroup < t.n;
+      mc[i] = get4_codes<FULL>(t.m, e, t.n, vec);
+      vc[i] = get4_codes<FULL>(t.v, e, t.n, vec);
       ms[i] = live ? t.m_scale[row] : 1.f;
       vs[i] = live ? t.v_scale[row] : 1.f;
     }
@@ -258,30 +278,33 @@ __device__ __forceinline__ void chunk_step(const PlanTensor& t, int64_t chunk, c
     const Updated y = update(p[i].y, g[i].y * gscale, m[i].y, v[i].y, a, step_size, decay);
     const Updated z = update(p[i].z, g[i].z * gscale, m[i].z, v[i].z, a, step_size, decay);
     const Updated w = update(p[i].w, g[i].w * gscale, m[i].w, v[i].w, a, step_size, decay);
-    put4<TP>(t.p, e, t.n, vec, make_float4(x.p, y.p, z.p, w.p));
+    put4<FULL, TP>(t.p, e, t.n, vec, make_float4(x.p, y.p, z.p, w.p));
     if (BITS == 32) {
-      put4<float>(t.m, e, t.n, vec, make_float4(x.m, y.m, z.m, w.m));
-      put4<float>(t.v, e, t.n, vec, make_float4(x.v, y.v, z.v, w.v));
+      put4<FULL, float>(t.m, e, t.n, vec, make_float4(x.m, y.m, z.m, w.m));
+      put4<FULL, float>(t.v, e, t.n, vec, make_float4(x.v, y.v, z.v, w.v));
     } else {
       // elements past n were read as 0 and stay 0: they do not touch the group's scales
-      const uint32_t mtop = max(max(finite_mag(x.m), finite_mag(y.m)), max(finite_mag(z.m), finite_mag(w.m)));
-      const uint32_t vtop = max(max(finite_mag(x.r), finite_mag(y.r)), max(finite_mag(z.r), finite_mag(w.r)));
-      const uint32_t mb = scale_bits(wave_max_bits(mtop)), vb = scale_bits(wave_max_bits(vtop));
-      const float mi = __uint_as_float((254u << 23) - mb), vi = __uint_as_float((254u << 23) - vb);
       const uint32_t h = hash0 + (uint32_t)(i * kGroup + lane * 4);
       const uint32_t h0 = mix32(h), h1 = mix32(h + 1u), h2 = mix32(h + 2u), h3 = mix32(h + 3u);
-      put4_codes(t.m, e, t.n, vec,
-                 encode(x.m, mi, h0 & 0xffffu, 0u) | encode(y.m, mi, h1 & 0xffffu, 0u) << 8 |
-                     encode(z.m, mi, h2 & 0xffffu, 0u) << 16 | encode(w.m, mi, h3 & 0xffffu, 0u) << 24);
-      put4_codes(t.v, e, t.n, vec,
-                 encode(x.r, vi, h0 >> 16, 1u) | encode(y.r, vi, h1 >> 16, 1u) << 8 |
-                     encode(z.r, vi, h2 >> 16, 1u) << 16 | encode(w.r, vi, h3 >> 16, 1u) << 24);
-      if (lane == 0 && e0 + i * kGroup < t.n) {
+      uint32_t mb, vb;
+      put4_codes<FULL>(t.m, e, t.n, vec, encode4<false>(x.m, y.m, z.m, w.m, h0, h1, h2, h3, mb));
+      put4_codes<FULL>(t.v, e, t.n, vec, encode4<true>(x.r, y.r, z.r, w.r, h0, h1, h2, h3, vb));
+      if (lane == 0 && (FULL || e0 + i * kGroup < t.n)) {
         t.m_scale[(e0 >> 8) + i] = __uint_as_float(mb);
         t.v_scale[(e0 >> 8) + i] = __uint_as_float(vb);
       }
     }
   }
+}
+
+template <int BITS, typename TP, typename TG>
+__device__ __forceinline__ void chunk_step(const PlanTensor& t, int64_t chunk, const StepArgs& a, float gscale) {
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int64_t e0 = (chunk - t.first_chunk) * kChunk + wave * kPerWave;
+  if (t.vec && e0 + kPerWave <= t.n)  // all of the wave's elements, without a check at each
+    wave_step<BITS, TP, TG, true>(t, chunk, wave, e0, a, gscale);
+  else
+    wave_step<BITS, TP, TG, false>(t, chunk, wave, e0, a, gscale);
 }
 
 template <int BITS>
