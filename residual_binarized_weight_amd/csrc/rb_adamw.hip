@@ -71,9 +71,18 @@ __host__ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
 }
 
 template <typename T> struct Elem4;
+// 16-byte accesses marked as streamed (non-temporal): each byte passes once a step, and a step over 45 M
+// elements takes 207 us with the mark and 235 without (8-bit states: 115 / 139). Only one whose tensors fit
+// the 256 MB cache and are touched by nothing else between two steps loses (8.4 M: 40 / 36 us).
+typedef float f4 __attribute__((ext_vector_type(4)));
 template <> struct Elem4<float> {
-  __device__ static __forceinline__ float4 load(const float* p) { return *reinterpret_cast<const float4*>(p); }
-  __device__ static __forceinline__ void store(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+  __device__ static __forceinline__ float4 load(const float* p) {
+    const f4 r = __builtin_nontemporal_load(reinterpret_cast<const f4*>(p));
+    return make_float4(r[0], r[1], r[2], r[3]);
+  }
+  __device__ static __forceinline__ void store(float* p, float4 v) {
+    __builtin_nontemporal_store((f4){v.x, v.y, v.z, v.w}, reinterpret_cast<f4*>(p));
+  }
   __device__ static __forceinline__ float narrow(float v) { return v; }
 };
 template <> struct Elem4<__half> {

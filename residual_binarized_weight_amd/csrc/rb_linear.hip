@@ -14,6 +14,7 @@
 namespace rb {
 namespace {
 
+
 typedef _Float16 l_h8 __attribute__((ext_vector_type(8)));
 typedef __bf16 l_b8 __attribute__((ext_vector_type(8)));
 typedef float l_f4 __attribute__((ext_vector_type(4)));
@@ -78,7 +79,7 @@ __device__ __forceinline__ void finish8(const Epilogue& e, float (&v)[8], int64_
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] += b[j];
   }
-  if (e.Z) store8<TA>(static_cast<TA*>(e.Z) + m * e.ldz, n, N, v);
+  if (e.Z) store8<TA, true>(static_cast<TA*>(e.Z) + m * e.ldz, n, N, v);
   if (e.act != RB_ACT_NONE) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = act_value(v[j], e.act);
@@ -89,7 +90,7 @@ __device__ __forceinline__ void finish8(const Epilogue& e, float (&v)[8], int64_
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] += r[j];
   }
-  store8<TY>(static_cast<TY*>(e.Y) + m * e.ldy, n, N, v);
+  store8<TY, true>(static_cast<TY*>(e.Y) + m * e.ldy, n, N, v);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -98,9 +99,6 @@ __device__ __forceinline__ void finish8(const Epilogue& e, float (&v)[8], int64_
 // 16 bytes per lane from the buffer to LDS (lane l's at base + 16 l)
 __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t r, uint8_t* base, uint32_t voff, int soff) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (l_lds_void*)base, 16, voff, soff, 0, 0);
-}
-__device__ __forceinline__ l_u4 load_16(__amdgpu_buffer_rsrc_t r, uint32_t voff, int soff) {
-  return __builtin_amdgcn_raw_buffer_load_b128(r, (int)voff, soff, 0);
 }
 
 constexpr int kTK = 64;            // columns per step
@@ -231,7 +229,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void linear_tile_kernel(TileArgs a
 #pragma unroll
       for (int j = 0; j < TN; ++j) acc[i][j] = mfma(TA(0), wf[kh][j], xf[kh][i], acc[i][j]);
   };
-  constexpr int kR = TM + TN, kM = TM * TN;
+  constexpr int kR = TM + TN;
   const auto barrier = [] {  // the raw barrier: __syncthreads would also wait for every load in flight
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
@@ -439,7 +437,7 @@ __global__ __launch_bounds__(256) void linear_grad_kernel(GradArgs a) {
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum[j] += d[j];
-    if (a.dZ) store8<TA>(static_cast<TA*>(a.dZ) + m * a.lddz, n, a.N, d);
+    if (a.dZ) store8<TA, true>(static_cast<TA*>(a.dZ) + m * a.lddz, n, a.N, d);
   }
   if (!a.part) return;
   if (w > 0) {

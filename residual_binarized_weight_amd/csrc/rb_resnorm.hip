@@ -16,6 +16,7 @@
 namespace rb {
 namespace {
 
+
 // 8 columns from c of a row of n (0: of a row that is not there) into r; what lies past its end
 // becomes 0. LONG: rows of 8 columns and more, without element loads.
 template <bool LONG, typename T>
@@ -179,14 +180,14 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void resnorm_forward_kernel(
 #pragma unroll
       for (int j = 0; j < 8; ++j) u[i][j] += a.alpha * r[i][j];
     }
-    if (a.S) store8<TS>(static_cast<TS*>(a.S) + row * a.lds, c, D, u[i]);
+    if (a.S) store8<TS, true>(static_cast<TS*>(a.S) + row * a.lds, c, D, u[i]);
   }
   if (a.pre != RB_NORM_NONE) {
     // columns past D hold 0: an absent load gives 0 for every operand above
     row_stats<TPR, NV>(u, c0, a.D, a.pre, a.eps, slots[2], slots[3], mu1, rs1);
     apply_norm<LONG, TPR, NV>(u, c0, D, mu1, rs1, a.w_pre, a.b_pre);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) store8<TA>(static_cast<TA*>(a.X) + row * a.ldx, c0 + i * TPR * 8, D, u[i]);
+    for (int i = 0; i < NV; ++i) store8<TA, true>(static_cast<TA*>(a.X) + row * a.ldx, c0 + i * TPR * 8, D, u[i]);
   }
   if (a.stats && live && t == 0) {
     float* st = a.stats + row * 4;
@@ -368,7 +369,7 @@ __global__ __launch_bounds__(bwd_threads(TPR)) void resnorm_backward_kernel(
         float dr[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) dr[j] = a.alpha * T[i][j];
-        store8<TS>(static_cast<TS*>(a.dR) + row * a.lddr, c, D, dr);
+        store8<TS, true>(static_cast<TS*>(a.dR) + row * a.lddr, c, D, dr);
       }
       widen8<TA>(q.y[i], yh[i]);
       if (post) {
@@ -384,7 +385,7 @@ __global__ __launch_bounds__(bwd_threads(TPR)) void resnorm_backward_kernel(
           dg[j] = u * T[i][j];
         }
         if (a.ldg) {
-          if (a.dgate) store8<TA>(static_cast<TA*>(a.dgate) + row * a.lddg, c, D, dg);
+          if (a.dgate) store8<TA, true>(static_cast<TA*>(a.dgate) + row * a.lddg, c, D, dg);
 #pragma unroll
           for (int j = 0; j < 8; ++j) T[i][j] *= Vec8<TA>::get(q.g[i], j);
         } else {
@@ -417,7 +418,7 @@ __global__ __launch_bounds__(bwd_threads(TPR)) void resnorm_backward_kernel(
         for (int j = 0; j < 8; ++j) e[i][j] = fmaf(-yh[i][j], c2, fmaf(e[i][j], rs0, c1));
     }
 #pragma unroll
-    for (int i = 0; i < NV; ++i) store8<TA>(static_cast<TA*>(a.dY) + row * a.lddy, c0 + i * TPR * 8, D, e[i]);
+    for (int i = 0; i < NV; ++i) store8<TA, true>(static_cast<TA*>(a.dY) + row * a.lddy, c0 + i * TPR * 8, D, e[i]);
   };
   // The next row's loads: with registers for two rows issued before this row is begun, otherwise as soon
   // as this row's values are used up. Group 0 has the block's lowest row: while that is live, all groups
