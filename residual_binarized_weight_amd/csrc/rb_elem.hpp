@@ -109,6 +109,15 @@ template <typename T>
 __device__ __forceinline__ void load8_long(typename Vec8<T>::Raw& r, const T* row, int c, int n) {
   if (c < n) r = *reinterpret_cast<const typename Vec8<T>::Raw*>(row + (c + 8 <= n ? c : n - 8));
 }
+// load8 for a uniform n: one wide load where n is 8 or more (an element load would hold up the wave)
+template <typename T>
+__device__ __forceinline__ typename Vec8<T>::Raw load8_any(const T* row, int c, int n) {
+  if (n < 8) return load8<T>(row, c, n);
+  typename Vec8<T>::Raw r = {};
+  load8_long<T>(r, row, c, n);
+  if (c < n && c + 8 > n) shift_down(r, c + 8 - n);
+  return r;
+}
 template <typename T, bool NT = false>
 __device__ __forceinline__ void store8(T* row, int c, int n, const float (&v)[8]) {
   if (c + 8 <= n) {

@@ -75,7 +75,7 @@ template <typename TA, typename TY>
 __device__ __forceinline__ void finish8(const Epilogue& e, float (&v)[8], int64_t m, int n, int N) {
   if (e.bias) {
     float b[8];
-    widen8<float>(load8<float>(e.bias, n, N), b);
+    widen8<float>(load8_any<float>(e.bias, n, N), b);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] += b[j];
   }
@@ -86,7 +86,7 @@ __device__ __forceinline__ void finish8(const Epilogue& e, float (&v)[8], int64_
   }
   if (e.R) {
     float r[8];
-    widen8<TY>(load8<TY>(static_cast<const TY*>(e.R) + m * e.ldr, n, N), r);
+    widen8<TY>(load8_any<TY>(static_cast<const TY*>(e.R) + m * e.ldr, n, N), r);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] += r[j];
   }
@@ -130,8 +130,8 @@ struct TileArgs {
 //
 // AL: rows of both operands are 16-byte aligned and K is a multiple of 8: the rows go to LDS directly
 // (buffer loads, out of range past a tile's rows and past the columns, where they give 0). Otherwise
-// they pass through registers one step ahead, by 16-byte loads at any address, and the step that holds
-// the end of the columns is read element by element.
+// they pass through registers one step ahead, by 16-byte loads at any address; the vector that holds the
+// end of the columns is read 8 columns before it and shifted.
 template <typename TA, typename TY, int WM, int WN, int TM, int TN, int kS, bool AL>
 __global__ __launch_bounds__(64 * WM * WN, 2) void linear_tile_kernel(TileArgs a) {
   constexpr int kWaves = WM * WN;
@@ -188,18 +188,27 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void linear_tile_kernel(TileArgs a
       load_to_lds(i < kPerX ? rx : rw, base + (i * kWaves + w) * 1024, ok ? off[i] : kOob, k0 * 2);
   };
   l_u4 hold[kPer];
-  const auto fetch = [&](int s) {
+  const auto fetch = [&](int s, l_u4 (&hold)[kPer]) {
     const int k0 = kb + s * kTK, c = k0 + 8 * xc;
     if (k0 + kTK <= ke) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
         hold[i] = __builtin_bit_cast(l_u4, *reinterpret_cast<const typename Vec8<TA>::Raw*>(row[i] + c));
+    } else if (ke >= 8) {
+      typename Vec8<TA>::Raw r[kPer] = {};
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) load8_long<TA>(r[i], row[i], c, ke);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        if (c < ke && c + 8 > ke) shift_down(r[i], 8 - ke % 8);
+        hold[i] = __builtin_bit_cast(l_u4, r[i]);
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < kPer; ++i) hold[i] = __builtin_bit_cast(l_u4, load8<TA>(row[i], c, ke));
     }
   };
-  const auto put = [&](int stage) {
+  const auto put = [&](int stage, const l_u4 (&hold)[kPer]) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
       *reinterpret_cast<l_u4*>(l_smem + stage * kStage + (i * kWaves + w) * 1024 + lane * 16) = hold[i];
@@ -242,11 +251,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void linear_tile_kernel(TileArgs a
     for (int s = 0; s < kS; ++s) dma(s, s);
     __builtin_amdgcn_s_waitcnt(wait_vmcnt((kS - 1) * kPer));
   } else {
-    fetch(0);
-    put(0);
-    fetch(1);
-    put(1);
-    fetch(2);
+    l_u4 second[kPer];
+    fetch(0, hold);
+    fetch(1, second);
+    put(0, hold);
+    put(1, second);
+    fetch(2, hold);
     __builtin_amdgcn_s_waitcnt(kWaitLds);
   }
   barrier();
@@ -269,8 +279,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void linear_tile_kernel(TileArgs a
     if constexpr (AL) {
       dma(s + kS, st);
     } else {
-      put(st);
-      fetch(s + 3);
+      put(st, hold);
+      fetch(s + 3, hold);
     }
     __builtin_amdgcn_sched_barrier(0);
     read(0, next);
@@ -335,10 +345,10 @@ __global__ __launch_bounds__(256) void linear_join_kernel(JoinArgs a) {
   const int64_t m = blockIdx.y;
   if (n >= a.N) return;
   float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
+#pragma unroll 8
   for (int c = 0; c < a.chunks; ++c) {
     float p[8];
-    widen8<float>(load8<float>(a.part + ((int64_t)c * a.M + m) * a.N, n, a.N), p);
+    widen8<float>(load8_any<float>(a.part + ((int64_t)c * a.M + m) * a.N, n, a.N), p);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] += p[j];
   }
@@ -369,14 +379,24 @@ __global__ __launch_bounds__(256) void linear_rows_kernel(TileArgs a) {
 #pragma unroll
     for (int r = 0; r < kRows; ++r) sum[m][r] = 0.f;
   for (int k0 = 0; k0 < a.K; k0 += 512 * kSteps) {
-    typename Vec8<TA>::Raw wr[kSteps][kRows], xr[kSteps][MR];
+    typename Vec8<TA>::Raw wr[kSteps][kRows] = {}, xr[kSteps][MR] = {};
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       const int c = k0 + 512 * s + 8 * lane;
 #pragma unroll
-      for (int r = 0; r < kRows; ++r) wr[s][r] = load8<TA>(row[r], c, a.K);
+      for (int r = 0; r < kRows; ++r) load8_long<TA>(wr[s][r], row[r], c, a.K);
 #pragma unroll
-      for (int m = 0; m < MR; ++m) xr[s][m] = load8<TA>(X + (m < a.M ? m : 0) * a.ldx, c, a.K);
+      for (int m = 0; m < MR; ++m) load8_long<TA>(xr[s][m], X + (m < a.M ? m : 0) * a.ldx, c, a.K);
+    }
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const int c = k0 + 512 * s + 8 * lane;
+      if (c < a.K && c + 8 > a.K) {  // the vector at the end of the columns
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) shift_down(wr[s][r], c + 8 - a.K);
+#pragma unroll
+        for (int m = 0; m < MR; ++m) shift_down(xr[s][m], c + 8 - a.K);
+      }
     }
 #pragma unroll
     for (int s = 0; s < kSteps; ++s)
@@ -429,9 +449,9 @@ __global__ __launch_bounds__(256) void linear_grad_kernel(GradArgs a) {
 #pragma unroll 4
   for (int64_t m = r0 + w; m < r1; m += 4) {
     float d[8], z[8];
-    widen8<TY>(load8<TY>(static_cast<const TY*>(a.dY) + m * a.lddy, n, a.N), d);
+    widen8<TY>(load8_any<TY>(static_cast<const TY*>(a.dY) + m * a.lddy, n, a.N), d);
     if (a.act != RB_ACT_NONE) {
-      widen8<TA>(load8<TA>(static_cast<const TA*>(a.Z) + m * a.ldz, n, a.N), z);
+      widen8<TA>(load8_any<TA>(static_cast<const TA*>(a.Z) + m * a.ldz, n, a.N), z);
 #pragma unroll
       for (int j = 0; j < 8; ++j) d[j] *= act_slope(z[j], a.act);
     }
@@ -556,7 +576,7 @@ hipError_t launch_rows(const TileArgs& a, hipStream_t s) {
 
 template <typename TA, typename TY>
 hipError_t launch_product(TileArgs a, void* ws, hipStream_t s) {
-  if (a.M <= kMaxRows) return launch_rows<TA, TY>(a, s);
+  if (a.M <= kMaxRows && a.K >= 8) return launch_rows<TA, TY>(a, s);
   const bool al = tile_aligned(a.X, a.ldx, a.W, a.ldw, a.K);
   const Plan p = plan_tiles(a.M, a.N, a.K, al);
   a.chunk_k = (a.K + kTK - 1) / kTK * kTK;
@@ -598,7 +618,7 @@ int grad_strip(int64_t M, int64_t N) {
 }  // namespace
 
 size_t linear_workspace_bytes(int64_t N, int64_t K, int64_t M) {
-  if (M <= kMaxRows) return 0;
+  if (M <= kMaxRows) return 0;  // fewer than 8 columns are one chunk
   size_t most = 0;
   for (int al = 0; al < 2; ++al) {
     const Plan p = plan_tiles(M, N, K, al != 0);
