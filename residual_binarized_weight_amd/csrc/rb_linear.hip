@@ -7,6 +7,7 @@
 //   linear_tile_kernel    a tile of batch rows by weight rows per block, on the matrix cores
 //   linear_join_kernel    the sums of K chunks, where a tile's columns are split, and the epilogue
 //   linear_rows_kernel    up to 4 batch rows, on the vector units: a wave streams whole weight rows
+//   linear_few_kernel     5 to 16 batch rows, on the matrix cores, a block's waves splitting the columns
 //   linear_grad_kernel    dZ and, per strip of rows, partial column sums; linear_grad_sum_kernel adds them
 #include "rb_elem.hpp"
 #include "rb_internal.h"
@@ -428,6 +429,65 @@ __global__ __launch_bounds__(256) void linear_rows_kernel(TileArgs a) {
 }
 
 // ---------------------------------------------------------------------------------------------
+// 5 to 16 batch rows: one launch on the matrix cores, without partial sums in memory. A block owns 16 weight
+// rows; its 8 waves take the 64-column steps in turn, each with its fragments straight from memory (a weight
+// element is needed once, X stays in L2), and join in LDS in their order. The fragments' 16-byte pieces cost
+// the address unit a piece each, which bounds the weights' rate near HBM's for one X fragment per weight
+// fragment and below it for two (more than 16 rows).
+// ---------------------------------------------------------------------------------------------
+constexpr int kFewRows = 16;
+
+template <typename TA, typename TY>
+__global__ __launch_bounds__(512) void linear_few_kernel(TileArgs a) {
+  constexpr int kWaves = 8, kAhead = 4;  // steps whose loads a wave has in flight
+  __shared__ __align__(16) float sums[kWaves][256];
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int lr = lane & 15, lj = lane >> 4;
+  const int n0 = blockIdx.x * 16;
+  // rows past the last one repeat it: their outputs are not stored
+  const TA* const wrow = static_cast<const TA*>(a.W) + (int64_t)(n0 + lr < a.N ? n0 + lr : a.N - 1) * a.ldw;
+  const TA* const xrow = static_cast<const TA*>(a.X) + (lr < a.M ? lr : (int)a.M - 1) * a.ldx;
+  l_f4 acc = (l_f4){0.f, 0.f, 0.f, 0.f};
+  for (int k0 = w * kTK; k0 < a.K; k0 += kAhead * kWaves * kTK) {
+    typename Vec8<TA>::Raw wf[kAhead][2] = {}, xf[kAhead][2] = {};
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int c = k0 + s * kWaves * kTK + 32 * h + 8 * lj;
+        load8_long<TA>(wf[s][h], wrow, c, a.K);
+        load8_long<TA>(xf[s][h], xrow, c, a.K);
+      }
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int c = k0 + s * kWaves * kTK + 32 * h + 8 * lj;
+        if (c < a.K && c + 8 > a.K) {  // the vector at the end of the columns
+          shift_down(wf[s][h], c + 8 - a.K);
+          shift_down(xf[s][h], c + 8 - a.K);
+        }
+        acc = mfma(TA(0), __builtin_bit_cast(l_u4, wf[s][h]), __builtin_bit_cast(l_u4, xf[s][h]), acc);
+      }
+  }
+  *reinterpret_cast<l_f4*>(&sums[w][lane * 4]) = acc;
+  __syncthreads();
+  // thread 16 m + n: D's lane 16 (n / 4) + m holds weight row n in element n % 4
+  const int m = threadIdx.x >> 4, nn = threadIdx.x & 15, n = n0 + nn;
+  if (m >= a.M || n >= a.N) return;
+  float v = 0.f;
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) v += sums[i][((nn >> 2) * 16 + m) * 4 + (nn & 3)];
+  const Epilogue& e = a.e;
+  if (e.bias) v += e.bias[n];
+  if (e.Z) static_cast<TA*>(e.Z)[m * e.ldz + n] = Vec8<TA>::narrow(v);
+  if (e.act != RB_ACT_NONE) v = act_value(v, e.act);
+  if (e.R) v += (float)static_cast<const TY*>(e.R)[m * e.ldr + n];
+  static_cast<TY*>(e.Y)[m * e.ldy + n] = Vec8<TY>::narrow(v);
+}
+
+// ---------------------------------------------------------------------------------------------
 // the epilogue's backward: a block owns 512 columns (8 per thread over 64 lanes) and a strip of rows,
 // which its 4 waves take in turn; each thread keeps its columns' sums in fp32
 // ---------------------------------------------------------------------------------------------
@@ -494,6 +554,17 @@ bool tile_aligned(const void* X, int64_t ldx, const void* W, int64_t ldw, int64_
   const auto a16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
   // a tile's rows lie within 2^31 bytes, the out-of-range marker
   return a16(X) && a16(W) && ldx % 8 == 0 && ldw % 8 == 0 && K % 8 == 0 && ldx < (1 << 21) && ldw < (1 << 21);
+}
+
+// The forms without tiles. Up to 4 rows the vector units' products cost nothing beside the weights. Up to 16
+// the one-launch form wins while launches and the join weigh more than its lower rate for the weights (us,
+// one launch / tiles and join: 16 x 4096 x 4096 10.6 / 13.9; 16 x 4096 x 11008 26 / 22.6; unaligned
+// 12 x 1000 x 1411 8.3 / 18, 16 x 4096 x 4096 22.9 / 20.5). Both read 8 columns at least.
+enum class Small { kNone, kRows, kFew };
+Small small_form(int64_t M, int64_t N, int64_t K, bool aligned) {
+  if (K < 8 || M > kFewRows) return Small::kNone;
+  if (M <= kMaxRows) return Small::kRows;
+  return N * K <= (int64_t(1) << (aligned ? 25 : 23)) ? Small::kFew : Small::kNone;
 }
 
 // How a product is laid over the GPU's 256 compute units: `bm` batch rows by 256 weight rows per tile
@@ -576,8 +647,14 @@ hipError_t launch_rows(const TileArgs& a, hipStream_t s) {
 
 template <typename TA, typename TY>
 hipError_t launch_product(TileArgs a, void* ws, hipStream_t s) {
-  if (a.M <= kMaxRows && a.K >= 8) return launch_rows<TA, TY>(a, s);
   const bool al = tile_aligned(a.X, a.ldx, a.W, a.ldw, a.K);
+  switch (small_form(a.M, a.N, a.K, al)) {
+    case Small::kRows: return launch_rows<TA, TY>(a, s);
+    case Small::kFew:
+      linear_few_kernel<TA, TY><<<dim3((uint32_t)((a.N + 15) / 16)), 512, 0, s>>>(a);
+      return hipGetLastError();
+    case Small::kNone: break;
+  }
   const Plan p = plan_tiles(a.M, a.N, a.K, al);
   a.chunk_k = (a.K + kTK - 1) / kTK * kTK;
   if (p.big_n > 0) {
@@ -618,9 +695,9 @@ int grad_strip(int64_t M, int64_t N) {
 }  // namespace
 
 size_t linear_workspace_bytes(int64_t N, int64_t K, int64_t M) {
-  if (M <= kMaxRows) return 0;  // fewer than 8 columns are one chunk
   size_t most = 0;
   for (int al = 0; al < 2; ++al) {
+    if (small_form(M, N, K, al != 0) != Small::kNone) continue;
     const Plan p = plan_tiles(M, N, K, al != 0);
     const size_t b = p.chunks > 1 ? (size_t)p.chunks * (size_t)M * (size_t)(N - p.big_n) * 4 : 0;
     most = b > most ? b : most;

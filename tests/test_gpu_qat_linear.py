@@ -100,12 +100,12 @@ def test_epilogues(act, dt, ydt, bias, res, save_z):
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 4096, 4096), (5, 1000, 9000), (17, 520, 8192), (300, 700, 4100), (1100, 4100, 520),
-                                   (2048, 4096, 1024), (700, 11008, 640)])
+                                   (2048, 4096, 1024), (700, 11008, 640), (7, 4200, 8200)])
 def test_long_and_wide(M, N, K):
     case(6, M, N, K, "bf16", "gelu_tanh", True, True, "f32")
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 2000, 4099), (40, 1500, 3001), (513, 1030, 1027)])
+@pytest.mark.parametrize("M,N,K", [(1, 2000, 4099), (3, 3000, 2049), (9, 3000, 3001), (40, 1500, 3001), (513, 1030, 1027)])
 def test_long_and_wide_unaligned(M, N, K):
     case(7, M, N, K, "f16", "gelu", True, True, "f16", True)
 
