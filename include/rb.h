@@ -446,8 +446,8 @@ rb_status rb_qat_autotune(const void* X, const void* dY, rb_dtype a_dtype, int64
  *   dY       [M][lddy] in dy_dtype, RB_F32 or a_dtype;  Z  [M][ldz] in a_dtype (may be NULL for RB_ACT_NONE)
  *   dZ       [M][lddz] in a_dtype, or NULL with a db; may be dY or Z (same type and leading dimension)
  *   db       fp32 [N] or NULL
- *   ws       rb_workspace_bytes(RB_OP_QAT_LINEAR_BACKWARD, 1, N, 1, M) bytes, 16-byte aligned (NULL if
- *            db is NULL); no zero-filling needed. */
+ *   ws       rb_workspace_bytes(RB_OP_QAT_LINEAR_BACKWARD, 1, N, 1, M) bytes, 16-byte aligned (NULL if that
+ *            is 0 or db is NULL); no zero-filling needed. */
 typedef enum rb_act { RB_ACT_NONE = 0, RB_ACT_RELU = 1, RB_ACT_GELU = 2, RB_ACT_GELU_TANH = 3, RB_ACT_SILU = 4 } rb_act;
 rb_status rb_qat_linear(const void* X, rb_dtype a_dtype, int64_t M, int64_t ldx, const void* What, int64_t ldwh,
                         int64_t N, int64_t K, const float* bias, int32_t act, const void* R, int64_t ldr, void* Z,

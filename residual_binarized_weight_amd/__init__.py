@@ -429,8 +429,9 @@ def qat_linear_backward(dY: torch.Tensor, Z: torch.Tensor | None, act: str = "no
         db = None
     elif db is None:
         db = torch.empty(N, dtype=torch.float32, device=dY.device)
-    if ws is None and bias:
-        ws = torch.empty(_ws_bytes(RB_OP_QAT_LINEAR_BACKWARD, N, 1, M), dtype=torch.uint8, device=dY.device)
+    n = _ws_bytes(RB_OP_QAT_LINEAR_BACKWARD, N, 1, M)
+    if ws is None and bias and n:
+        ws = torch.empty(n, dtype=torch.uint8, device=dY.device)
     dyp, lddy = _rows("dY", dY, M, N, dY.dtype)
     zp, ldz = _rows("Z", Z, M, N, dt)
     dzp, lddz = _rows("dZ", dZ, M, N, dt)

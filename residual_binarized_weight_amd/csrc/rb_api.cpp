@@ -110,8 +110,11 @@ size_t rb_workspace_bytes(rb_op op, int32_t k, int64_t N, int64_t K, int64_t M) 
       const size_t p = rb::linear_workspace_bytes(N, K, M);
       return p > 0 ? rb::zero_region_bytes(N) + p : 0;
     }
-    case RB_OP_QAT_LINEAR_BACKWARD:
-      return (N > kQatMaxDim || M > kMaxDim) ? 0 : rb::zero_region_bytes(N) + rb::linear_backward_workspace_bytes(N, M);
+    case RB_OP_QAT_LINEAR_BACKWARD: {
+      if (N > kQatMaxDim || M > kMaxDim) return 0;
+      const size_t p = rb::linear_backward_workspace_bytes(N, M);
+      return p > 0 ? rb::zero_region_bytes(N) + p : 0;
+    }
     default: return 0;
   }
 }
@@ -470,12 +473,12 @@ rb_status rb_qat_linear_backward(const void* dY, rb_dtype dy_dtype, int64_t M, i
   if (!act_dtype(a_dtype) || (dy_dtype != RB_F32 && dy_dtype != a_dtype)) return RB_ERR_UNSUPPORTED;
   if (!elem_aligned(dY, dy_dtype) || !elem_aligned(Z, a_dtype) || !elem_aligned(dZ, a_dtype) || !aligned(db, 4))
     return RB_ERR_MISALIGNED;
-  const size_t need = rb::zero_region_bytes(N) + rb::linear_backward_workspace_bytes(N, M);
-  if (db && (!ws || ws_bytes < need)) return RB_ERR_WORKSPACE;
+  const size_t part = db ? rb::linear_backward_workspace_bytes(N, M) : 0;
+  if (part > 0 && (!ws || ws_bytes < rb::zero_region_bytes(N) + part)) return RB_ERR_WORKSPACE;
   if (!aligned(ws, 16)) return RB_ERR_MISALIGNED;
   log_call("rb_qat_linear_backward", N, 0, M, act);
   return from_hip(rb::launch_linear_backward(dY, dy_dtype, M, N, lddy, Z, a_dtype, ldz, act, dZ, lddz, db,
-                                             db ? static_cast<char*>(ws) + rb::zero_region_bytes(N) : nullptr,
+                                             part > 0 ? static_cast<char*>(ws) + rb::zero_region_bytes(N) : nullptr,
                                              static_cast<hipStream_t>(stream)));
 }
 

@@ -684,11 +684,13 @@ hipError_t launch_product(TileArgs a, void* ws, hipStream_t s) {
   return hipGetLastError();
 }
 
-// strips of rows: enough blocks to fill the GPU, few enough partial sums
+// Strips of rows: enough blocks to fill the GPU, few enough partial sums. Up to 8 rows (2 per wave) are one
+// strip, whose sums are db itself: 4 x 4096 2.9 us against 4.9 with a second launch, but 16 x 4096 6.0
+// against 5.0.
 int grad_strip(int64_t M, int64_t N) {
+  if (M <= 8) return 8;
   const int64_t cols = (N + 511) / 512, want = (1024 + cols - 1) / cols;
-  int64_t strip = (M + want - 1) / want;
-  strip = (strip + 3) / 4 * 4;
+  const int64_t strip = ((M + want - 1) / want + 3) / 4 * 4;
   return (int)(strip < 4 ? 4 : strip);
 }
 
@@ -716,7 +718,7 @@ hipError_t launch_linear(const void* X, rb_dtype a_dtype, int64_t M, int64_t ldx
 
 size_t linear_backward_workspace_bytes(int64_t N, int64_t M) {
   const int strip = grad_strip(M, N);
-  return (size_t)((M + strip - 1) / strip) * (size_t)N * 4;
+  return M <= strip ? 0 : (size_t)((M + strip - 1) / strip) * (size_t)N * 4;
 }
 
 hipError_t launch_linear_backward(const void* dY, rb_dtype dy_dtype, int64_t M, int64_t N, int64_t lddy, const void* Z,
@@ -724,7 +726,7 @@ hipError_t launch_linear_backward(const void* dY, rb_dtype dy_dtype, int64_t M, 
                                   hipStream_t s) {
   const int strip = grad_strip(M, N);
   const int strips = (int)((M + strip - 1) / strip);
-  const GradArgs a{dY, Z, dZ, db ? static_cast<float*>(ws) : nullptr, M, lddy, ldz, lddz, (int)N, act, strip};
+  const GradArgs a{dY, Z, dZ, !db ? nullptr : strips == 1 ? db : static_cast<float*>(ws), M, lddy, ldz, lddz, (int)N, act, strip};
   const dim3 grid((uint32_t)((N + 511) / 512), (uint32_t)strips);
   if (a_dtype == RB_F16) {
     if (dy_dtype == RB_F32)
@@ -737,7 +739,7 @@ hipError_t launch_linear_backward(const void* dY, rb_dtype dy_dtype, int64_t M, 
     linear_grad_kernel<__bf16, __bf16><<<grid, 256, 0, s>>>(a);
   }
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !db) return e;
+  if (e != hipSuccess || !db || strips == 1) return e;
   linear_grad_sum_kernel<<<dim3((uint32_t)((N + 63) / 64)), 512, 0, s>>>(a.part, strips, (int)N, db);
   return hipGetLastError();
 }

@@ -49,7 +49,7 @@ def test_linear_rejects(kw, status):
 
 
 def linear_backward(**kw):
-    a = dict(dY=P, dydt=F32, M=4, N=64, lddy=64, Z=P, dt=BF16, ldz=64, act=4, dZ=P, lddz=64, db=P, ws=P, wsb=1 << 40)
+    a = dict(dY=P, dydt=F32, M=400, N=64, lddy=64, Z=P, dt=BF16, ldz=64, act=4, dZ=P, lddz=64, db=P, ws=P, wsb=1 << 40)
     a.update(kw)
     return L.rb_qat_linear_backward(a["dY"], a["dydt"], a["M"], a["N"], a["lddy"], a["Z"], a["dt"], a["ldz"], a["act"],
                                     a["dZ"], a["lddz"], a["db"], a["ws"], a["wsb"], None)
@@ -187,7 +187,9 @@ def test_workspace_sizes():
     assert ws(_lib.RB_OP_RESNORM_BACKWARD, 4096, 1, 2048) == zero(4096) + 5 * 256 * 4096 * 4
     assert ws(_lib.RB_OP_RESNORM_BACKWARD, 4096, 1, 3) == zero(4096) + 5 * 3 * 4096 * 4
     assert ws(_lib.RB_OP_RESNORM_BACKWARD, 16385, 1, 3) == 0
-    assert ws(_lib.RB_OP_QAT_LINEAR_BACKWARD, 512, 1, 4) == zero(512) + 512 * 4
+    assert ws(_lib.RB_OP_QAT_LINEAR_BACKWARD, 512, 1, 8) == 0       # one strip: its sums are db
+    got = ws(_lib.RB_OP_QAT_LINEAR_BACKWARD, 512, 1, 9) - zero(512)
+    assert got > 0 and got % (512 * 4) == 0
 
 
 # ---------------------------------------------------------------------------------------------
