@@ -114,7 +114,7 @@ def pack(W: torch.Tensor, k: int, h: torch.Tensor | None = None, group: int = 0,
     if planes is None:
         planes = torch.zeros((k, N, ldp), dtype=torch.int32, device=W.device)
     shape = (k, N) if group == 0 else (k, N, (K + group - 1) // group)
-    g = torch.empty((M, D), dtype=scale_dtype, device=W.device)
+    g = torch.empty(shape, dtype=scale_dtype, device=W.device)
     check("rb_pack", lib.rb_pack(_ptr(W), _dt(W.dtype), N, K, W.stride(0), k, group, _ptr(h),
                                  _dt(scale_dtype), _ptr(planes), ldp, _ptr(g), _ptr(d_status),
                                  _stream()))
