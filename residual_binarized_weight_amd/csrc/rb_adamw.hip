@@ -4,7 +4,9 @@
 //   p <- p (1 - lr wd) - lr / (1 - b1^t) * m / (r / sqrt(1 - b2^t) + eps)
 //
 // Every element is read and written once, so the step is bound by HBM: 28 bytes per element with
-// fp32 parameters, gradients and states, 16 with 8-bit states.
+// fp32 parameters, gradients and states, 16 with 8-bit states. Measured over three 4096 x 11008
+// weights and their scales (135 M elements): 619 us = 6.1 TB/s in 32 bits, 359 us = 6.1 TB/s in 8.
+// 256 x 512 with its scales: 6.2 us, a launch and one element's chain of operations.
 //
 // Split. Tensors are cut into chunks of 4096 elements; a map of the chunks (one 32-bit tensor
 // number each, 1/4000 of the traffic) lets one launch serve a 4096 x 11008 weight and its 4096

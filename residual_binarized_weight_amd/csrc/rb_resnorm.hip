@@ -9,13 +9,16 @@
 // consecutive columns each (16-byte accesses), and its two norms are reduced there one after the
 // other: by DPP inside a wave, through LDS between waves. All sums are fp32; the mean is taken
 // before the squares, so a large mean costs no digits.
+//
+// Measured (bf16, fp32 stream, rms norms, a gate per channel): forward 2048 x 4096 18 to 19 us, 101 MB
+// = 5.3 TB/s, about what a copy reaches; one row 3 us. Stores are streamed (nothing here reads them
+// again): 23.7 us without.
 #include "rb_elem.hpp"
 #include "rb_internal.h"
 #include <type_traits>
 
 namespace rb {
 namespace {
-
 
 // 8 columns from c of a row of n (0: of a row that is not there) into r; what lies past its end
 // becomes 0. LONG: rows of 8 columns and more, without element loads.
@@ -202,6 +205,12 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void resnorm_forward_kernel(
 // A block walks over rows and keeps the column sums of its rows in registers; at the end its row
 // groups are joined through LDS and the block's sums go to the workspace, where a second kernel
 // adds them over the blocks in a fixed order.
+//
+// Measured, bf16 with an fp32 stream, rms norms and a gate per channel, 2048 x 4096: 36 us and 4 for
+// the sums, 151 MB = 4.2 TB/s; a row's loads wait while the row before it is reduced, and only the next
+// row's are in flight. 1537 x 8191 in bf16, layer norms and a gate per element: 71 us and 8.6, 202 MB =
+// 2.8 TB/s; 1024 threads leave 128 registers each, which do not hold a second row. One block per compute
+// unit: with two (512 blocks) the first takes 43 us and the sums 6.6.
 // ---------------------------------------------------------------------------------------------
 struct BwdArgs {
   const void *dX, *dS, *Y, *S, *gate;
