@@ -187,6 +187,8 @@ def test_workspace_sizes():
     assert ws(_lib.RB_OP_RESNORM_BACKWARD, 4096, 1, 2048) == zero(4096) + 5 * 256 * 4096 * 4
     assert ws(_lib.RB_OP_RESNORM_BACKWARD, 4096, 1, 3) == zero(4096) + 5 * 3 * 4096 * 4
     assert ws(_lib.RB_OP_RESNORM_BACKWARD, 16385, 1, 3) == 0
+    for M, strips in ((1, 1), (5, 2), (256, 64), (257, 52), (2048, 64)):    # past 8192 columns: strips, and the rows' means
+        assert ws(_lib.RB_OP_RESNORM_BACKWARD, 9000, 1, M) == zero(9000) + 5 * strips * 9000 * 4 + 16 * M
     assert ws(_lib.RB_OP_QAT_LINEAR_BACKWARD, 512, 1, 8) == 0       # one strip: its sums are db
     got = ws(_lib.RB_OP_QAT_LINEAR_BACKWARD, 512, 1, 9) - zero(512)
     assert got > 0 and got % (512 * 4) == 0

@@ -239,6 +239,30 @@ def test_backward_rows(M, D):
     run_backward(80, M, D, "bf16", "f32", "rms", "rms", "channel", False)
 
 
+@pytest.mark.parametrize("M", [1, 65, 260, 301])
+@pytest.mark.parametrize("D", [8193, 8705, 9001])
+def test_backward_wide_rows(M, D):
+    """Rows that no block holds: strips of 4 and 5 rows, a last strip with fewer, last columns of 1 to 7."""
+    run_backward(100, M, D, "bf16", "bf16", "layer", "layer", "channel", True)
+
+
+@pytest.mark.parametrize("dt,sdt", [("bf16", "f32"), ("f16", "f16"), ("f32", "f32")])
+@pytest.mark.parametrize("post,pre", [("none", "rms"), ("rms", "none"), ("layer", "rms"), ("none", "none")])
+@pytest.mark.parametrize("gate", ["none", "channel", "element"])
+def test_backward_wide_kinds(dt, sdt, post, pre, gate):
+    run_backward(101, 6, 8300, dt, sdt, post, pre, gate, gate == "element", ld=8311, off=3, with_ds=gate != "none")
+
+
+def test_backward_wide_in_place_and_deterministic():
+    a, dX, dS, S, st, got = run_backward(102, 70, 8705, "bf16", "bf16", "rms", "layer", "channel", False)
+    kw = dict(w_post=a["w_post"], gate=a["gate"], alpha=a["alpha"], pre="layer", post="rms")
+    for out in ("Y", "dX"):
+        x, y, s = dX.clone(), a["Y"].clone(), dS.clone()
+        again = rb.resnorm_backward(x, s, y, S, st, a["w_pre"], dY=y if out == "Y" else x, dR=s, **kw)
+        torch.cuda.synchronize()
+        assert all(torch.equal(again[k], got[k]) for k in got if got[k] is not None)
+
+
 def test_backward_against_differences():
     """Central differences of L = <X, dX> + <S, dS> in the library's own fp32 forward, along random
     directions of every input: their truncation error is h^2 and their rounding 1e-6 / h of |L|'s terms."""
