@@ -7,7 +7,8 @@
 //   linear_tile_kernel    a tile of batch rows by weight rows per block, on the matrix cores
 //   linear_join_kernel    the sums of K chunks, where a tile's columns are split, and the epilogue
 //   linear_rows_kernel    up to 4 batch rows, on the vector units: a wave streams whole weight rows
-//   linear_few_kernel     5 to 16 batch rows, on the matrix cores, a block's waves splitting the columns
+//   linear_few_kernel     small products of 5 to 256 batch rows, on the matrix cores, a block's waves splitting
+//                         the columns
 //   linear_grad_kernel    dZ and, per strip of rows, partial column sums; linear_grad_sum_kernel adds them
 #include "rb_elem.hpp"
 #include "rb_internal.h"
@@ -435,13 +436,13 @@ __global__ __launch_bounds__(256) void linear_rows_kernel(TileArgs a) {
 }
 
 // ---------------------------------------------------------------------------------------------
-// 5 to 16 batch rows: one launch on the matrix cores, without partial sums in memory. A block owns 16 weight
-// rows; its 8 waves take the 64-column steps in turn, each with its fragments straight from memory (a weight
-// element is needed once, X stays in L2), and join in LDS in their order. The fragments' 16-byte pieces cost
-// the address unit a piece each, which bounds the weights' rate near HBM's for one X fragment per weight
-// fragment and below it for two (more than 16 rows).
+// Small products of 5 to 256 batch rows: one launch on the matrix cores, without partial sums in memory. A
+// block owns 16 weight rows by 16 batch rows; its 8 waves take the 64-column steps in turn, each with its
+// fragments straight from memory, and join in LDS in their order. The fragments' 16-byte pieces cost the
+// address unit a piece each, which bounds the rate: 0.11 us a step for the 256 units at once (4096 columns
+// 7.1 us), 0.3 where rows are not 16-byte aligned.
 // ---------------------------------------------------------------------------------------------
-constexpr int kFewRows = 16;
+constexpr int kFewRows = 256;
 
 template <typename TA, typename TY>
 __global__ __launch_bounds__(512) void linear_few_kernel(TileArgs a) {
@@ -453,7 +454,8 @@ __global__ __launch_bounds__(512) void linear_few_kernel(TileArgs a) {
   const int n0 = blockIdx.x * 16;
   // rows past the last one repeat it: their outputs are not stored
   const TA* const wrow = static_cast<const TA*>(a.W) + (int64_t)(n0 + lr < a.N ? n0 + lr : a.N - 1) * a.ldw;
-  const TA* const xrow = static_cast<const TA*>(a.X) + (lr < a.M ? lr : (int)a.M - 1) * a.ldx;
+  const int64_t m0 = (int64_t)blockIdx.y * 16;
+  const TA* const xrow = static_cast<const TA*>(a.X) + (m0 + lr < a.M ? m0 + lr : a.M - 1) * a.ldx;
   l_f4 acc = (l_f4){0.f, 0.f, 0.f, 0.f};
   for (int k0 = w * kTK; k0 < a.K; k0 += kAhead * kWaves * kTK) {
     typename Vec8<TA>::Raw wf[kAhead][2] = {}, xf[kAhead][2] = {};
@@ -480,11 +482,13 @@ __global__ __launch_bounds__(512) void linear_few_kernel(TileArgs a) {
   *reinterpret_cast<l_f4*>(&sums[w][lane * 4]) = acc;
   __syncthreads();
   // thread 16 m + n: D's lane 16 (n / 4) + m holds weight row n in element n % 4
-  const int m = threadIdx.x >> 4, nn = threadIdx.x & 15, n = n0 + nn;
+  if (threadIdx.x >= 256) return;
+  const int mm = threadIdx.x >> 4, nn = threadIdx.x & 15, n = n0 + nn;
+  const int64_t m = m0 + mm;
   if (m >= a.M || n >= a.N) return;
   float v = 0.f;
 #pragma unroll
-  for (int i = 0; i < kWaves; ++i) v += sums[i][((nn >> 2) * 16 + m) * 4 + (nn & 3)];
+  for (int i = 0; i < kWaves; ++i) v += sums[i][((nn >> 2) * 16 + mm) * 4 + (nn & 3)];
   const Epilogue& e = a.e;
   if (e.bias) v += e.bias[n];
   if (e.Z) static_cast<TA*>(e.Z)[m * e.ldz + n] = Vec8<TA>::narrow(v);
@@ -563,17 +567,6 @@ bool tile_aligned(const void* X, int64_t ldx, const void* W, int64_t ldw, int64_
   return a16(X) && a16(W) && ldx % 8 == 0 && ldw % 8 == 0 && K % 8 == 0 && ldx < (1 << 21) && ldw < (1 << 21);
 }
 
-// The forms without tiles. Up to 4 rows the vector units' products cost nothing beside the weights. Up to 16
-// the one-launch form wins while launches and the join weigh more than its lower rate for the weights (us,
-// one launch / tiles and join: 16 x 4096 x 4096 10.6 / 13.9; 16 x 4096 x 11008 26 / 22.6; unaligned
-// 12 x 1000 x 1411 8.3 / 18, 16 x 4096 x 4096 22.9 / 20.5). Both read 8 columns at least.
-enum class Small { kNone, kRows, kFew };
-Small small_form(int64_t M, int64_t N, int64_t K, bool aligned) {
-  if (K < 8 || M > kFewRows) return Small::kNone;
-  if (M <= kMaxRows) return Small::kRows;
-  return N * K <= (int64_t(1) << (aligned ? 25 : 23)) ? Small::kFew : Small::kNone;
-}
-
 // How a product is laid over the GPU's 256 compute units: `bm` batch rows by 256 weight rows per tile
 // (32, 64, 128; 256 for the first `big_n` weight rows), the columns in `chunks`.
 //
@@ -589,6 +582,7 @@ Small small_form(int64_t M, int64_t N, int64_t K, bool aligned) {
 // 4096: 28.7 us whole, 14.4 us in 4 chunks).
 struct Plan {
   int bm, chunks, chunk_k, big_n;
+  double est;
 };
 Plan plan_tiles(int64_t M, int64_t N, int64_t K, bool aligned) {
   Plan p{};
@@ -616,7 +610,23 @@ Plan plan_tiles(int64_t M, int64_t N, int64_t K, bool aligned) {
     }
   }
   p.chunks = (int)((K + p.chunk_k - 1) / p.chunk_k);
+  p.est = best;
   return p;
+}
+
+// The forms without tiles; both read 8 columns at least. Up to 4 rows the vector units' products cost nothing
+// beside the weights. The one-launch form on the matrix cores is taken by its estimate against the tiles', up to
+// the 256 rows the estimate was fitted over: it saves the join and the pipeline's ends, and reads each operand
+// once per 16 rows of the other (us, one launch / tiles: 64 x 512 x 512 3.0 / 7.2; 64 x 300 x 520 3.1 / 9.1;
+// 16 x 4096 x 4096 10.6 / 13.9; 64 x 2048 x 2048 9.7 / 10.7; 128 x 2048 x 2048 16.8 / 12.2; rows not aligned: 48 x
+// 1027 x 1411 8.6 / 13.0; 128 x 1027 x 1411 19.6 / 16.1; 20 x 1000 x 4001 21.5 / 12.9).
+enum class Small { kNone, kRows, kFew };
+Small small_form(int64_t M, int64_t N, int64_t K, bool aligned) {
+  if (K < 8 || M > kFewRows) return Small::kNone;
+  if (M <= kMaxRows) return Small::kRows;
+  const int64_t rounds = ((N + 15) / 16 * ((M + 15) / 16) + 255) / 256, steps = (K + kTK - 1) / kTK;
+  const Plan p = plan_tiles(M, N, K, aligned);
+  return p.big_n == 0 && 2.6 + (double)(rounds * steps) * (aligned ? 0.13 : 0.33) < p.est ? Small::kFew : Small::kNone;
 }
 
 template <typename TA, typename TY, int WM, int WN, int TM, int kS, bool AL>
@@ -658,7 +668,7 @@ hipError_t launch_product(TileArgs a, void* ws, hipStream_t s) {
   switch (small_form(a.M, a.N, a.K, al)) {
     case Small::kRows: return launch_rows<TA, TY>(a, s);
     case Small::kFew:
-      linear_few_kernel<TA, TY><<<dim3((uint32_t)((a.N + 15) / 16)), 512, 0, s>>>(a);
+      linear_few_kernel<TA, TY><<<dim3((uint32_t)((a.N + 15) / 16), (uint32_t)((a.M + 15) / 16)), 512, 0, s>>>(a);
       return hipGetLastError();
     case Small::kNone: break;
   }

@@ -99,6 +99,37 @@ def test_epilogues(act, dt, ydt, bias, res, save_z):
     case(5, 37, 2050, 2048, dt, act, bias, res, ydt, save_z)      # split columns: the join's epilogue
 
 
+# the same edges where more rows, or longer ones, bring the tiles
+@pytest.mark.parametrize("M", [257, 271, 288, 321, 400])
+@pytest.mark.parametrize("N,K", [(1, 8), (63, 64), (257, 72), (300, 136), (65, 1000)])
+def test_tile_edges_of_more_rows(M, N, K):
+    case(8, M, N, K, "bf16", bias=True, ydt="f32")
+
+
+@pytest.mark.parametrize("M", [257, 290, 385])
+@pytest.mark.parametrize("N,K", [(1, 1), (5, 3), (64, 63), (258, 129), (100, 997)])
+def test_tile_edges_unaligned_of_more_rows(M, N, K):
+    case(9, M, N, K, "f16", bias=True, ydt="f32")
+
+
+@pytest.mark.parametrize("pad,off", [(8, 0), (8, 8), (3, 0), (1, 5)])
+def test_strides_and_offsets_of_more_rows(pad, off):
+    for K in (200, 2056):
+        case(10, 300, 70, K, "bf16", act="silu", bias=True, res=True, save_z=True, pad=pad, off=off)
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("dt,ydt", [("bf16", "bf16"), ("f16", "f32")])
+def test_epilogues_of_more_rows(act, dt, ydt):
+    case(11, 290, 130, 160, dt, act, True, True, ydt, True)
+    case(12, 60, 1030, 4104, dt, act, True, True, ydt, True)      # split columns: the join's epilogue
+
+
+@pytest.mark.parametrize("M,N,K", [(20, 1030, 8200), (61, 1027, 1411), (100, 2050, 2056), (129, 3000, 1000), (200, 1500, 2049)])
+def test_middle_rows(M, N, K):
+    case(13, M, N, K, "bf16", "gelu", True, True, "bf16", True)
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 4096, 4096), (5, 1000, 9000), (17, 520, 8192), (300, 700, 4100), (1100, 4100, 520),
                                    (2048, 4096, 1024), (700, 11008, 640), (7, 4200, 8200)])
 def test_long_and_wide(M, N, K):
