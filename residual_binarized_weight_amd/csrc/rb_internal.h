@@ -11,6 +11,18 @@ namespace rb {
 
 int device_cu_count();  // compute units of the current device (cached)
 
+// HIP refuses a launch of 2^32 threads or more in one dimension: longer runs of blocks are launched in parts
+// of 2^20 (a part takes milliseconds, so its launch costs nothing). launch(first, blocks) starts one.
+template <typename F>
+hipError_t launch_in_parts(int64_t blocks, F launch) {
+  constexpr int64_t kPart = int64_t(1) << 20;
+  for (int64_t first = 0; first < blocks; first += kPart) {
+    launch(first, (uint32_t)(blocks - first < kPart ? blocks - first : kPart));
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 hipError_t launch_pack(const void* W, rb_dtype w_dtype, int64_t N, int64_t K, int64_t ldw, int k,
                        int group, const void* h, rb_dtype scale_dtype, uint32_t* planes, int64_t ldp,
                        void* g, int32_t* d_status, hipStream_t s);

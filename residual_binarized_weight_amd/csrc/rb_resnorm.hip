@@ -115,6 +115,7 @@ struct FwdArgs {
   int64_t M, ldy, ldr, ldg, lds, ldx;
   int D, post, pre;
   float alpha, eps;
+  int64_t row0;  // the launch's first row
 };
 
 // y = x-hat w + b over the thread's columns
@@ -141,7 +142,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void resnorm_forward_kernel(
   __shared__ float2 slots[4][16];
   const int t = threadIdx.x % TPR;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);  // rows are scalar: so are their addresses
-  const int64_t row = (int64_t)blockIdx.x * kRows + wave / (TPR / 64);
+  const int64_t row = a.row0 + (int64_t)blockIdx.x * kRows + wave / (TPR / 64);
   const bool live = row < a.M;
   const int D = live ? a.D : 0;  // a group past the last row takes part in the barriers only
   const int c0 = t * 8;
@@ -219,6 +220,7 @@ struct BwdArgs {
   int64_t M, lddx, ldds, ldy, lds, ldg, lddy, lddr, lddg;
   int D, post, pre, slot[5];  // slot: a vector's place among the partial sums, -1 where it is not wanted
   float alpha;
+  int64_t row0;           // the means' form only: the launch's first row
 };
 enum { kDwPre, kDbPre, kDwPost, kDbPost, kDgate };
 
@@ -491,7 +493,7 @@ __global__ __launch_bounds__(kWideThreads) void resnorm_backward_means_kernel(Bw
                                                                              const float* __restrict__ w_post,
                                                                              float4* means) {
   __shared__ float2 slots[2][16];
-  const int64_t row = blockIdx.x;
+  const int64_t row = a.row0 + blockIdx.x;
   const float mu0 = stats[row * 4], rs0 = stats[row * 4 + 1], mu1 = stats[row * 4 + 2], rs1 = stats[row * 4 + 3];
   const float inv = 1.f / (float)a.D;
   float2 m1 = make_float2(0.f, 0.f), m0 = m1;
@@ -652,12 +654,13 @@ __global__ __launch_bounds__(512) void resnorm_sum_kernel(SumArgs a) {
 constexpr int kBwdGrid = 256;  // one block per compute unit
 
 template <typename TA, typename TS, int TPR, int NV, bool LONG = true>
-hipError_t forward(const FwdArgs& a, hipStream_t s) {
+hipError_t forward(FwdArgs a, hipStream_t s) {
   constexpr int threads = TPR < 256 ? 256 : TPR;
   constexpr int rows = TPR < 256 ? 256 / TPR : 1;
-  const int64_t grid = (a.M + rows - 1) / rows;
-  resnorm_forward_kernel<TA, TS, TPR, NV, LONG><<<dim3((uint32_t)grid), threads, 0, s>>>(a);
-  return hipGetLastError();
+  return launch_in_parts((a.M + rows - 1) / rows, [&](int64_t first, uint32_t blocks) {
+    a.row0 = first * rows;
+    resnorm_forward_kernel<TA, TS, TPR, NV, LONG><<<dim3(blocks), threads, 0, s>>>(a);
+  });
 }
 
 // the fewest threads that hold a row, 8 columns each (16 from 8193 columns on)
@@ -702,8 +705,12 @@ hipError_t backward_width(const BwdArgs& a, const BwdVectors& v, int grid, hipSt
   if (a.D <= 512 * 8) return backward<TA, TS, 512>(a, v, grid, s);
   if (a.D <= kWideColumns) return backward<TA, TS, 1024>(a, v, grid, s);
   float4* const means = reinterpret_cast<float4*>(a.part + ((int64_t)5 * grid * a.D + 3) / 4 * 4);
-  resnorm_backward_means_kernel<TA, TS><<<dim3((uint32_t)a.M), kWideThreads, 0, s>>>(a, v.stats, v.w_pre, v.w_post, means);
-  if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  const hipError_t e = launch_in_parts(a.M, [&](int64_t first, uint32_t rows) {
+    BwdArgs part = a;
+    part.row0 = first;
+    resnorm_backward_means_kernel<TA, TS><<<dim3(rows), kWideThreads, 0, s>>>(part, v.stats, v.w_pre, v.w_post, means);
+  });
+  if (e != hipSuccess) return e;
   const int strip = (int)((a.M + grid - 1) / grid);
   resnorm_backward_strip_kernel<TA, TS><<<dim3((uint32_t)((a.D + 511) / 512), (uint32_t)grid), 256, 0, s>>>(
       a, v.stats, v.w_pre, v.w_post, v.b_post, means, strip);
@@ -718,7 +725,7 @@ hipError_t launch_resnorm_forward(const void* Y, rb_dtype a_dtype, int64_t M, in
                                   const float* b_pre, float eps, void* S, int64_t lds, void* X, int64_t ldx,
                                   float* stats, hipStream_t s) {
   const FwdArgs a{Y, R, gate, w_post, b_post, w_pre, b_pre, S, X, stats, M, ldy, ldr, ldg, lds, ldx, (int)D, post, pre,
-                  alpha, eps};
+                  alpha, eps, 0};
   if (a_dtype == RB_F32) return forward_width<float, float>(a, s);
   if (a_dtype == RB_F16)
     return s_dtype == RB_F32 ? forward_width<_Float16, float>(a, s) : forward_width<_Float16, _Float16>(a, s);
@@ -746,7 +753,7 @@ hipError_t launch_resnorm_backward(const void* dX, rb_dtype a_dtype, int64_t M, 
                                    hipStream_t s) {
   const BwdVectors v{stats, w_pre, w_post, b_post};
   BwdArgs a{dX, dS, Y, S, gate, dY, dR, ldg ? dgate : nullptr, static_cast<float*>(ws),
-            M, lddx, ldds, ldy, lds, gate ? ldg : 0, lddy, lddr, lddg, (int)D, post, pre, {-1, -1, -1, -1, -1}, alpha};
+            M, lddx, ldds, ldy, lds, gate ? ldg : 0, lddy, lddr, lddg, (int)D, post, pre, {-1, -1, -1, -1, -1}, alpha, 0};
   SumArgs sum{a.part, {}, resnorm_grid(D, M), (int)D};
   int vectors = 0;
   const auto want = [&](int k, float* out) {
