@@ -11,8 +11,9 @@ namespace rb {
 
 int device_cu_count();  // compute units of the current device (cached)
 
-// HIP refuses a launch of 2^32 threads or more in one dimension: longer runs of blocks are launched in parts
-// of 2^20 (a part takes milliseconds, so its launch costs nothing). launch(first, blocks) starts one.
+// A grid of 2^32 threads or more in one dimension is past HIP's limit and runs short without an error: longer runs
+// of blocks are launched in parts of 2^20 (a part takes milliseconds, so its launch costs nothing).
+// launch(first, blocks) starts one.
 template <typename F>
 hipError_t launch_in_parts(int64_t blocks, F launch) {
   constexpr int64_t kPart = int64_t(1) << 20;

@@ -126,7 +126,8 @@ struct TileArgs {
   const void *X, *W;
   int64_t ldx, ldw, M;
   int N, K;
-  uint32_t tiles_m, tiles, per_xcd;
+  uint32_t tiles_m, tiles, per_xcd;  // tiles: the end of the launch's run
+  uint32_t first;                    // its first tile, or block of weight rows
   int chunk_k;    // columns per K chunk, a multiple of kTK
   float* part;    // [chunks][M][N] fp32 sums, or NULL: one chunk, epilogue here
   Epilogue e;
@@ -161,7 +162,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void linear_tile_kernel(TileArgs a
   static_assert(AL || kS == 2, "through registers a step is written two steps ahead");
   extern __shared__ __align__(16) uint8_t l_smem[];
   const uint32_t blk = blockIdx.x;
-  const uint32_t t = blk % kXcds * a.per_xcd + blk / kXcds;  // an XCD's blocks take one run of tiles
+  const uint32_t t = a.first + blk % kXcds * a.per_xcd + blk / kXcds;  // an XCD's blocks take one run of tiles
   if (t >= a.tiles) return;
   const int64_t m0 = (int64_t)__builtin_amdgcn_readfirstlane(t % a.tiles_m) * BM;
   const int n0 = __builtin_amdgcn_readfirstlane(t / a.tiles_m) * BN;
@@ -384,7 +385,7 @@ template <typename TA, typename TY, int MR, int kRows, int kSteps>
 __global__ __launch_bounds__(256) void linear_rows_kernel(TileArgs a) {
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int n0 = (blockIdx.x * 4 + w) * kRows;
+  const int n0 = ((a.first + blockIdx.x) * 4 + w) * kRows;
   if (n0 >= a.N) return;
   const TA* const X = static_cast<const TA*>(a.X);
   const TA* row[kRows];
@@ -648,28 +649,32 @@ hipError_t launch_tile(TileArgs a, int chunks, hipStream_t s) {
                                                      hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (attr != hipSuccess) return attr;
   const int64_t tm = (a.M + BM - 1) / BM, tiles = tm * ((a.N + BN - 1) / BN);
-  if (tiles > 0x70000000) return hipErrorInvalidConfiguration;
+  if (tiles > 0xffffffffll) return hipErrorInvalidConfiguration;  // outputs of 2^40 elements and more
   a.tiles_m = (uint32_t)tm;
-  a.tiles = (uint32_t)tiles;
-  a.per_xcd = (uint32_t)((tiles + kXcds - 1) / kXcds);
-  linear_tile_kernel<TA, TY, WM, WN, TM, 4, kS, AL>
-      <<<dim3(a.per_xcd * kXcds, (uint32_t)chunks), 64 * WM * WN, lds, s>>>(a);
-  return hipGetLastError();
+  return launch_in_parts(tiles, [&](int64_t first, uint32_t count) {
+    a.first = (uint32_t)first;
+    a.tiles = a.first + count;
+    a.per_xcd = (count + kXcds - 1) / kXcds;
+    linear_tile_kernel<TA, TY, WM, WN, TM, 4, kS, AL>
+        <<<dim3(a.per_xcd * kXcds, (uint32_t)chunks), 64 * WM * WN, lds, s>>>(a);
+  });
 }
 
 // One batch row: a weight row per wave, 8 loads of it in flight (4096 x 4096 fp16: 6.9 us, 4.9 TB/s; 2 rows
 // by 4 loads 7.7, 4 by 4 8.1). Up to 4 batch rows: 2 weight rows per wave halve the reads of X (7.4 us;
 // 1 by 8 9.3), where that leaves enough waves.
 template <typename TA, typename TY>
-hipError_t launch_rows(const TileArgs& a, hipStream_t s) {
-  const dim3 ones((uint32_t)((a.N + 3) / 4)), twos((uint32_t)((a.N + 7) / 8));
-  if (a.M == 1)
-    linear_rows_kernel<TA, TY, 1, 1, 8><<<ones, 256, 0, s>>>(a);
-  else if (a.N < 2048)
-    linear_rows_kernel<TA, TY, 4, 1, 8><<<ones, 256, 0, s>>>(a);
-  else
-    linear_rows_kernel<TA, TY, 4, 2, 4><<<twos, 256, 0, s>>>(a);
-  return hipGetLastError();
+hipError_t launch_rows(TileArgs a, hipStream_t s) {
+  const bool pairs = a.M > 1 && a.N >= 2048;
+  return launch_in_parts(pairs ? ((int64_t)a.N + 7) / 8 : ((int64_t)a.N + 3) / 4, [&](int64_t first, uint32_t blocks) {
+    a.first = (uint32_t)first;
+    if (a.M == 1)
+      linear_rows_kernel<TA, TY, 1, 1, 8><<<dim3(blocks), 256, 0, s>>>(a);
+    else if (!pairs)
+      linear_rows_kernel<TA, TY, 4, 1, 8><<<dim3(blocks), 256, 0, s>>>(a);
+    else
+      linear_rows_kernel<TA, TY, 4, 2, 4><<<dim3(blocks), 256, 0, s>>>(a);
+  });
 }
 
 template <typename TA, typename TY>
@@ -740,7 +745,7 @@ hipError_t launch_linear(const void* X, rb_dtype a_dtype, int64_t M, int64_t ldx
   const auto lines = [](const void* p, int64_t ld, rb_dtype t) {
     return reinterpret_cast<uintptr_t>(p) % 128 == 0 && ld * (t == RB_F32 ? 4 : 2) % 128 == 0;
   };
-  TileArgs a{X, W, ldx, ldw, M, (int)N, (int)K, 0, 0, 0, 0, nullptr,
+  TileArgs a{X, W, ldx, ldw, M, (int)N, (int)K, 0, 0, 0, 0, 0, nullptr,
              {bias, R, Z, Y, ldr, ldz, ldy, act, lines(Z, ldz, a_dtype), lines(Y, ldy, y_dtype)}};
   if (a_dtype == RB_F16)
     return y_dtype == RB_F32 ? launch_product<_Float16, float>(a, ws, s) : launch_product<_Float16, _Float16>(a, ws, s);

@@ -89,3 +89,15 @@ def assert_product_close(y_gpu: np.ndarray, y_ref: np.ndarray, sabs: np.ndarray,
     assert not bad.any(), (f"{bad.sum()} outputs out of tolerance; worst ratio "
                            f"{np.max(err / np.maximum(lim, 1e-300)):.3g} at {np.argwhere(bad)[:3].tolist()}")
     return float(np.max(err / np.maximum(lim, 1e-300)))
+
+
+def long_buffer(M, ld, dtype, fill=None):
+    """M rows ld elements apart: normal numbers, or all `fill`."""
+    t = torch.empty((M, ld), dtype=dtype, device=dev())
+    return t.normal_() if fill is None else t.fill_(fill)
+
+
+def pieces(n):
+    """Short runs of n indexes: the first, the last, and some around multiples of 2^20."""
+    at = {0, n - 37, *range(1 << 20, n - 37, max(1 << 20, n // 5 >> 20 << 20))}
+    return [slice(max(0, a - 5), min(n, a + 37)) for a in sorted(at)]

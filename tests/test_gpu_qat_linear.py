@@ -16,7 +16,7 @@ import torch
 
 import residual_binarized_weight_amd as rb
 from oracle import block_oracle as BO
-from tests.gpu_util import dev
+from tests.gpu_util import dev, long_buffer, pieces
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs the GPU")]
@@ -280,3 +280,36 @@ def test_refusals():
         rb.qat_linear(mat(r, 40, 8192, "bf16"), mat(r, 64, 8192, "bf16"), ws=torch.empty(16, dtype=torch.uint8, device=dev()))
     with pytest.raises(rb.RbError):
         rb.qat_linear_backward(X, None, act="relu", a_dtype=torch.bfloat16)
+
+
+# ---------------------------------------------------------------------------------------------
+# more rows than one launch takes
+# ---------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("M", [1, 3])
+def test_weight_rows_past_one_launch(M):
+    """2^26 weight rows and more (2^32 threads), 4.8 G elements apart from first to last: every output is written,
+    sampled ones are right."""
+    N, K = (1 << 26) + 37, 8
+    W = long_buffer(N, 72, DT["bf16"])[:, :K]
+    X, b = long_buffer(M, K, DT["bf16"]), long_buffer(1, N, torch.float32)[0]
+    R = long_buffer(M, N, torch.float32)
+    Y, Z = long_buffer(M, N, torch.float32, float("nan")), long_buffer(M, N, DT["bf16"], float("nan"))
+    rb.qat_linear(X, W, bias=b, act="silu", residual=R, Y=Y, Z=Z)
+    assert not torch.isnan(Y).any() and not torch.isnan(Z).any()
+    for p in pieces(N):
+        check(X, W[p], b[p], "silu", R[:, p], Y[:, p], Z[:, p])
+    del W, b, R, Y, Z
+    torch.cuda.empty_cache()
+
+
+def test_batch_rows_past_one_launch():
+    """2^30 batch rows and more: 2^23 tiles of 512 threads, 8.6 G elements in X and in Y."""
+    M, N, K = (1 << 30) + 77, 8, 8
+    W, X = long_buffer(N, K, DT["f16"]), long_buffer(M, K, DT["f16"])
+    Y = long_buffer(M, N, DT["f16"], float("nan"))
+    rb.qat_linear(X, W, act="relu", Y=Y)
+    assert not torch.isnan(Y).any()
+    for p in pieces(M):
+        check(X[p], W, None, "relu", None, Y[p], None)
+    del X, Y
+    torch.cuda.empty_cache()

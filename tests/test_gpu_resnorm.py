@@ -13,7 +13,7 @@ import torch
 
 import residual_binarized_weight_amd as rb
 from oracle import block_oracle as BO
-from tests.gpu_util import dev
+from tests.gpu_util import dev, long_buffer, pieces
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs the GPU")]
@@ -335,25 +335,13 @@ def test_refusals():
 # ---------------------------------------------------------------------------------------------
 # more rows than one launch takes
 # ---------------------------------------------------------------------------------------------
-def long_buffer(M, ld, dt, fill=None):
-    """M rows ld elements apart: normal numbers, or all `fill`."""
-    t = torch.empty((M, ld), dtype=DT[dt], device=dev())
-    return t.normal_() if fill is None else t.fill_(fill)
-
-
-def pieces(M):
-    """Short runs of rows: the first, the last, and around the middle ones that are multiples of 2^20."""
-    at = {0, M - 37, *range(1 << 20, M - 37, max(1 << 20, M // 5 >> 20 << 20))}
-    return [slice(max(0, a - 5), min(M, a + 37)) for a in sorted(at)]
-
-
 @pytest.mark.parametrize("M,D,ld", [((1 << 26) + 9, 8, 72), ((1 << 20) + 5, 1030, 1040)])
 def test_forward_rows_past_one_launch(M, D, ld):
     """2^32 threads and more, and offsets past 2^32 elements: every row is written, and sampled runs of rows are
     what a call on them alone gives (a row's result does not depend on the others)."""
     r = np.random.default_rng(98)
     a = dict(w_pre=vec(r, D), w_post=vec(r, D), gate=vec(r, D), alpha=0.75, pre="rms", post="rms", eps=EPS)
-    Y, S, X = long_buffer(M, ld, "f16")[:, :D], long_buffer(M, ld, "f16")[:, :D], long_buffer(M, ld, "f16", float("nan"))[:, :D]
+    Y, S, X = long_buffer(M, ld, DT["f16"])[:, :D], long_buffer(M, ld, DT["f16"])[:, :D], long_buffer(M, ld, DT["f16"], float("nan"))[:, :D]
     R = [S[p].clone() for p in pieces(M)]
     _, _, st = rb.resnorm_forward(Y, S, S=S, X=X, **a)
     assert not torch.isnan(X).any() and torch.all(st[:, 1] > 0) and torch.all(st[:, 3] > 0)
@@ -368,7 +356,7 @@ def test_forward_rows_past_one_launch(M, D, ld):
 def test_backward_wide_rows_past_one_launch():
     """The same of the row means' launch: 2^20 rows and more of over 8192 columns, 8.6 G elements a tensor."""
     M, D = (1 << 20) + 3, 8200
-    dX, S = long_buffer(M, D, "f16"), long_buffer(M, D, "f16")
+    dX, S = long_buffer(M, D, DT["f16"]), long_buffer(M, D, DT["f16"])
     w = vec(np.random.default_rng(99), D)
     st = torch.zeros((M, 4), device=dev())
     st[:, 3] = 1.0
