@@ -531,8 +531,9 @@ rb_status rb_resnorm_backward(const void* dX, rb_dtype a_dtype, int64_t M, int64
  *   p, g     aligned to their element; m and v to 4 bytes with state_bits 32; scales to 4 bytes
  *            (NULL with state_bits 32). Pointers at 16 bytes (8 for 2-byte types) make the
  *            accesses wide; others only cost time.
- *   count    0 .. 2^20; chunks receives the number of 4096-element chunks (below 2^31), which
- *            the steps take. Tensors must not overlap.
+ *   count    0 .. 2^20; chunks receives the number of 4096-element chunks, which the
+ *            steps take; 2^24 of them (6.9e10 elements, more than the device's memory holds) and more are
+ *            RB_ERR_UNSUPPORTED. Tensors must not overlap.
  * rb_adamw_plan_bytes: 0 if t is NULL with count > 0, count is out of range or an n is negative.
  *
  * rb_adamw_step

@@ -551,6 +551,9 @@ rb_status rb_resnorm_backward(const void* dX, rb_dtype a_dtype, int64_t M, int64
                                               static_cast<hipStream_t>(stream)));
 }
 
+// a block of 256 threads per chunk, and a grid holds less than 2^32 threads
+constexpr int64_t kAdamwMaxChunks = (int64_t(1) << 24) - 1;
+
 static bool adamw_counts_ok(const rb_adamw_tensor* t, int64_t count) {
   if (count < 0 || count > (int64_t(1) << 20) || (count > 0 && !t)) return false;
   int64_t chunks = 0;
@@ -570,6 +573,7 @@ rb_status rb_adamw_plan(const rb_adamw_tensor* t, int64_t count, int32_t state_b
                         int64_t* chunks) {
   if (!image || !chunks || !adamw_counts_ok(t, count)) return RB_ERR_INVALID_ARG;
   if (state_bits != 32 && state_bits != 8) return RB_ERR_INVALID_ARG;
+  if (rb::adamw_chunks(t, count) > kAdamwMaxChunks) return RB_ERR_UNSUPPORTED;
   for (int64_t i = 0; i < count; ++i) {
     const rb_adamw_tensor& x = t[i];
     const rb_dtype pd = static_cast<rb_dtype>(x.p_dtype), gd = static_cast<rb_dtype>(x.g_dtype);
@@ -599,6 +603,7 @@ rb_status rb_adamw_step(const void* plan, int64_t chunks, int32_t state_bits, in
   if (!std::isfinite(lr) || lr < 0.0 || !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0))
     return RB_ERR_INVALID_ARG;
   if (!std::isfinite(eps) || !(static_cast<float>(eps) > 0.f)) return RB_ERR_INVALID_ARG;
+  if (chunks > kAdamwMaxChunks) return RB_ERR_UNSUPPORTED;
   if (!aligned(plan, 16) || !aligned(grad_scale, 4) || !aligned(skip, 4)) return RB_ERR_MISALIGNED;
   log_call("rb_adamw_step", chunks, state_bits, 0, 0);
   return from_hip(rb::launch_adamw_step(plan, chunks, state_bits, step, lr, beta1, beta2, eps, grad_scale, skip, seed,

@@ -176,6 +176,15 @@ def test_adamw_step_rejects(kw, status):
                            a["skip"], 0, None) == status
 
 
+def test_adamw_chunks_of_one_launch():
+    """A block of 256 threads per chunk: 2^24 of them do not fit a grid, and would run short without an error."""
+    most = 4096 * ((1 << 24) - 1)
+    assert plan([tensor(n=most)])[::2] == (_lib.RB_OK, (1 << 24) - 1)
+    assert plan([tensor(n=most + 1)])[0] == UNSUPPORTED
+    assert plan([tensor(n=most), tensor(n=1)])[0] == UNSUPPORTED
+    assert L.rb_adamw_step(P, 1 << 24, 32, 1, 1e-3, 0.9, 0.99, 1e-8, None, None, 0, None) == UNSUPPORTED
+
+
 def test_workspace_sizes():
     zero = lambda n: (8 * n + 255) // 256 * 256  # noqa: E731
     ws = lambda op, n, k, m: L.rb_workspace_bytes(op, 1, n, k, m)  # noqa: E731
