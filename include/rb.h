@@ -473,12 +473,13 @@ rb_status rb_qat_linear_backward(const void* dY, rb_dtype dy_dtype, int64_t M, i
  *   Buffers are aligned to their element; rows need no other alignment. Elements past D of a row
  *   are not touched.
  *
- * rb_resnorm_forward -- R may be NULL (no residual), S may be NULL (not kept), stats too; X must be
- *   given where pre is not RB_NORM_NONE. alpha finite, eps finite and > 0. S may be R and X may be
+ * rb_resnorm_forward -- R may be NULL (no residual), stats too. With a pre norm X must be given and S may
+ *   be NULL (not kept); with pre RB_NORM_NONE S is the only output: it must be given and X must be NULL
+ *   (RB_ERR_INVALID_ARG). alpha finite, eps finite and > 0. S may be R and X may be
  *   Y (same leading dimension); other overlaps are not allowed.
  *
  * rb_resnorm_backward -- gradients from those of X (dX, needed where pre is not RB_NORM_NONE, as
- *   are S and w_pre) and of S (dS, NULL = 0), with the forward's Y (may be NULL if post is
+ *   are S and w_pre; NULL otherwise) and of S (dS, NULL = 0, needed for RB_NORM_NONE), with the forward's Y (may be NULL if post is
  *   RB_NORM_NONE and there is no gate), S and stats; with d = dy (.) w and xh = (x - mu) rstd a
  *   norm gives rstd (d - xh mean(d xh) - [layer] mean(d)):
  *     T = dS + norm_pre's gradient;  dR = alpha T;  dgate = u (.) T;  dY = norm_post's gradient of gate (.) T

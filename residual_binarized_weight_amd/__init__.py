@@ -459,7 +459,7 @@ def resnorm_forward(Y: torch.Tensor, R: torch.Tensor | None, w_pre: torch.Tensor
     output, R [M][D] the stream (Y's type or fp32; None: no residual), `gate` an fp32 vector [D], rows
     [M][D] of Y's type or None; `pre` and `post` name the norms ("none", "rms", "layer"; post
     defaults to "rms" where w_post is given), w_* and b_* are fp32 [D]. Returns (S, X, stats): S in
-    R's type, X in Y's (None for pre "none"), stats [M][4] fp32 for the backward."""
+    R's type, X in Y's (None for pre "none", which takes no X), stats [M][4] fp32 for the backward."""
     M, D = Y.shape
     post = post or ("none" if w_post is None else "rms")
     sdt = R.dtype if R is not None else S.dtype if S is not None else Y.dtype
@@ -487,7 +487,7 @@ def resnorm_backward(dX: torch.Tensor | None, dS: torch.Tensor | None, Y: torch.
                      alpha: float = 1.0, pre: str = "rms", post: str | None = None, bias: bool = False,
                      dY: torch.Tensor | None = None, dR: torch.Tensor | None = None, ws: torch.Tensor | None = None,
                      out: dict | None = None):
-    """Gradients of resnorm_forward's inputs from those of X (dX) and S (dS; None: zero), in a dict:
+    """Gradients of resnorm_forward's inputs from those of X (dX; None for pre "none") and S (dS; None: zero), in a dict:
     dY, dR, dgate (like the gate), dw_pre, dw_post and, with `bias`, db_pre, db_post (fp32 [D]); None
     where there is no such input. `out` holds buffers for any of the vectors' or the gate's gradients, by
     these names. Other arguments as in the forward call."""

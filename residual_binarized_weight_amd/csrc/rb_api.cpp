@@ -505,7 +505,8 @@ rb_status rb_resnorm_forward(const void* Y, rb_dtype a_dtype, int64_t M, int64_t
                              const float* w_post, const float* b_post, int32_t pre, const float* w_pre,
                              const float* b_pre, float eps, void* S, int64_t lds, void* X, int64_t ldx, float* stats,
                              void* stream) {
-  if (!Y || (pre != RB_NORM_NONE && !X) || (!S && !X)) return RB_ERR_INVALID_ARG;
+  // without a pre norm the stream is the output: an X would stay unwritten
+  if (!Y || (pre == RB_NORM_NONE ? !S || X : !X)) return RB_ERR_INVALID_ARG;
   rb_status st = check_resnorm(a_dtype, s_dtype, M, D, gate, ldg, alpha, post, w_post, b_post, pre, w_pre);
   if (st != RB_OK) return st;
   if (!row_ld(ldy, D) || (R && !row_ld(ldr, D)) || (S && !row_ld(lds, D)) || (X && !row_ld(ldx, D)))
@@ -526,7 +527,8 @@ rb_status rb_resnorm_backward(const void* dX, rb_dtype a_dtype, int64_t M, int64
                               const float* w_post, const float* b_post, int32_t pre, const float* w_pre, void* dY,
                               int64_t lddy, void* dR, int64_t lddr, void* dgate, int64_t lddg, float* dw_post,
                               float* db_post, float* dw_pre, float* db_pre, void* ws, size_t ws_bytes, void* stream) {
-  if (!stats || !dY || (pre != RB_NORM_NONE && (!dX || !S)) || (pre == RB_NORM_NONE && !dS)) return RB_ERR_INVALID_ARG;
+  // ... and has the only gradient: a dX would be dropped
+  if (!stats || !dY || (pre == RB_NORM_NONE ? !dS || dX : !dX || !S)) return RB_ERR_INVALID_ARG;
   if (!Y && (post != RB_NORM_NONE || gate)) return RB_ERR_INVALID_ARG;
   if ((post == RB_NORM_NONE && (dw_post || db_post)) || (pre == RB_NORM_NONE && (dw_pre || db_pre)) || (!gate && dgate))
     return RB_ERR_INVALID_ARG;

@@ -120,6 +120,19 @@ def test_resnorm_backward_rejects(kw, status):
     assert resnorm_backward(**kw) == status
 
 
+def test_resnorm_without_a_pre_norm_takes_no_x():
+    """The stream is the only output then: an X would stay unwritten, a dX would be dropped."""
+    none = dict(pre=0, wpre=None)
+    assert resnorm(**none) == INVALID
+    assert resnorm(**none, S=None, lds=0) == INVALID
+    assert resnorm(**none, X=None, S=None) == INVALID
+    assert resnorm_backward(**none, dwpre=None) == INVALID
+    assert resnorm_backward(**none, dwpre=None, dX=None, dS=None) == INVALID
+    # what is left passes these checks and meets a later one
+    assert resnorm(**none, X=None, S=P2) == MISALIGNED
+    assert resnorm_backward(**none, dwpre=None, dX=None, ws=None) == WORKSPACE
+
+
 def tensor(n=100, **kw):
     a = dict(p=0x100000, g=0x200000, m=0x300000, v=0x400000, m_scale=0x500000, v_scale=0x600000, n=n, lr_mult=1.0,
              weight_decay=0.1, p_dtype=F32, g_dtype=F32)
