@@ -468,7 +468,8 @@ rb_status rb_qat_linear_backward(const void* dY, rb_dtype dy_dtype, int64_t M, i
  *   a_dtype   type of Y, X and a gate of rows: RB_F32, RB_F16, RB_BF16
  *   s_dtype   type of the stream R, S: a_dtype or RB_F32
  *   gate      NULL (ones); with ldg = 0 an fp32 [D] vector; otherwise [M][ldg] in a_dtype
- *   post, pre rb_norm; w_*, b_* fp32 [D] (w needed where the norm is not RB_NORM_NONE; b NULL = 0)
+ *   post, pre rb_norm; w_*, b_* fp32 [D] (w needed where the norm is not RB_NORM_NONE, whose
+ *             own w and b are not used; b NULL = 0)
  *   stats     fp32 [M][4]: post mean, post rstd, pre mean, pre rstd (0 for RB_NORM_NONE)
  *   Buffers are aligned to their element; rows need no other alignment. Elements past D of a row
  *   are not touched.

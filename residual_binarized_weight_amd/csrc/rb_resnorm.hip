@@ -751,7 +751,7 @@ hipError_t launch_resnorm_backward(const void* dX, rb_dtype a_dtype, int64_t M, 
                                    void* dY, int64_t lddy, void* dR, int64_t lddr, void* dgate, int64_t lddg,
                                    float* dw_post, float* db_post, float* dw_pre, float* db_pre, void* ws,
                                    hipStream_t s) {
-  const BwdVectors v{stats, w_pre, w_post, b_post};
+  const BwdVectors v{stats, w_pre, w_post, post == RB_NORM_NONE ? nullptr : b_post};  // no norm, no bias in u
   BwdArgs a{dX, dS, Y, S, gate, dY, dR, ldg ? dgate : nullptr, static_cast<float*>(ws),
             M, lddx, ldds, ldy, lds, gate ? ldg : 0, lddy, lddr, lddg, (int)D, post, pre, {-1, -1, -1, -1, -1}, alpha, 0};
   SumArgs sum{a.part, {}, resnorm_grid(D, M), (int)D};

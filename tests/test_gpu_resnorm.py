@@ -253,6 +253,21 @@ def test_backward_wide_kinds(dt, sdt, post, pre, gate):
     run_backward(101, 6, 8300, dt, sdt, post, pre, gate, gate == "element", ld=8311, off=3, with_ds=gate != "none")
 
 
+@pytest.mark.parametrize("D", [300, 6000, 8300])
+@pytest.mark.parametrize("gate", ["channel", "element"])
+def test_vectors_of_an_absent_norm_are_not_used(D, gate):
+    """post "none" with a w_post and a b_post: u is Y itself, in both directions."""
+    a, dX, dS, S, st, got = run_backward(103, 6, D, "bf16", "f32", "none", "rms", gate, False)
+    r = np.random.default_rng(104)
+    w, b = vec(r, D), vec(r, D)
+    same = rb.resnorm_forward(**{**a, "w_post": w, "b_post": b}, eps=EPS)
+    back = rb.resnorm_backward(dX, dS, a["Y"], S, st, a["w_pre"], w_post=w, b_post=b, gate=a["gate"], alpha=a["alpha"],
+                               pre="rms", post="none")
+    torch.cuda.synchronize()
+    assert torch.equal(same[0], S) and torch.equal(same[2], st)
+    assert all(torch.equal(back[k], got[k]) for k in got if got[k] is not None)
+
+
 def test_backward_wide_in_place_and_deterministic():
     a, dX, dS, S, st, got = run_backward(102, 70, 8705, "bf16", "bf16", "rms", "layer", "channel", False)
     kw = dict(w_post=a["w_post"], gate=a["gate"], alpha=a["alpha"], pre="layer", post="rms")
