@@ -32,15 +32,31 @@ __device__ __forceinline__ l_f4 mfma(__bf16, l_u4 a, l_u4 b, l_f4 c) {
 }
 
 // ---------------------------------------------------------------------------------------------
-// activations, in fp32: their own error is a few units of 2^-24 of |z|, below every storage type's
+// activations, in fp32. Relative to the value their errors are some tens of units of 2^-24 and, in the
+// tails, the exponentials' arguments times it (z^2 / 2 for the normal density, 17 at z = -5 for the tanh form).
 // ---------------------------------------------------------------------------------------------
 constexpr float kGeluA = 0.7978845608028654f;  // sqrt(2 / pi)
 constexpr float kGeluB = 0.044715f;
 __device__ __forceinline__ float logistic(float z) { return __builtin_amdgcn_rcpf(1.f + __expf(-z)); }
+// The normal CDF, e = exp(-z^2 / 2): below zero e r(|z|), above one minus that. 1 + erf loses every digit below zero
+// (4 % of the value at z = -5). r, half of exp(x^2) erfc(x), is a polynomial in s = 1 / (1 + 0.3 |z|) without a constant
+// term, fitted over |z| = 0 .. 14 by least squares with weights moved towards the largest relative error: 8 units of
+// 2^-24 in fp32. The backward of 2048 x 11008 in bf16 takes 34 us with it, 40 with 1 + erff, 47 with erfcf.
+__device__ __forceinline__ float normal_cdf(float z, float e) {
+  const float s = __builtin_amdgcn_rcpf(fmaf(0.3f, fabsf(z), 1.f));
+  float r = fmaf(s, 0.035674576f, -0.15720132f);
+  r = fmaf(s, r, 0.20634893f);
+  r = fmaf(s, r, -0.053678185f);
+  r = fmaf(s, r, 0.12855819f);
+  r = fmaf(s, r, 0.09991466f);
+  r = fmaf(s, r, 0.12075376f);
+  r = fmaf(s, r, 0.11962932f) * s * e;
+  return z > 0.f ? 1.f - r : r;
+}
 __device__ __forceinline__ float act_value(float z, int act) {
   switch (act) {
     case RB_ACT_RELU: return z < 0.f ? 0.f : z;
-    case RB_ACT_GELU: return 0.5f * z * (1.f + erff(z * 0.7071067811865476f));
+    case RB_ACT_GELU: return z * normal_cdf(z, __expf(-0.5f * z * z));
     case RB_ACT_GELU_TANH: return z * logistic(2.f * kGeluA * (z + kGeluB * z * z * z));  // (1 + tanh a) / 2
     case RB_ACT_SILU: return z * logistic(z);
   }
@@ -49,8 +65,10 @@ __device__ __forceinline__ float act_value(float z, int act) {
 __device__ __forceinline__ float act_slope(float z, int act) {
   switch (act) {
     case RB_ACT_RELU: return z > 0.f ? 1.f : 0.f;
-    case RB_ACT_GELU:
-      return 0.5f * (1.f + erff(z * 0.7071067811865476f)) + z * 0.3989422804014327f * __expf(-0.5f * z * z);
+    case RB_ACT_GELU: {
+      const float e = __expf(-0.5f * z * z);
+      return normal_cdf(z, e) + z * 0.3989422804014327f * e;
+    }
     case RB_ACT_GELU_TANH: {
       const float g = logistic(2.f * kGeluA * (z + kGeluB * z * z * z));
       return g + z * g * (1.f - g) * 2.f * kGeluA * (1.f + 3.f * kGeluB * z * z);

@@ -10,6 +10,8 @@ Comparison rules, u = 2^-24:
 * dZ: the slope's evaluation within 24 u (1 + |z|) of |dY|; db: those errors and M u of sum |dZ|;
 * rounded outputs add half a unit of their type.
 """
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -257,6 +259,53 @@ def test_slope_is_the_difference_quotient(act):
     zz, h = n64(z), 1e-4
     diff = (BO.activation(zz + h, act)[0] - BO.activation(zz - h, act)[0]) / (2 * h)
     assert np.max(np.abs(n64(db) - diff[0])) <= h * h + 24 * U * 10 + 1e-10 / h
+
+
+def tail_terms(act, z):
+    """Relative errors of the activations' parts at z, in units of U: those of a rounded argument of the normal tail
+    (twice its square, z^2, for two roundings) and of the logistic function (seven roundings and the product with
+    log2 e); and 40 for exp, the tail's ratio (up to 32), the reciprocal and the products."""
+    if act == "gelu":
+        return 40 + 3 * z * z
+    return 40 + 9 * np.abs(z if act == "silu" else 2 * np.sqrt(2 / np.pi) * (z + 0.044715 * z ** 3))
+
+
+@pytest.mark.parametrize("act", ACTS[2:])
+def test_activations_keep_their_digits_in_the_tails(act):
+    """Every value against itself, not against z: z comes exactly, as the bias of a product of zeros."""
+    z = torch.linspace(-9, 9, 3001, device=dev())
+    X = torch.zeros((1, 8), dtype=torch.bfloat16, device=dev())
+    W = torch.zeros((z.numel(), 8), dtype=torch.bfloat16, device=dev())
+    Y, _ = rb.qat_linear(X, W, bias=z, act=act, y_dtype=torch.float32)
+    torch.cuda.synchronize()
+    zz = n64(z)
+    ref = zz * tail_cdf(act, zz)
+    near(Y[0], ref, tail_terms(act, zz) * U * np.abs(ref), "Y")
+
+
+@pytest.mark.parametrize("act", ACTS[2:])
+def test_slopes_keep_their_digits_in_the_tails(act):
+    """Below zero, against the sum of the slope's terms; db of one row is the slope in fp32."""
+    z = torch.linspace(-9, -0.25, 3001, device=dev()).to(torch.float16).reshape(1, -1)
+    _, db = rb.qat_linear_backward(torch.ones_like(z, dtype=torch.float32), z, act=act)
+    torch.cuda.synchronize()
+    zz = n64(z)[0]
+    g = tail_cdf(act, zz)
+    if act == "gelu":
+        second = zz * np.exp(-0.5 * zz * zz) / np.sqrt(2 * np.pi)
+    else:
+        second = zz * g * (1 - g)
+        if act == "gelu_tanh":
+            second *= 2 * np.sqrt(2 / np.pi) * (1 + 3 * 0.044715 * zz * zz)
+    near(db, g + second, 2 * tail_terms(act, zz) * U * (g + np.abs(second)), "slope")
+
+
+def tail_cdf(act, z):
+    """What the activation multiplies z by, in 64 bits without cancellation."""
+    if act == "gelu":
+        return 0.5 * np.vectorize(math.erfc)(-z / math.sqrt(2.0))
+    a = z if act == "silu" else 2 * np.sqrt(2 / np.pi) * (z + 0.044715 * z ** 3)
+    return 1 / (1 + np.exp(-a))
 
 
 def test_refusals():
