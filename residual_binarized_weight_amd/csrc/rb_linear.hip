@@ -71,7 +71,8 @@ __device__ __forceinline__ float act_slope(float z, int act) {
     }
     case RB_ACT_GELU_TANH: {
       const float g = logistic(2.f * kGeluA * (z + kGeluB * z * z * z));
-      return g + z * g * (1.f - g) * 2.f * kGeluA * (1.f + 3.f * kGeluB * z * z);
+      // from |z| = 16 on g is 0 or 1 and the second term 0, whatever its factor: z^2 must not overflow there
+      return g + z * g * (1.f - g) * 2.f * kGeluA * (1.f + 3.f * kGeluB * fminf(z * z, 256.f));
     }
     case RB_ACT_SILU: {
       const float g = logistic(z);

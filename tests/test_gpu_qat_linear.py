@@ -261,6 +261,18 @@ def test_slope_is_the_difference_quotient(act):
     assert np.max(np.abs(n64(db) - diff[0])) <= h * h + 24 * U * 10 + 1e-10 / h
 
 
+@pytest.mark.parametrize("act", ACTS[1:])
+def test_slopes_of_huge_values(act):
+    """0 and 1 for every finite value far out, also where its square or cube overflows."""
+    big = torch.tensor([30.0, 1e4, 1e13, 1.5e19, 2e19, 1e30, 3e38], device=dev())
+    z = torch.cat([big, -big]).to(torch.bfloat16).reshape(1, -1)
+    dZ, db = rb.qat_linear_backward(torch.ones_like(z), z, act=act)
+    torch.cuda.synchronize()
+    want = [1.0] * 7 + [0.0] * 7
+    # -30: slopes of 1e-11 and less
+    assert np.all(np.abs(n64(dZ)[0] - want) <= 1e-10) and np.all(np.abs(n64(db) - want) <= 1e-10)
+
+
 def tail_terms(act, z):
     """Relative errors of the activations' parts at z, in units of U: those of a rounded argument of the normal tail
     (twice its square, z^2, for two roundings) and of the logistic function (seven roundings and the product with
