@@ -440,8 +440,8 @@ rb_status rb_qat_autotune(const void* X, const void* dY, rb_dtype a_dtype, int64
  *            partial sums of a product with few output tiles, whose columns are split over the GPU
  *            and joined in a fixed order (deterministic); no zero-filling needed.
  *
- * rb_qat_linear_backward -- from dY = the gradient of Y: dZ = dY (.) act'(Z) (relu's slope at 0 is
- *   0) and db = the column sums of the unrounded dZ in fp32, in a fixed order. dZ is what
+ * rb_qat_linear_backward -- from dY = the gradient of Y: dZ = dY (.) act'(Z) (relu's slope is 1
+ *   where Z > 0 and 0 elsewhere, at 0 and for a NaN too) and db = the column sums of the unrounded dZ in fp32, in a fixed order. dZ is what
  *   rb_qat_backward takes as its dY; R's gradient is dY itself.
  *   dY       [M][lddy] in dy_dtype, RB_F32 or a_dtype;  Z  [M][ldz] in a_dtype (may be NULL for RB_ACT_NONE)
  *   dZ       [M][lddz] in a_dtype, or NULL with a db; may be dY or Z (same type and leading dimension)

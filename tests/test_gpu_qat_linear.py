@@ -273,6 +273,25 @@ def test_slopes_of_huge_values(act):
     assert np.all(np.abs(n64(dZ)[0] - want) <= 1e-10) and np.all(np.abs(n64(db) - want) <= 1e-10)
 
 
+@pytest.mark.parametrize("act", ACTS)
+def test_non_finite_z_in_the_activation_and_its_slope(act):
+    """A NaN stays one in the value; its slope is NaN but for relu, whose slope is z > 0, as stated."""
+    z = torch.tensor([[float("nan"), float("inf"), -float("inf"), 1.0, 0.0, -0.0, -1.0, 2.0]], device=dev())
+    X, W = torch.zeros((1, 8), dtype=torch.float16, device=dev()), torch.zeros((8, 8), dtype=torch.float16, device=dev())
+    Y, Z = rb.qat_linear(X, W, bias=z[0], act=act, save_z=True)
+    dZ, db = rb.qat_linear_backward(torch.ones_like(Z), Z, act=act)
+    torch.cuda.synchronize()
+    assert np.array_equal(n64(Z), n64(z), equal_nan=True)
+    y, d = n64(Y)[0], n64(dZ)[0]
+    assert np.isnan(y[0]) and y[1] == np.inf and np.all(np.isfinite(y[3:])) and np.all(np.isfinite(d[3:]))
+    if act == "relu":
+        assert y[2] == 0 and d.tolist() == [0, 1, 0, 1, 0, 0, 0, 1] and np.array_equal(n64(db), d)
+    elif act == "none":
+        assert y[2] == -np.inf and np.all(d == 1)
+    else:
+        assert np.isnan(d[0])
+
+
 def tail_terms(act, z):
     """Relative errors of the activations' parts at z, in units of U: those of a rounded argument of the normal tail
     (twice its square, z^2, for two roundings) and of the logistic function (seven roundings and the product with
