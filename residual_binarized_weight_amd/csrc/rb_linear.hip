@@ -600,48 +600,56 @@ bool tile_aligned(const void* X, int64_t ldx, const void* W, int64_t ldw, int64_
 // How a product is laid over the GPU's 256 compute units: `bm` batch rows by 256 weight rows per tile
 // (32, 64, 128; 256 for the first `big_n` weight rows), the columns in `chunks`.
 //
+// The layout is chosen by estimate, in us: a step of a tile costs `one` when few units are busy and `all`
+// when every unit loads at once; 5 for the launch and the ends of the pipeline; a split costs its partial
+// sums' way to memory and back (5 MB / us) and 2 for the join. The figures are fits to measured runs (16..1024
+// rows, 1000..4096 weight rows and columns), where the choice is within 10 % of the best of the 15 layouts; one
+// layout for all would cost up to twice the time (512 x 4096 x 4096: 32-row tiles 30.6 us, 128-row tiles 47.7 us
+// and in 4 chunks 35.4 us; 64 x 4096 x 4096: 28.7 us whole, 14.4 us in 4 chunks).
+//
 // 256-row tiles move two thirds of the bytes per product that 128-row ones do, but a round of 256 of
-// them must be full to pay: whole rounds go to them, the rest to the small tiles (2048 x 11008 x 4096:
-// 127 + 70 us; 128-row tiles alone 198 us, 256-row ones alone 196 us).
-// The rest, and every smaller product, is laid out by estimate, in us: a step of a tile costs `one` when
-// few units are busy and `all` when every unit loads at once; 5 for the launch and the ends of the
-// pipeline; a split costs its partial sums' way to memory and back (5 MB / us) and 2 for the join. The
-// figures are fits to measured runs (16..1024 rows, 1000..4096 weight rows and columns), where the choice
-// is within 10 % of the best of the 15 layouts; one layout for all would cost up to twice the time
-// (512 x 4096 x 4096: 32-row tiles 30.6 us, 128-row tiles 47.7 us and in 4 chunks 35.4 us; 64 x 4096 x
-// 4096: 28.7 us whole, 14.4 us in 4 chunks).
+// them must be full to pay: whole rounds go to them (kBig a step), the rest to the small tiles. Small tiles alone
+// are taken where they are estimated at kClear of that time and less, which is where most of the last row of
+// 256-row tiles is empty. Measured, 256-row tiles first / small ones alone: 2048 x 11008 x 4096 170 / 186 us,
+// 150 x 65536 x 256 26 / 36, 700 x 24576 x 4096 158 / 178; 2550 x 9640 x 2064 220 / 147, 520 x 24576 x 256 34 / 27,
+// 1300 x 11264 x 1024 54 / 46, 2666 x 15176 x 496 120 / 101. Between kClear and equal estimates it goes either way
+// (1100 x 14336 x 4096 149 / 129, 3381 x 4824 x 240 38 / 50).
 struct Plan {
   int bm, chunks, chunk_k, big_n;
   double est;
 };
-Plan plan_tiles(int64_t M, int64_t N, int64_t K, bool aligned) {
+Plan plan_small_tiles(int64_t M, int64_t N, int64_t K, bool aligned) {
   Plan p{};
-  const int64_t tn = (N + 255) / 256;
-  if (aligned && M > 128) {
-    const int64_t tm2 = (M + 255) / 256, rounds = tm2 * tn / 256;
-    if (rounds > 0) p.big_n = (int)(rounds * 256 / tm2 * 256 < N ? rounds * 256 / tm2 * 256 : N);
-  }
-  const int64_t n = N - p.big_n, steps = (K + kTK - 1) / kTK;
+  const int64_t steps = (K + kTK - 1) / kTK;
   struct { int bm; double one, all; } const kinds[2][3] = {{{32, 0.79, 0.9}, {64, 1.0, 1.15}, {128, 1.07, 1.3}},
                                                            {{32, 0.36, 0.38}, {64, 0.50, 0.65}, {128, 0.65, 0.95}}};
-  double best = 0.0;
   for (const auto& k : kinds[aligned]) {
-    const int64_t tiles = (M + k.bm - 1) / k.bm * ((n + 255) / 256);
+    const int64_t tiles = (M + k.bm - 1) / k.bm * ((N + 255) / 256);
     for (int64_t c = 1; c <= 16 && (c == 1 || (c * 2 <= steps && tiles * c <= 512)); c *= 2) {
       const int64_t blocks = tiles * c, rounds = (blocks + 255) / 256, each = (steps + c - 1) / c;
       const double load = blocks < 256 ? (double)blocks / 256 : 1.0;
       const double est = 5.0 + (double)rounds * (double)(each + 2) * (k.one + (k.all - k.one) * load) +
-                         (c > 1 ? 2.0 + (double)c * (double)M * (double)n * 8 / 5e6 : 0.0);
-      if (p.bm == 0 || est < best) {
-        best = est;
+                         (c > 1 ? 2.0 + (double)c * (double)M * (double)N * 8 / 5e6 : 0.0);
+      if (p.bm == 0 || est < p.est) {
+        p.est = est;
         p.bm = k.bm;
         p.chunk_k = (int)each * kTK;
       }
     }
   }
   p.chunks = (int)((K + p.chunk_k - 1) / p.chunk_k);
-  p.est = best;
   return p;
+}
+Plan plan_tiles(int64_t M, int64_t N, int64_t K, bool aligned) {
+  constexpr double kBig = 1.6, kClear = 0.87;
+  const Plan small = plan_small_tiles(M, N, K, aligned);
+  const int64_t tm = (M + 255) / 256, rounds = tm * ((N + 255) / 256) / 256;
+  if (!aligned || rounds == 0) return small;
+  const int64_t big_n = rounds * 256 / tm * 256 < N ? rounds * 256 / tm * 256 : N;
+  Plan p = big_n < N ? plan_small_tiles(M, N - big_n, K, aligned) : Plan{};
+  p.big_n = (int)big_n;
+  p.est += 5.0 + (double)rounds * (double)((K + kTK - 1) / kTK + 2) * kBig;
+  return big_n == 0 || small.est < kClear * p.est ? small : p;
 }
 
 // The forms without tiles; both read 8 columns at least. Up to 4 rows the vector units' products cost nothing
@@ -656,7 +664,7 @@ Small small_form(int64_t M, int64_t N, int64_t K, bool aligned) {
   if (M <= kMaxRows) return Small::kRows;
   const int64_t rounds = ((N + 15) / 16 * ((M + 15) / 16) + 255) / 256, steps = (K + kTK - 1) / kTK;
   const Plan p = plan_tiles(M, N, K, aligned);
-  return p.big_n == 0 && 2.6 + (double)(rounds * steps) * (aligned ? 0.13 : 0.33) < p.est ? Small::kFew : Small::kNone;
+  return 2.6 + (double)(rounds * steps) * (aligned ? 0.13 : 0.33) < p.est ? Small::kFew : Small::kNone;
 }
 
 template <typename TA, typename TY, int WM, int WN, int TM, int kS, bool AL>

@@ -216,6 +216,23 @@ def test_workspace_sizes():
     assert got > 0 and got % (512 * 4) == 0
 
 
+def test_product_workspace_follows_the_layout_rule():
+    """The partial sums of the layout that the restated rule chooses, over 6000 shapes; 256-row tiles first where small
+    tiles alone are not clearly estimated below them (312 x 33832 x 1024 and 617 x 25264 x 4096 are whole, where 256-row
+    tiles would leave a rest with split columns)."""
+    from tests import linear_forms as F
+    r = np.random.default_rng(40)
+    draw = lambda lo, hi: np.exp(r.uniform(np.log(lo), np.log(hi), 6000)).round().astype(int)  # noqa: E731
+    shapes = list(zip(draw(1, 8192), draw(1, 40000), draw(1, 12000)))
+    shapes += [(M, (N + 7) // 8 * 8, (K + 7) // 8 * 8) for M, N, K in shapes[:2000]]
+    shapes += [(312, 33832, 1024), (617, 25264, 4096), (1654, 9712, 3608), (2048, 11008, 4096), (2048, 4096, 11008)]
+    for M, N, K in shapes:
+        w = F.workspace(int(M), int(N), int(K))
+        assert L.rb_workspace_bytes(_lib.RB_OP_QAT_LINEAR, 1, int(N), int(K), int(M)) == (w and w + (8 * int(N) + 255) // 256 * 256)
+    assert F.tiles(312, 33832, 1024, True)[1] == 0 and F.tiles(617, 25264, 4096, True)[1] == 0
+    assert F.form(2550, 9640, 2064, True) == "128" and F.form(2048, 11008, 4096, True) == "256+128"
+
+
 # ---------------------------------------------------------------------------------------------
 # the oracle's own pins
 # ---------------------------------------------------------------------------------------------
