@@ -18,6 +18,7 @@ import torch
 
 import residual_binarized_weight_amd as rb
 from oracle import block_oracle as BO
+from tests import linear_forms as F
 from tests.gpu_util import dev, long_buffer, pieces
 
 pytestmark = [pytest.mark.gpu,
@@ -393,3 +394,91 @@ def test_batch_rows_past_one_launch():
         check(X[p], W, None, "relu", None, Y[p], None)
     del X, Y
     torch.cuda.empty_cache()
+
+
+# ---------------------------------------------------------------------------------------------
+# every form of the product: what the tests above ask of some shapes, asked of each
+# ---------------------------------------------------------------------------------------------
+FORMS = [
+    ("rows", 1, 131, 96), ("rows", 3, 131, 97), ("rows", 4, 2051, 96), ("few", 67, 131, 96), ("few", 61, 131, 97),
+    ("32", 300, 131, 96), ("32", 300, 131, 97), ("32+join", 300, 131, 2056), ("32+join", 300, 131, 2057),
+    ("64", 900, 2050, 72), ("64", 900, 2050, 73), ("64+join", 513, 67, 8200), ("64+join", 513, 67, 2057),
+    ("128", 1999, 2050, 72), ("128", 1999, 2050, 73), ("128+join", 1300, 67, 8200), ("128+join", 1300, 67, 2057),
+    ("128", 1537, 4100, 515), ("128+join", 1000, 4096, 2050),
+    ("256", 1999, 8190, 72), ("256", 4096, 4096, 200), ("256", 257, 32765, 72), ("256+32", 1999, 8203, 72),
+    ("256+64", 1537, 11003, 72), ("256+128", 2000, 11003, 1024),
+]
+TYPES = [("bf16", "f32", "odd"), ("bf16", "bf16", "lines"), ("f16", "f16", "odd"), ("f16", "f32", "lines")]
+
+
+def form_id(f):
+    return f"{f[0]}-{f[1]}x{f[2]}x{f[3]}"
+
+
+def operands(seed, M, N, K, dt, form):
+    assert F.form(M, N, K, K % 8 == 0) == form
+    torch.manual_seed(seed)
+    return (torch.randn((M, K), device=dev()).to(DT[dt]), torch.randn((N, K), device=dev()).mul_(0.1).to(DT[dt]))
+
+
+def check_on_gpu(X, W, b, act, R, Y, Z):
+    """check() in 64 bits on the GPU, for the large ones."""
+    x, w = X.double(), W.double().t().contiguous()
+    S = x.abs() @ w.abs() + b.double().abs()
+    zo = x @ w + b.double()
+    yo = zo * torch.sigmoid(zo) if act == "silu" else zo
+    a = yo.abs()
+    yo = yo + (0 if R is None else R.double())
+    r = 0 if R is None else R.double().abs()
+    for got, ref, lim, what in ((Z, zo, 2e-5 * S, "Z"),
+                                (Y, yo, 1.13 * 2e-5 * S + 16 * U * (zo.abs() + a) + 2 * U * (yo.abs() + r), "Y")):
+        err = (got.double() - ref).abs()
+        ok = err <= lim + UNIT[got.dtype] * ref.abs() + TINY[got.dtype]
+        assert ok.all(), (what, int((~ok).sum()), (~ok).nonzero()[:3].tolist())
+
+
+@pytest.mark.parametrize("dt,ydt,place", TYPES)
+@pytest.mark.parametrize("form", FORMS, ids=form_id)
+def test_every_form(form, dt, ydt, place):
+    """Bias, activation, residual and kept Z, the outputs inside buffers of 7: rows at odd places with the residual in
+    Y itself, or rows that start 128-byte lines with a residual of its own. Nothing around them is written."""
+    name, M, N, K = form
+    X, W = operands(15, M, N, K, dt, name)
+    b = torch.randn(N, device=dev())
+    ld, o = (N + 9, 3) if place == "odd" else ((N + 63) // 64 * 64 + 64, 0)
+    Yb, Zb = (torch.full((M + 2, ld), 7.0, dtype=DT[t], device=dev()) for t in (ydt, dt))
+    Y, Z = Yb[1:M + 1, o:N + o], Zb[1:M + 1, o:N + o]
+    R = torch.randn((M, N), device=dev()).to(DT[ydt])
+    if place == "odd":
+        Y.copy_(R)
+    rb.qat_linear(X, W, bias=b, act="silu", residual=Y if place == "odd" else R, Y=Y, Z=Z)
+    torch.cuda.synchronize()
+    check_on_gpu(X, W, b, "silu", R, Y, Z)
+    for t in (Yb, Zb):
+        assert torch.all(t[0] == 7) and torch.all(t[M + 1:] == 7) and torch.all(t[:, :o] == 7) and torch.all(t[:, o + N:] == 7)
+
+
+@pytest.mark.parametrize("form", [f for f in FORMS if f[1] < 1000 or f[0] in ("256", "256+32")], ids=form_id)
+def test_non_finite_values_stay_in_their_row_and_column_in_every_form(form):
+    name, M, N, K = form
+    X, W = operands(16, M, N, K, "bf16", name)
+    m, n = (7 if M > 7 else 0), N - 2
+    X[m, 3], W[n, K - 1] = float("nan"), float("inf")
+    Y, _ = rb.qat_linear(X, W, y_dtype=torch.float32)
+    torch.cuda.synchronize()
+    want = torch.zeros((M, N), dtype=torch.bool, device=dev())
+    want[m], want[:, n] = True, True
+    assert torch.equal(~torch.isfinite(Y), want)
+
+
+@pytest.mark.parametrize("form", [f for f in FORMS if f[1:] in ((300, 131, 96), (300, 131, 2057), (1999, 8203, 72))], ids=form_id)
+def test_tiles_on_another_stream(form):
+    name, M, N, K = form
+    X, W = operands(17, M, N, K, "f16", name)
+    b = torch.zeros(N, device=dev())
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        Y, Z = rb.qat_linear(X, W, bias=b, act="silu", save_z=True)
+    s.synchronize()
+    check_on_gpu(X, W, b, "silu", None, Y, Z)
