@@ -5,7 +5,7 @@
 //
 // Every element is read and written once, so the step is bound by HBM: 28 bytes per element with
 // fp32 parameters, gradients and states, 16 with 8-bit states. Measured over three 4096 x 11008
-// weights and their scales (135 M elements): 619 us = 6.1 TB/s in 32 bits, 359 us = 6.1 TB/s in 8.
+// weights and their scales (135 M elements): 621 us = 6.1 TB/s in 32 bits, 362 us = 6.0 TB/s in 8.
 // 256 x 512 with its scales: 6.2 us, a launch and one element's chain of operations.
 //
 // Split. Tensors are cut into chunks of 4096 elements; a map of the chunks (one 32-bit tensor

@@ -91,8 +91,9 @@ struct Epilogue {
   int act;
   bool line_z, line_y;  // every row starts a 128-byte line
 };
-// Streamed where rows start lines (2048 x 11008 x 4096 with Z 190 us against 194); elsewhere a streamed line that
-// two stores write in part goes to memory twice (3441 x 2583 x 640 with Z 58 us against 40).
+// Streamed where rows start lines (2048 x 11008 x 4096 with Z 182 us against 186); elsewhere a streamed line that
+// two stores write in part goes to memory twice (3441 x 2583 x 640 with bias and Z, bf16: 39 us against 31, with
+// operands that are not aligned 48 against 41).
 template <typename T>
 __device__ __forceinline__ void store_out(T* row, int c, int n, const float (&v)[8], bool line) {
   if (line)
@@ -164,12 +165,12 @@ struct TileArgs {
 // they pass through registers one step ahead, by 16-byte loads at any address; the vector that holds the
 // end of the columns is read 8 columns before it and shifted.
 //
-// What bounds it: bringing the operands to LDS. 2048 x 4096 x 11008 (bf16, fp32 stream) takes 172 us
-// from cold memory and 154 warm; its matrix instructions alone take 113, everything but the global loads
-// 128, the loads alone 159 (111 warm). Hence the large tiles (a byte brought serves 64 multiply-adds of a
-// 256 x 256 tile, 43 of a 128 x 256 one) and the ring that keeps kS - 1 steps in flight. Two waves per SIMD:
-// with one (tiles of 4 waves) 192 to 249. 32x32x16 instructions: 202. Weight fragments straight from
-// memory to registers, 16 bytes a row: 244.
+// What bounds it: bringing the operands to LDS. 2048 x 4096 x 11008 (bf16, fp32 stream) takes 176 to 181 us
+// from cold memory and 173 with everything in the cache; taken apart, when it took 172 cold, the matrix
+// instructions alone took 113, everything but the global loads 128, the loads alone 159 (111 warm). Hence the large
+// tiles (a byte brought serves 64 multiply-adds of a 256 x 256 tile, 43 of a 128 x 256 one) and the ring that keeps
+// kS - 1 steps in flight. Against the 172: two waves per SIMD; with one (tiles of 4 waves) 192 to 249. 32x32x16
+// instructions: 202. Weight fragments straight from memory to registers, 16 bytes a row: 244.
 template <typename TA, typename TY, int WM, int WN, int TM, int TN, int kS, bool AL>
 __global__ __launch_bounds__(64 * WM * WN, 2) void linear_tile_kernel(TileArgs a) {
   constexpr int kWaves = WM * WN;
@@ -530,7 +531,7 @@ __global__ __launch_bounds__(512) void linear_few_kernel(TileArgs a) {
 // ---------------------------------------------------------------------------------------------
 // the epilogue's backward: a block owns 512 columns (8 per thread over 64 lanes) and a strip of rows,
 // which its 4 waves take in turn; each thread keeps its columns' sums in fp32. HBM bounds it: 2048 x
-// 11008 in bf16 30 us for 135 MB, 4.5 TB/s, and 4 us for the sums.
+// 11008 in bf16 31.7 us for 135 MB, 4.3 TB/s, of which 4 for the sums.
 // ---------------------------------------------------------------------------------------------
 struct GradArgs {
   const void *dY, *Z;

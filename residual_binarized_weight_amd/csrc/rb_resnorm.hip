@@ -10,9 +10,11 @@
 // other: by DPP inside a wave, through LDS between waves. All sums are fp32; the mean is taken
 // before the squares, so a large mean costs no digits.
 //
-// Measured (bf16, fp32 stream, rms norms, a gate per channel): forward 2048 x 4096 18 to 19 us, 101 MB
-// = 5.3 TB/s, about what a copy reaches; one row 3 us. Stores are streamed (nothing here reads them
-// again): 23.7 us without.
+// Measured (bf16, fp32 stream, rms norms, a gate per channel): forward 2048 x 4096 18 us, 101 MB = 5.5 TB/s,
+// about what a copy reaches; one row 3 us. Stores are streamed (nothing here reads them again): 23.7 us
+// without. Wide rows, 16 columns per thread from 8193 on: 2048 x 8192 41 us, x 12000 72 us (4.1 TB/s), x 16384 89 us
+// (4.5 TB/s). Narrow ones leave lanes without work: 16384 x 512 18 us, 65536 x 128, 16 lanes of 64, 34 us for the
+// same bytes (backward 39 and 92).
 #include "rb_elem.hpp"
 #include "rb_internal.h"
 #include <type_traits>
@@ -444,7 +446,7 @@ __global__ __launch_bounds__(bwd_threads(TPR)) void resnorm_backward_kernel(
 // beside the row: one kernel takes the two norms' means of every row (a row's chunks are read twice, the
 // second time from L2), the other walks down strips of rows, 512 columns wide, with the sums in registers.
 // Every tensor is read from memory twice, and dY and dR may still replace what they are made of. 2048 x 12000,
-// bf16, rms norms and a gate per channel: 75 + 79 us and 5 for the sums with an fp32 stream; the row in one
+// bf16, rms norms and a gate per channel: 152 to 159 us (75 + 79 and 5 for the sums) with an fp32 stream; the row in one
 // block of 1024 threads with 16 columns each, sums in spilled registers, took 486. Up to 8192 columns one
 // reading is faster: 2048 x 8192 76 us and 6.
 // ---------------------------------------------------------------------------------------------
