@@ -203,6 +203,39 @@ def test_8bit_step_follows_the_definition(offset):
         chunk += (n + 4095) // 4096
 
 
+def test_8bit_step_past_32_bits():
+    """One tensor of over 2^32 elements: offsets, scales and the random numbers' positions on both sides of 2^32."""
+    n, step, seed = (1 << 32) + 3 * 4096 + 77, 3, 99
+    torch.manual_seed(106)
+    p, g = torch.empty(n, dtype=torch.bfloat16, device=dev()).normal_(), torch.empty(n, dtype=torch.bfloat16, device=dev()).normal_()
+    m, v = (torch.randint(0, 0x79, (n,), dtype=torch.uint8, device=dev()) for _ in range(2))
+    ms, vs = (torch.full(((n + 255) // 256,), 0.5, device=dev()) for _ in range(2))
+    parts = [slice(0, 512), slice((1 << 32) - 512, (1 << 32) + 512), slice(n - 77 - 256, n)]
+    group = [slice(s.start // 256, (s.stop + 255) // 256) for s in parts]
+    before = [[np64(p[s]), np64(g[s]), m[s].cpu().numpy(), v[s].cpu().numpy()] for s in parts]
+    plan = rb.adamw_plan([p], [g], state_bits=8, m=[m.view(torch.float8_e4m3fn)], v=[v.view(torch.float8_e4m3fn)],
+                         m_scale=[ms], v_scale=[vs])
+    rb.adamw_step(plan, step, seed=seed, **HYPER)
+    torch.cuda.synchronize()
+    b1, b2 = HYPER["beta1"], HYPER["beta2"]
+    for s, q, (p0, g0, mc, vc) in zip(parts, group, before):
+        half = np.full(q.stop - q.start, 0.5)
+        m0, r0 = BO.adamw_decode(mc, half), BO.adamw_decode(vc, half)
+        po, mo, vo = BO.adamw(p0, g0, m0, r0 * r0, step, HYPER["lr"], b1, b2, HYPER["eps"])
+        mt = b1 * np.abs(m0) + (1 - b1) * np.abs(g0)
+        h = BO.adamw_random(np.arange(s.start, s.stop), step, seed)
+        # bf16 gradients meet the states' few values: sums that cancel to within their own error may have either sign
+        codes = m[s].cpu().numpy()
+        mo = np.where(np.abs(mo) <= 4 * U * mt, np.copysign(mo, BO.E4M3[codes]), mo)
+        check_codes(mo, 4 * U * mt, codes, np64(ms[q]), h & 0xFFFF, False)
+        check_codes(np.sqrt(vo), 5 * U * np.sqrt(vo), v[s].cpu().numpy(), np64(vs[q]), h >> 16, True)
+        den = np.sqrt(vo / (1 - b2 ** step)) + HYPER["eps"]
+        lim = 3 * U * np.abs(p0) + 20 * U * HYPER["lr"] * mt / (1 - b1 ** step) / den + (U + UNIT["bf16"]) * np.abs(po)
+        assert np.all(np.abs(np64(p[s]) - po) <= lim + TINY["bf16"])
+    del p, g, m, v, plan
+    torch.cuda.empty_cache()
+
+
 def test_8bit_unchanged_state_is_stored_unchanged():
     """1 - 2^-53 rounds to 1: with no gradient the states stay, and their values must be stored again
     exactly. A group whose largest magnitude equals its scale (code 0x78) takes the next power of two,

@@ -396,6 +396,20 @@ def test_batch_rows_past_one_launch():
     torch.cuda.empty_cache()
 
 
+def test_backward_offsets_past_32_bits():
+    """4.3 G elements a tensor, dZ in place of dY."""
+    M, N = (1 << 29) + 77, 8
+    dY, Z = long_buffer(M, N, DT["f16"]), long_buffer(M, N, DT["f16"])
+    some = [n64(dY[p]) for p in pieces(M)]
+    _, db = rb.qat_linear_backward(dY, Z, act="silu", dZ=dY)
+    for p, d in zip(pieces(M), some):
+        z = n64(Z[p])
+        near(dY[p], BO.linear_backward(d, z, "silu")[0], 24 * U * (1 + np.abs(z)) * np.abs(d), "dZ")
+    assert torch.isfinite(db).all()
+    del dY, Z
+    torch.cuda.empty_cache()
+
+
 # ---------------------------------------------------------------------------------------------
 # every form of the product: what the tests above ask of some shapes, asked of each
 # ---------------------------------------------------------------------------------------------

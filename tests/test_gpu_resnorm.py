@@ -383,3 +383,20 @@ def test_backward_wide_rows_past_one_launch():
     assert torch.isfinite(got["dw_pre"]).all()
     del dX, S, got
     torch.cuda.empty_cache()
+
+
+def test_backward_offsets_past_32_bits():
+    """Rows up to 8192 columns, walked by 256 blocks: 4.3 G elements a tensor, in place."""
+    M, D = (1 << 22) + 7, 1030
+    dX, S = long_buffer(M, D, DT["f16"]), long_buffer(M, D, DT["f16"])
+    w = vec(np.random.default_rng(105), D)
+    st = torch.zeros((M, 4), device=dev())
+    st[:, 3] = 1.0
+    some = [(dX[p].clone(), S[p].clone()) for p in pieces(M)]
+    got = rb.resnorm_backward(dX, None, S, S, st, w, dY=dX)
+    for p, (x, s) in zip(pieces(M), some):
+        want = rb.resnorm_backward(x, None, s, s, st[p], w)
+        assert torch.equal(got["dY"][p], want["dY"]) and torch.equal(got["dR"][p], want["dR"])
+    assert torch.isfinite(got["dw_pre"]).all()
+    del dX, S, got
+    torch.cuda.empty_cache()
