@@ -68,7 +68,11 @@ typedef enum rb_op {
   RB_OP_QAT_BACKWARD = 6,
   RB_OP_RESNORM_BACKWARD = 7,      /* k = K = 1, N = D */
   RB_OP_QAT_LINEAR = 8,            /* k = 1 */
-  RB_OP_QAT_LINEAR_BACKWARD = 9    /* k = K = 1 */
+  RB_OP_QAT_LINEAR_BACKWARD = 9,   /* k = K = 1 */
+  RB_OP_QAT_GLU = 10,              /* k = 1 */
+  RB_OP_QAT_GLU_BACKWARD = 11,     /* k = K = 1 */
+  RB_OP_QAT_GLU_DX = 12,           /* k = 1; N the hidden width, K that of dX */
+  RB_OP_MUON_STEP = 13             /* k = M = 1 */
 } rb_op;
 
 /* Version of this ABI (major*10000 + minor*100 + patch). */
@@ -400,7 +404,7 @@ rb_status rb_qat_matmul(const void* X, rb_dtype a_dtype, int64_t M, int64_t ldx,
 
 /* rb_qat_backward -- from the forward's X, What and planes and the incoming dY:
  *   dW   output [N][lddw] fp32 (lddw >= K), the shared weight's gradient
- *   dX   output [M][lddx] (lddx >= K), dx_dtype RB_F32 or a_dtype
+ *   dX   output [M][lddx] (lddx >= K), dx_dtype RB_F32 or a_dtype; NULL: not computed
  *   dg   output [k][N] fp32;  dh  output [k][K] fp32 (fixed-order fp32 sums: deterministic for
  *        a given dW)
  *   ws   rb_workspace_bytes(RB_OP_QAT_BACKWARD, k, N, K, M) bytes, 16-byte aligned, for the
@@ -455,6 +459,51 @@ rb_status rb_qat_linear(const void* X, rb_dtype a_dtype, int64_t M, int64_t ldx,
 rb_status rb_qat_linear_backward(const void* dY, rb_dtype dy_dtype, int64_t M, int64_t N, int64_t lddy, const void* Z,
                                  rb_dtype a_dtype, int64_t ldz, int32_t act, void* dZ, int64_t lddz, float* db, void* ws,
                                  size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------------
+ * rb_qat_glu* -- the first half of a gated feed-forward block: both projections, the activation and the product
+ * in one kernel, and its backward. (The second half is rb_qat_linear on H.)
+ *
+ * rb_qat_glu
+ *     G = X Wg^T + bg;  U = X Wu^T + bu;  H = act(G) (.) U
+ *   on the library's matrix-core kernels with fp32 sums; H is computed from the fp32 G and U.
+ *   X [M][ldx], Wg [N][ldwg], Wu [N][ldwu] in a_dtype (RB_F16 or RB_BF16), any alignment of rows (16-byte aligned
+ *   operands with leading dimensions and K multiples of 8 are the fast case)
+ *   1 <= M, N, K; N, K <= 2^28, M below 2^31; leading dimensions below 2^31
+ *   bg, bu   fp32 [N] or NULL;  act  rb_act, of G (SILU: the swish gate; NONE: a bilinear one)
+ *   G, U     [M][ldg], [M][ldu] in a_dtype: rounded, for rb_qat_glu_backward; each may be NULL
+ *   H        [M][ldh] in h_dtype, RB_F32 or a_dtype. No output may overlap an input or another output.
+ *   ws       rb_workspace_bytes(RB_OP_QAT_GLU, 1, N, K, M) bytes (may be 0: NULL), 16-byte aligned: the partial
+ *            sums of tiles that are split over the GPU, joined in a fixed order (deterministic); no zero-filling needed.
+ *
+ * rb_qat_glu_backward -- from dH, the gradient of H, and the forward's G and U:
+ *     dG = dH (.) U (.) act'(G);  dU = dH (.) act(G)  (slopes as in rb_qat_linear_backward)
+ *   and the biases' gradients, the column sums of the unrounded dG and dU in fp32, in a fixed order.
+ *   dH       [M][lddh] in dh_dtype, RB_F32 or a_dtype;  G [M][ldg], U [M][ldu] in a_dtype
+ *   dG, dU   outputs [M][lddg], [M][lddu] in a_dtype: what rb_qat_glu_dx and rb_qat_backward take. Each may be any one of
+ *            dH, G and U (same type and leading dimension), but not the same one.
+ *   dbg, dbu outputs fp32 [N], each may be NULL
+ *   ws       rb_workspace_bytes(RB_OP_QAT_GLU_BACKWARD, 1, N, 1, M) bytes, 16-byte aligned (NULL if that is 0
+ *            or dbg and dbu are NULL); no zero-filling needed.
+ *
+ * rb_qat_glu_dx -- the input's gradient, both products in one run of fp32 sums:
+ *     dX = dG Wg + dU Wu
+ *   dG [M][lddg], dU [M][lddu], Wg [N][ldwg], Wu [N][ldwu] in a_dtype, any alignment (fast: 16 bytes, leading
+ *   dimensions, N and K multiples of 8);  dX [M][lddx] in dx_dtype, RB_F32 or a_dtype; it overlaps no input
+ *   ws       rb_workspace_bytes(RB_OP_QAT_GLU_DX, 1, N, K, M) bytes as for rb_qat_glu
+ *   The weights' gradients, dWg = dG^T X and dWu = dU^T X, with those of their scales: rb_qat_backward with dX NULL.
+ * --------------------------------------------------------------------------------------- */
+rb_status rb_qat_glu(const void* X, rb_dtype a_dtype, int64_t M, int64_t ldx, const void* Wg, int64_t ldwg, const void* Wu,
+                     int64_t ldwu, int64_t N, int64_t K, const float* bg, const float* bu, int32_t act, void* G,
+                     int64_t ldg, void* U, int64_t ldu, void* H, rb_dtype h_dtype, int64_t ldh, void* ws, size_t ws_bytes,
+                     void* stream);
+rb_status rb_qat_glu_backward(const void* dH, rb_dtype dh_dtype, int64_t M, int64_t N, int64_t lddh, const void* G,
+                              int64_t ldg, const void* U, int64_t ldu, rb_dtype a_dtype, int32_t act, void* dG,
+                              int64_t lddg, void* dU, int64_t lddu, float* dbg, float* dbu, void* ws, size_t ws_bytes,
+                              void* stream);
+rb_status rb_qat_glu_dx(const void* dG, int64_t lddg, const void* dU, int64_t lddu, rb_dtype a_dtype, int64_t M,
+                        const void* Wg, int64_t ldwg, const void* Wu, int64_t ldwu, int64_t N, int64_t K, void* dX,
+                        rb_dtype dx_dtype, int64_t lddx, void* ws, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------------------
  * rb_resnorm_* -- the norms between two blocks, in one pass: the norm after a block, its gate, the
@@ -565,6 +614,66 @@ rb_status rb_adamw_plan(const rb_adamw_tensor* t, int64_t count, int32_t state_b
 rb_status rb_adamw_step(const void* plan, int64_t chunks, int32_t state_bits, int64_t step, double lr, double beta1,
                         double beta2, double eps, const float* grad_scale, const int32_t* skip, uint32_t seed,
                         void* stream);
+
+/* ---------------------------------------------------------------------------------------
+ * rb_muon_step -- an optimizer step of one matrix (a shared weight of coupled training) by momentum and
+ * Newton-Schulz products, which bring the update's singular values near 1.
+ *     m <- momentum m + s G;  u = s G + momentum m with nesterov, else m  (u = s G without a momentum buffer)
+ *     X = u / (||u||_F + eps);  `steps` times: A = X X^T, X <- a X + (b A + c A^2) X, (a, b, c) = (3.4445, -4.7750, 2.0315)
+ *     W <- W (1 - lr weight_decay) - lr scale X;  O = X
+ *   (of a matrix with N > K the transpose is iterated, which gives the same X). m, u, the norm (sums in fp64) and the
+ *   update are fp32; the products take fp16 operands and sum in fp32, X is held in two fp16: X is off by about 0.1 to
+ *   0.2 % in the Frobenius norm. A NaN or infinity in u makes X, and with it W, NaN; u = 0 gives X = 0.
+ *   W        [N][ldw] fp32, updated in place, or NULL (only m and O are written)
+ *   G        [N][ldg] in g_dtype, RB_F32, RB_F16 or RB_BF16
+ *   mom      [N][ldm] fp32, updated in place, or NULL (momentum and nesterov are then not used)
+ *   O        output [N][ldo] in o_dtype, RB_F16 or RB_BF16, or NULL; one of W and O at least. No buffer overlaps another.
+ *   N, K     1 .. 2^21 - 1; leading dimensions >= K, below 2^31
+ *   lr, scale, weight_decay   finite and >= 0; 0 <= momentum < 1; eps finite and > 0 as an fp32; steps 1 .. 16
+ *   grad_scale  s: optional device fp32;  skip  optional device int32: the step changes nothing if it is not 0
+ *   ws       rb_workspace_bytes(RB_OP_MUON_STEP, 1, N, K, 1) bytes, 16-byte aligned; no zero-filling needed.
+ *            (0 for sizes out of range.) Equal inputs give equal results.
+ * --------------------------------------------------------------------------------------- */
+rb_status rb_muon_step(float* W, int64_t ldw, const void* G, rb_dtype g_dtype, int64_t ldg, float* mom, int64_t ldm,
+                       int64_t N, int64_t K, double lr, double momentum, int32_t nesterov, double weight_decay,
+                       double scale, int32_t steps, double eps, const float* grad_scale, const int32_t* skip, void* O,
+                       rb_dtype o_dtype, int64_t ldo, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------------
+ * rb_q4_* -- 4-bit weights with group scales, for the layers that are not binarized.
+ *     What[n][c] = s (q - 8), or s q + z with offsets;  q = 0 .. 15, one s (and z) per row n and `group` columns
+ * Format
+ *   codes    tiles of 16 rows by 128 columns, [ceil(N / 16)][ceil(K / 128)][64][4] uint32 (rb_q4_codes_bytes bytes),
+ *            16-byte aligned: words 16 j + r of a tile belong to its row r, word i of them to columns 32 i + 8 j .. + 7,
+ *            column c of these in the four bits from 16 (c % 2) + 4 (c / 2) on. Codes past the rows and columns are 0.
+ *   s, z     fp16 [ceil(K / group)][N]; z NULL: no offsets
+ *   group    32, 64 or 128;  1 <= N, K <= 2^28
+ *
+ * rb_q4_pack -- from W [N][ldw] (RB_F32, RB_F16, RB_BF16): every step in fp32, s and z rounded to fp16 (to nearest even)
+ *     without offsets:  s = max|W| * (1 / 7), q = clamp(rint(W / s), -8, 7) + 8
+ *     with z:           z = min W, s = (max W - min W) * (1 / 15), q = clamp(rint((W - z) / s), 0, 15)
+ *   over the group (W / s is taken as 0 where s is 0). d_status: optional device int32; the call ORs 1 into it if W
+ *   holds a NaN or an infinity or a scale overflows (outputs of that group are then unspecified).
+ *
+ * rb_q4_dequant -- What [N][ldw] in w_dtype: s (q - 8) or s q + z, rounded once. What rb_qat_linear and rb_qat_glu take
+ *   for larger batches.
+ *
+ * rb_q4_gemv -- y [M][ldy] = x What^T for x [M][ldx] in x_dtype (RB_F16 or RB_BF16, any alignment), 1 <= M <= 16 (larger:
+ *   RB_ERR_UNSUPPORTED), fp32 sums, y in y_dtype, RB_F32 or x_dtype. x must be finite: an infinity gives NaN in its row.
+ * rb_q4_glu -- y = act(x Wg^T) (.) (x Wu^T) in one launch, both weights N x K with one group size; each with or
+ *   without offsets.
+ *   The calls need no workspace; sums are in a fixed order (deterministic).
+ * --------------------------------------------------------------------------------------- */
+size_t rb_q4_codes_bytes(int64_t N, int64_t K); /* 0 for sizes out of range */
+rb_status rb_q4_pack(const void* W, rb_dtype w_dtype, int64_t N, int64_t K, int64_t ldw, int32_t group, uint32_t* codes,
+                     void* s, void* z, int32_t* d_status, void* stream);
+rb_status rb_q4_dequant(const uint32_t* codes, const void* s, const void* z, int64_t N, int64_t K, int32_t group, void* What,
+                        rb_dtype w_dtype, int64_t ldw, void* stream);
+rb_status rb_q4_gemv(const uint32_t* codes, const void* s, const void* z, int64_t N, int64_t K, int32_t group, const void* x,
+                     rb_dtype x_dtype, int64_t M, int64_t ldx, void* y, rb_dtype y_dtype, int64_t ldy, void* stream);
+rb_status rb_q4_glu(const uint32_t* codes_g, const void* s_g, const void* z_g, const uint32_t* codes_u, const void* s_u,
+                    const void* z_u, int64_t N, int64_t K, int32_t group, int32_t act, const void* x, rb_dtype x_dtype,
+                    int64_t M, int64_t ldx, void* y, rb_dtype y_dtype, int64_t ldy, void* stream);
 
 #ifdef __cplusplus
 }

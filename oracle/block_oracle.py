@@ -181,3 +181,96 @@ def adamw_grid(x, scales):
     """(a, grid): |x| in units of scale / 256 and the spacing of e4m3 numbers there."""
     a = np.abs(_f(x)) / np.repeat(scales, 256)[:np.size(x)] * 256.0
     return a, np.ldexp(1.0, np.maximum(np.frexp(a)[1] - 1, -6) - 3)
+
+
+# ---------------------------------------------------------------------------------------------
+# gated feed-forward block
+# ---------------------------------------------------------------------------------------------
+def glu(X, Wg, Wu, bg=None, bu=None, act: str = "silu"):
+    """(H, G, U): G = X Wg^T + bg, U = X Wu^T + bu, H = act(G) U."""
+    G, U = linear(X, Wg, bg)[1], linear(X, Wu, bu)[1]
+    return activation(G, act)[0] * U, G, U
+
+
+def glu_backward(dH, G, U, act: str = "silu"):
+    """(dG, dU, dbg, dbu) of H = act(G) U."""
+    value, slope = activation(G, act)
+    dG, dU = _f(dH) * _f(U) * slope, _f(dH) * value
+    return dG, dU, dG.sum(axis=0), dU.sum(axis=0)
+
+
+def glu_dx(dG, dU, Wg, Wu):
+    return _f(dG) @ _f(Wg) + _f(dU) @ _f(Wu)
+
+
+# ---------------------------------------------------------------------------------------------
+# Newton-Schulz step
+# ---------------------------------------------------------------------------------------------
+NS_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
+
+
+def newton_schulz(u, steps: int = 5, eps: float = 1e-7):
+    """X of u: its singular values taken through x -> a x + b x^3 + c x^5, `steps` times, after division by
+    the Frobenius norm plus eps. From the singular value decomposition, so by another way than products."""
+    u = _f(u)
+    P, s, Q = np.linalg.svd(u, full_matrices=False)
+    s = s / (math.sqrt((u * u).sum()) + eps)
+    a, b, c = NS_COEFFICIENTS
+    for _ in range(steps):
+        s = a * s + b * s ** 3 + c * s ** 5
+    return (P * s) @ Q
+
+
+def muon(W, G, mom, lr, momentum=0.95, nesterov=True, weight_decay=0.0, scale=1.0, steps=5, eps=1e-7, grad_scale=1.0):
+    """(W, mom, X) after one step; mom may be None."""
+    g = _f(G) * grad_scale
+    m = None if mom is None else momentum * _f(mom) + g
+    u = g if m is None else g + momentum * m if nesterov else m
+    X = newton_schulz(u, steps, eps)
+    return (None if W is None else _f(W) * (1.0 - lr * weight_decay) - lr * scale * X), m, X
+
+
+# ---------------------------------------------------------------------------------------------
+# 4-bit weights with group scales
+# ---------------------------------------------------------------------------------------------
+def q4_quantise(W, group: int, offset: bool):
+    """(codes [N][K], s [groups][N], z [groups][N] or None) of fp32 weights; s and z are fp16, every other
+    step is rounded to fp32, as the definition says."""
+    W = np.asarray(W, dtype=np.float32)
+    N, K = W.shape
+    groups = -(-K // group)
+    q = np.zeros((N, K), dtype=np.int64)
+    s, z = np.zeros((groups, N), dtype=np.float16), np.zeros((groups, N), dtype=np.float16)
+    for g in range(groups):
+        w = W[:, g * group:(g + 1) * group]
+        if offset:
+            lo, hi = w.min(axis=1), w.max(axis=1)
+            z[g] = lo.astype(np.float16)
+            s[g] = ((hi - lo) * np.float32(1 / np.float32(15))).astype(np.float16)
+            d, first, last = w - z[g].astype(np.float32)[:, None], 0, 15
+        else:
+            s[g] = (np.abs(w).max(axis=1) * np.float32(1 / np.float32(7))).astype(np.float16)
+            d, first, last = w, -8, 7
+        sf = s[g].astype(np.float32)[:, None]
+        with np.errstate(divide="ignore", invalid="ignore"):
+            r = np.where(sf > 0, np.rint(d / sf), np.float32(0))
+        q[:, g * group:(g + 1) * group] = np.clip(r, first, last).astype(np.int64) - first
+    return q, s, z if offset else None
+
+
+def q4_codes(q):
+    """Codes [N][K] in the packed layout, [ceil(N / 16)][ceil(K / 128)][64][4] uint32, written entry by entry."""
+    N, K = q.shape
+    out = np.zeros((-(-N // 16), -(-K // 128), 64, 4), dtype=np.uint32)
+    n, c = np.meshgrid(np.arange(N), np.arange(K), indexing="ij")
+    lane = 16 * (c % 32 // 8) + n % 16
+    bit = 16 * (c % 2) + 4 * (c % 8 // 2)
+    np.bitwise_or.at(out, (n // 16, c // 128, lane, c % 128 // 32), q.astype(np.uint32) << bit.astype(np.uint32))
+    return out
+
+
+def q4_values(q, s, z, group: int):
+    """The weights that codes stand for."""
+    at = np.arange(q.shape[1]) // group
+    sc = _f(s)[at].T
+    return sc * (q - 8) if z is None else sc * q + _f(z)[at].T

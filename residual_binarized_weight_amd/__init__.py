@@ -18,9 +18,17 @@ return CUDA (HIP) tensors on the current device and enqueue on the current strea
   qat_autotune(X, dY, What, Y, dW, dX)           pick the fastest GEMM kernels for a shape
   Y, Z = qat_linear(X, What, bias, act, residual)   Y = act(X What^T + bias) + residual
   dZ, db = qat_linear_backward(dY, Z, act)       ... and its epilogue's gradients
+  H, G, U = qat_glu(X, Wg, Wu, act)              a gated block's first half: H = act(X Wg^T + bg) (X Wu^T + bu)
+  dG, dU, dbg, dbu = qat_glu_backward(dH, G, U, act)   ... its epilogue's gradients
+  dX = qat_glu_dx(dG, dU, Wg, Wu)                ... and its input's: dG Wg + dU Wu
   S, X, stats = resnorm_forward(Y, R, w_pre)     S = alpha R + gate norm_post(Y), X = norm_pre(S)
   grads = resnorm_backward(dX, dS, Y, S, stats, w_pre)   ... and its gradients
   adamw_step(plan, step, lr)                     AdamW over many tensors (adamw_plan), states in 32 or 8 bits
+  muon_step(W, G, mom, lr)                       a matrix's step by momentum and Newton-Schulz products
+  O = orthogonalize(G)                           ... those products alone
+  codes, s, z = q4_pack(W, group)                4-bit weights with group scales; q4_dequant reads them back
+  y = q4_gemv(codes, s, z, x, N)                 y = x What^T on 4-bit weights, M <= 16
+  y = q4_glu(Wg, Wu, x, N, act)                  ... and the gated pair act(x Wg^T) (x Wu^T)
 """
 from __future__ import annotations
 
@@ -31,12 +39,14 @@ import torch
 
 from . import _lib
 from ._lib import (RB_F16, RB_F32, RB_BF16, RB_OP_CODEBOOK_GEMV, RB_OP_GEMM_SMALL, RB_OP_GEMV,
-                   RB_OP_QAT_BACKWARD, RB_OP_QAT_LINEAR, RB_OP_QAT_LINEAR_BACKWARD, RB_OP_RESNORM_BACKWARD, RB_OP_SVID_INIT, RB_QAT_ENGINE_AUTO, RB_QAT_ENGINE_MFMA,
+                   RB_OP_MUON_STEP, RB_OP_QAT_BACKWARD, RB_OP_QAT_GLU, RB_OP_QAT_GLU_BACKWARD, RB_OP_QAT_GLU_DX,
+                   RB_OP_QAT_LINEAR, RB_OP_QAT_LINEAR_BACKWARD, RB_OP_RESNORM_BACKWARD, RB_OP_SVID_INIT, RB_QAT_ENGINE_AUTO, RB_QAT_ENGINE_MFMA,
                    RB_QAT_ENGINE_ROCBLAS, RbError, check, lib)
 
 __all__ = ["pack", "gemv", "gemv_variant", "gemm_small", "codebook_encode", "codebook_gemv", "codebook_mstep",
            "codebook_distinct", "codebook_learn", "svid_init", "qat_derive",
-           "qat_forward", "qat_matmul", "qat_backward", "qat_autotune", "qat_linear", "qat_linear_backward", "resnorm_forward",
+           "qat_forward", "qat_matmul", "qat_backward", "qat_autotune", "qat_linear", "qat_linear_backward", "qat_glu", "qat_glu_backward",
+           "qat_glu_dx", "muon_step", "orthogonalize", "q4_pack", "q4_dequant", "q4_gemv", "q4_glu", "resnorm_forward",
            "resnorm_backward", "adamw_plan", "adamw_step", "AdamWPlan", "workspace",
            "workspace_bytes", "storage_bits_per_weight", "version", "RbError", "lib"]
 
@@ -317,15 +327,19 @@ def qat_matmul(X: torch.Tensor, What: torch.Tensor, Y: torch.Tensor | None = Non
 
 def qat_backward(dY: torch.Tensor, X: torch.Tensor, What: torch.Tensor, planes: torch.Tensor, g: torch.Tensor,
                  h: torch.Tensor, dx_dtype=None, ws: torch.Tensor | None = None, dW: torch.Tensor | None = None,
-                 dX: torch.Tensor | None = None, dg: torch.Tensor | None = None, dh: torch.Tensor | None = None):
+                 dX: torch.Tensor | None = None, dg: torch.Tensor | None = None, dh: torch.Tensor | None = None,
+                 need_dx: bool = True):
     """Coupled-training backward from dY [M][N]: dW = dY^T X (fp32 [N][K]), dX = dY What
-    ([M][K], dx_dtype fp32 or the activation type), dg [k][N] and dh [k][K] (fp32)."""
+    ([M][K], dx_dtype fp32 or the activation type), dg [k][N] and dh [k][K] (fp32). Without `need_dx`
+    dX is not computed and None is returned for it (qat_glu_dx gives a gated block's)."""
+    if not need_dx and dX is not None:
+        raise ValueError("a dX to write needs need_dx")
     M, N = dY.shape
     K = X.shape[1]
     k = g.shape[0]
     dev = dY.device
     dW = torch.empty((N, K), dtype=torch.float32, device=dev) if dW is None else dW
-    dX = torch.empty((M, K), dtype=dx_dtype or X.dtype, device=dev) if dX is None else dX
+    dX = torch.empty((M, K), dtype=dx_dtype or X.dtype, device=dev) if dX is None and need_dx else dX
     dg = torch.empty((k, N), dtype=torch.float32, device=dev) if dg is None else dg
     dh = torch.empty((k, K), dtype=torch.float32, device=dev) if dh is None else dh
     if ws is None:
@@ -333,8 +347,8 @@ def qat_backward(dY: torch.Tensor, X: torch.Tensor, What: torch.Tensor, planes: 
     check("rb_qat_backward", lib.rb_qat_backward(_ptr_rows(dY), _dt(dY.dtype), M, dY.stride(0), _ptr_rows(X), X.stride(0),
                                                  _ptr_rows(What), What.stride(0), _ptr_rows(planes), planes.stride(1),
                                                  _ptr(g), _ptr(h), k, N, K, _ptr_rows(dW), dW.stride(0), _ptr_rows(dX),
-                                                 _dt(dX.dtype), dX.stride(0), _ptr(dg), _ptr(dh), _ptr(ws),
-                                                 ws.numel(), _stream()))
+                                                 _dt((X if dX is None else dX).dtype), 0 if dX is None else dX.stride(0),
+                                                 _ptr(dg), _ptr(dh), _ptr(ws), ws.numel(), _stream()))
     return dW, dX, dg, dh
 
 
@@ -439,6 +453,86 @@ def qat_linear_backward(dY: torch.Tensor, Z: torch.Tensor | None, act: str = "no
                                                                dzp, lddz, _vec("db", db, N), _ptr(ws),
                                                                0 if ws is None else ws.numel(), _stream()))
     return dZ, db
+
+
+def qat_glu(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: str = "silu", bias_g: torch.Tensor | None = None,
+            bias_u: torch.Tensor | None = None, h_dtype=None, save: bool = False, H: torch.Tensor | None = None,
+            G: torch.Tensor | None = None, U: torch.Tensor | None = None, ws: torch.Tensor | None = None):
+    """The first half of a gated feed-forward block in one kernel: G = X Wg^T + bias_g, U = X Wu^T + bias_u,
+    H = act(G) U, for X [M][K], Wg and Wu [N][K] (fp16 or bf16, rows may be strided), fp32 biases [N] and
+    `act` as for qat_linear. Returns (H, G, U): H [M][N] in X's type (default) or fp32; G and U, in X's type, are
+    kept for the backward if `save` or given, else None."""
+    M, K = X.shape
+    N = Wg.shape[0]
+    dt = X.dtype
+    if H is None:
+        H = torch.empty((M, N), dtype=h_dtype or dt, device=X.device)
+    if save:
+        G = torch.empty((M, N), dtype=dt, device=X.device) if G is None else G
+        U = torch.empty((M, N), dtype=dt, device=X.device) if U is None else U
+    n = _ws_bytes(RB_OP_QAT_GLU, N, K, M)
+    if ws is None and n:
+        ws = torch.empty(n, dtype=torch.uint8, device=X.device)
+    xp, ldx = _rows("X", X, M, K, dt)
+    gwp, ldwg = _rows("Wg", Wg, N, K, dt)
+    uwp, ldwu = _rows("Wu", Wu, N, K, dt)
+    hp, ldh = _rows("H", H, M, N, H.dtype)
+    gp, ldg = _rows("G", G, M, N, dt)
+    up, ldu = _rows("U", U, M, N, dt)
+    check("rb_qat_glu", lib.rb_qat_glu(xp, _dt(dt), M, ldx, gwp, ldwg, uwp, ldwu, N, K, _vec("bias_g", bias_g, N),
+                                       _vec("bias_u", bias_u, N), _ACT[act], gp, ldg, up, ldu, hp, _dt(H.dtype), ldh,
+                                       _ptr(ws), 0 if ws is None else ws.numel(), _stream()))
+    return H, G, U
+
+
+def qat_glu_backward(dH: torch.Tensor, G: torch.Tensor, U: torch.Tensor, act: str = "silu", bias: bool = False,
+                     dG: torch.Tensor | None = None, dU: torch.Tensor | None = None, dbg: torch.Tensor | None = None,
+                     dbu: torch.Tensor | None = None, ws: torch.Tensor | None = None):
+    """The gated epilogue's gradients from dH [M][N] (fp32 or the activation type) and the forward's G and U:
+    (dG, dU, dbg, dbu), dG = dH U act'(G) and dU = dH act(G) in the activation type and, with `bias` (or where
+    given), their column sums, fp32 [N], else None. dG and dU may be written over dH, G or U (not both over one)."""
+    M, N = dH.shape
+    dt = G.dtype
+    dev = dH.device
+    dG = torch.empty((M, N), dtype=dt, device=dev) if dG is None else dG
+    dU = torch.empty((M, N), dtype=dt, device=dev) if dU is None else dU
+    if bias:
+        dbg = torch.empty(N, dtype=torch.float32, device=dev) if dbg is None else dbg
+        dbu = torch.empty(N, dtype=torch.float32, device=dev) if dbu is None else dbu
+    n = 0 if dbg is None and dbu is None else _ws_bytes(RB_OP_QAT_GLU_BACKWARD, N, 1, M)
+    if ws is None and n:
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    hp, lddh = _rows("dH", dH, M, N, dH.dtype)
+    gp, ldg = _rows("G", G, M, N, dt)
+    up, ldu = _rows("U", U, M, N, dt)
+    dgp, lddg = _rows("dG", dG, M, N, dt)
+    dup, lddu = _rows("dU", dU, M, N, dt)
+    check("rb_qat_glu_backward", lib.rb_qat_glu_backward(hp, _dt(dH.dtype), M, N, lddh, gp, ldg, up, ldu, _dt(dt), _ACT[act],
+                                                         dgp, lddg, dup, lddu, _vec("dbg", dbg, N), _vec("dbu", dbu, N),
+                                                         _ptr(ws), 0 if ws is None else ws.numel(), _stream()))
+    return dG, dU, dbg, dbu
+
+
+def qat_glu_dx(dG: torch.Tensor, dU: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, dx_dtype=None,
+               dX: torch.Tensor | None = None, ws: torch.Tensor | None = None):
+    """The gated block's input gradient dX [M][K] = dG Wg + dU Wu (one kernel, fp32 sums over both products), in the
+    operands' type (default) or fp32."""
+    M, N = dG.shape
+    K = Wg.shape[1]
+    dt = dG.dtype
+    if dX is None:
+        dX = torch.empty((M, K), dtype=dx_dtype or dt, device=dG.device)
+    n = _ws_bytes(RB_OP_QAT_GLU_DX, N, K, M)
+    if ws is None and n:
+        ws = torch.empty(n, dtype=torch.uint8, device=dG.device)
+    gp, lddg = _rows("dG", dG, M, N, dt)
+    up, lddu = _rows("dU", dU, M, N, dt)
+    gwp, ldwg = _rows("Wg", Wg, N, K, dt)
+    uwp, ldwu = _rows("Wu", Wu, N, K, dt)
+    xp, lddx = _rows("dX", dX, M, K, dX.dtype)
+    check("rb_qat_glu_dx", lib.rb_qat_glu_dx(gp, lddg, up, lddu, _dt(dt), M, gwp, ldwg, uwp, ldwu, N, K, xp, _dt(dX.dtype),
+                                             lddx, _ptr(ws), 0 if ws is None else ws.numel(), _stream()))
+    return dX
 
 
 _NORM = {"none": _lib.RB_NORM_NONE, "rms": _lib.RB_NORM_RMS, "layer": _lib.RB_NORM_LAYER}
@@ -603,3 +697,106 @@ def adamw_step(plan: AdamWPlan, step: int, lr: float, beta1: float = 0.9, beta2:
         raise TypeError("skip is a device int32")
     check("rb_adamw_step", lib.rb_adamw_step(_ptr(plan.table), plan.chunks, plan.state_bits, step, lr, beta1, beta2,
                                              eps, _ptr(grad_scale), _ptr(skip), seed & 0xFFFFFFFF, _stream()))
+
+
+def muon_step(W: torch.Tensor | None, G: torch.Tensor, mom: torch.Tensor | None, lr: float, momentum: float = 0.95,
+              nesterov: bool = True, weight_decay: float = 0.0, scale: float | None = None, steps: int = 5,
+              eps: float = 1e-7, grad_scale: torch.Tensor | None = None, skip: torch.Tensor | None = None,
+              O: torch.Tensor | None = None, ws: torch.Tensor | None = None) -> None:
+    """One step of the matrix W [N][K] (fp32, in place) from its gradient G (fp32, fp16 or bf16): the momentum `mom`
+    (fp32, in place) takes grad_scale G in, the update's singular values are brought near 1 by `steps` Newton-Schulz
+    products, and W <- W (1 - lr weight_decay) - lr scale X. `scale` defaults to 0.2 sqrt(max(N, K)), which gives the
+    update AdamW's size. `grad_scale` (device fp32) and `skip` (device int32) as in adamw_step. O [N][K] (fp16 or
+    bf16) receives X; W may be None where O is given. Rows may be strided."""
+    N, K = G.shape
+    if grad_scale is not None and grad_scale.dtype != torch.float32:
+        raise TypeError("grad_scale is a device fp32")
+    if skip is not None and skip.dtype != torch.int32:
+        raise TypeError("skip is a device int32")
+    if ws is None:
+        ws = torch.empty(_ws_bytes(RB_OP_MUON_STEP, N, K, 1), dtype=torch.uint8, device=G.device)
+    wp, ldw = _rows("W", W, N, K, torch.float32)
+    gp, ldg = _rows("G", G, N, K, G.dtype)
+    mp, ldm = _rows("mom", mom, N, K, torch.float32)
+    op, ldo = _rows("O", O, N, K, torch.float16 if O is None else O.dtype)
+    scale = 0.2 * max(N, K) ** 0.5 if scale is None else scale
+    check("rb_muon_step", lib.rb_muon_step(wp, ldw, gp, _dt(G.dtype), ldg, mp, ldm, N, K, lr, momentum, int(nesterov),
+                                           weight_decay, scale, steps, eps, _ptr(grad_scale), _ptr(skip), op,
+                                           RB_F16 if O is None else _dt(O.dtype), ldo, _ptr(ws), ws.numel(), _stream()))
+
+
+def orthogonalize(G: torch.Tensor, steps: int = 5, eps: float = 1e-7, o_dtype=torch.bfloat16,
+                  O: torch.Tensor | None = None, ws: torch.Tensor | None = None) -> torch.Tensor:
+    """The Newton-Schulz products of muon_step alone: G [N][K] (fp32, fp16 or bf16) with its singular values brought
+    near 1, in fp16 or bf16."""
+    O = torch.empty(G.shape, dtype=o_dtype, device=G.device) if O is None else O
+    muon_step(None, G, None, 0.0, steps=steps, eps=eps, O=O, ws=ws)
+    return O
+
+
+def _q4(name: str, codes: torch.Tensor, s: torch.Tensor, z: torch.Tensor | None, N: int, K: int, group: int):
+    """Pointers of one 4-bit weight, its shapes checked."""
+    if codes.dtype is not torch.int32 or codes.numel() * 4 != lib.rb_q4_codes_bytes(N, K):
+        raise ValueError(f"{name}: codes are int32 [ceil(N / 16)][ceil(K / 128)][64][4]")
+    for t in (s, z):
+        if t is not None and (t.dtype is not torch.float16 or t.numel() != -(-K // group) * N):
+            raise ValueError(f"{name}: scales and offsets are fp16 [ceil(K / group)][N]")
+    return _ptr(codes), _ptr(s), _ptr(z)
+
+
+def q4_pack(W: torch.Tensor, group: int = 128, offset: bool = False, codes: torch.Tensor | None = None,
+            s: torch.Tensor | None = None, z: torch.Tensor | None = None, d_status: torch.Tensor | None = None):
+    """W [N][K] (fp32, fp16 or bf16, rows may be strided) in 4 bits with a scale per row and `group` columns (32, 64 or
+    128): (codes, s, z), W ~ s (q - 8), or with `offset` W ~ s q + z. The codes are int32 in tiles of 16 rows by
+    128 columns ([ceil(N / 16)][ceil(K / 128)][64][4]), s and z fp16 [ceil(K / group)][N], z None without offsets."""
+    N, K = W.shape
+    if group not in (32, 64, 128):
+        raise ValueError("group must be 32, 64 or 128")
+    shape = (-(-K // group), N)
+    if codes is None:
+        codes = torch.empty((-(-N // 16), -(-K // 128), 64, 4), dtype=torch.int32, device=W.device)
+    s = torch.empty(shape, dtype=torch.float16, device=W.device) if s is None else s
+    z = torch.empty(shape, dtype=torch.float16, device=W.device) if z is None and offset else z
+    if not offset and z is not None:
+        raise ValueError("offsets to write need offset")
+    cp, sp, zp = _q4("q4_pack", codes, s, z, N, K, group)
+    wp, ldw = _rows("W", W, N, K, W.dtype)
+    check("rb_q4_pack", lib.rb_q4_pack(wp, _dt(W.dtype), N, K, ldw, group, cp, sp, zp, _ptr(d_status), _stream()))
+    return codes, s, z
+
+
+def q4_dequant(codes: torch.Tensor, s: torch.Tensor, z: torch.Tensor | None, N: int, K: int, group: int = 128,
+               dtype=torch.float16, What: torch.Tensor | None = None) -> torch.Tensor:
+    """The weights [N][K] that q4_pack's result stands for, in fp32, fp16 or bf16 (for the products of larger batches)."""
+    What = torch.empty((N, K), dtype=dtype, device=codes.device) if What is None else What
+    cp, sp, zp = _q4("q4_dequant", codes, s, z, N, K, group)
+    wp, ldw = _rows("What", What, N, K, What.dtype)
+    check("rb_q4_dequant", lib.rb_q4_dequant(cp, sp, zp, N, K, group, wp, _dt(What.dtype), ldw, _stream()))
+    return What
+
+
+def q4_gemv(codes: torch.Tensor, s: torch.Tensor, z: torch.Tensor | None, x: torch.Tensor, N: int, group: int = 128,
+            y_dtype=None, y: torch.Tensor | None = None) -> torch.Tensor:
+    """y [M][N] = x What^T on q4_pack's weights for x [M][K] (fp16 or bf16, rows may be strided), M <= 16, in x's type
+    (default) or fp32."""
+    M, K = x.shape
+    y = torch.empty((M, N), dtype=y_dtype or x.dtype, device=x.device) if y is None else y
+    cp, sp, zp = _q4("q4_gemv", codes, s, z, N, K, group)
+    xp, ldx = _rows("x", x, M, K, x.dtype)
+    yp, ldy = _rows("y", y, M, N, y.dtype)
+    check("rb_q4_gemv", lib.rb_q4_gemv(cp, sp, zp, N, K, group, xp, _dt(x.dtype), M, ldx, yp, _dt(y.dtype), ldy, _stream()))
+    return y
+
+
+def q4_glu(Wg, Wu, x: torch.Tensor, N: int, group: int = 128, act: str = "silu", y_dtype=None,
+           y: torch.Tensor | None = None) -> torch.Tensor:
+    """A gated block's first half for decode batches, in one launch: y [M][N] = act(x Wg^T) (x Wu^T), Wg and Wu each the
+    (codes, s, z) of q4_pack (one group size); other arguments as in q4_gemv."""
+    M, K = x.shape
+    y = torch.empty((M, N), dtype=y_dtype or x.dtype, device=x.device) if y is None else y
+    g, u = _q4("Wg", *Wg, N, K, group), _q4("Wu", *Wu, N, K, group)
+    xp, ldx = _rows("x", x, M, K, x.dtype)
+    yp, ldy = _rows("y", y, M, N, y.dtype)
+    check("rb_q4_glu", lib.rb_q4_glu(*g, *u, N, K, group, _ACT[act], xp, _dt(x.dtype), M, ldx, yp, _dt(y.dtype), ldy,
+                                     _stream()))
+    return y

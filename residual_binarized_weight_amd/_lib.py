@@ -13,7 +13,8 @@ RB_OK, RB_ERR_INVALID_ARG, RB_ERR_UNSUPPORTED, RB_ERR_MISALIGNED, RB_ERR_WORKSPA
 RB_F32, RB_F16, RB_BF16 = 0, 1, 2
 RB_QAT_ENGINE_AUTO, RB_QAT_ENGINE_MFMA, RB_QAT_ENGINE_ROCBLAS = 0, 1, 2
 (RB_OP_PACK, RB_OP_GEMV, RB_OP_GEMM_SMALL, RB_OP_CODEBOOK_ENCODE, RB_OP_CODEBOOK_GEMV, RB_OP_SVID_INIT,
- RB_OP_QAT_BACKWARD, RB_OP_RESNORM_BACKWARD, RB_OP_QAT_LINEAR, RB_OP_QAT_LINEAR_BACKWARD) = range(10)
+ RB_OP_QAT_BACKWARD, RB_OP_RESNORM_BACKWARD, RB_OP_QAT_LINEAR, RB_OP_QAT_LINEAR_BACKWARD, RB_OP_QAT_GLU,
+ RB_OP_QAT_GLU_BACKWARD, RB_OP_QAT_GLU_DX, RB_OP_MUON_STEP) = range(14)
 RB_ACT_NONE, RB_ACT_RELU, RB_ACT_GELU, RB_ACT_GELU_TANH, RB_ACT_SILU = range(5)
 RB_NORM_NONE, RB_NORM_RMS, RB_NORM_LAYER = 0, 1, 2
 
@@ -70,6 +71,12 @@ SIGNATURES = {
                                      _i64, _vp, ctypes.c_int, _i64, _vp, _sz, _vp]),
     "rb_qat_linear_backward": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, ctypes.c_int, _i64, _i32, _vp,
                                               _i64, _vp, _vp, _sz, _vp]),
+    "rb_qat_glu": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _vp, _vp, _i32, _vp,
+                                  _i64, _vp, _i64, _vp, ctypes.c_int, _i64, _vp, _sz, _vp]),
+    "rb_qat_glu_backward": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, ctypes.c_int, _i32,
+                                           _vp, _i64, _vp, _i64, _vp, _vp, _vp, _sz, _vp]),
+    "rb_qat_glu_dx": (ctypes.c_int, [_vp, _i64, _vp, _i64, ctypes.c_int, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _vp,
+                                     ctypes.c_int, _i64, _vp, _sz, _vp]),
     "rb_resnorm_forward": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, ctypes.c_int, _i64, _vp, _i64,
                                           ctypes.c_float, _i32, _vp, _vp, _i32, _vp, _vp, ctypes.c_float, _vp, _i64,
                                           _vp, _i64, _vp, _vp]),
@@ -80,6 +87,16 @@ SIGNATURES = {
     "rb_adamw_plan": (ctypes.c_int, [_vp, _i64, _i32, _vp, _sz, _vp]),
     "rb_adamw_step": (ctypes.c_int, [_vp, _i64, _i32, _i64, ctypes.c_double, ctypes.c_double, ctypes.c_double,
                                      ctypes.c_double, _vp, _vp, ctypes.c_uint32, _vp]),
+    "rb_muon_step": (ctypes.c_int, [_vp, _i64, _vp, ctypes.c_int, _i64, _vp, _i64, _i64, _i64, ctypes.c_double,
+                                    ctypes.c_double, _i32, ctypes.c_double, ctypes.c_double, _i32, ctypes.c_double, _vp,
+                                    _vp, _vp, ctypes.c_int, _i64, _vp, _sz, _vp]),
+    "rb_q4_codes_bytes": (_sz, [_i64, _i64]),
+    "rb_q4_pack": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _vp]),
+    "rb_q4_dequant": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i64, _i32, _vp, ctypes.c_int, _i64, _vp]),
+    "rb_q4_gemv": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i64, _i32, _vp, ctypes.c_int, _i64, _i64, _vp, ctypes.c_int, _i64,
+                                  _vp]),
+    "rb_q4_glu": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i32, _i32, _vp, ctypes.c_int, _i64, _i64, _vp,
+                                 ctypes.c_int, _i64, _vp]),
     # streaming-read probe used by the bench (not part of the method)
     "rb_bench_stream_read": (ctypes.c_int, [_vp, _i64, _vp, _i32, _vp]),
     "rb_bench_gather": (ctypes.c_int, [_vp, ctypes.c_uint32, _i32, _vp, _i32, _vp]),

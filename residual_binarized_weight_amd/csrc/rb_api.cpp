@@ -25,6 +25,8 @@ bool is_pow2_in(int32_t v, int32_t lo, int32_t hi) {
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
 constexpr int64_t kQatMaxDim = int64_t(1) << 28;  // N and K of the training layer (32-bit byte offsets)
 
+constexpr int64_t kMuonMaxDim = (int64_t(1) << 21) - 1;  // a tile's rows lie within 2^31 bytes
+
 constexpr int64_t kResnormMaxD = 16384;  // a row is held in one block's registers
 
 bool act_dtype(rb_dtype d) { return d == RB_F16 || d == RB_BF16; }
@@ -115,6 +117,23 @@ size_t rb_workspace_bytes(rb_op op, int32_t k, int64_t N, int64_t K, int64_t M) 
       const size_t p = rb::linear_backward_workspace_bytes(N, M);
       return p > 0 ? rb::zero_region_bytes(N) + p : 0;
     }
+    case RB_OP_QAT_GLU: {
+      if (N > kQatMaxDim || K > kQatMaxDim || M > kMaxDim) return 0;
+      const size_t p = rb::glu_workspace_bytes(N, K, M);
+      return p > 0 ? rb::zero_region_bytes(N) + p : 0;
+    }
+    case RB_OP_QAT_GLU_BACKWARD: {
+      if (N > kQatMaxDim || M > kMaxDim) return 0;
+      const size_t p = rb::glu_backward_workspace_bytes(N, M);
+      return p > 0 ? rb::zero_region_bytes(N) + p : 0;
+    }
+    case RB_OP_QAT_GLU_DX: {
+      if (N > kQatMaxDim || K > kQatMaxDim || M > kMaxDim) return 0;
+      const size_t p = rb::glu_dx_workspace_bytes(N, K, M);
+      return p > 0 ? rb::zero_region_bytes(N) + p : 0;
+    }
+    case RB_OP_MUON_STEP:
+      return (N > kMuonMaxDim || K > kMuonMaxDim) ? 0 : rb::zero_region_bytes(N) + rb::muon_workspace_bytes(N, K);
     default: return 0;
   }
 }
@@ -381,11 +400,11 @@ rb_status rb_qat_backward(const void* dY, rb_dtype a_dtype, int64_t M, int64_t l
                           const float* h, int32_t k, int64_t N, int64_t K, float* dW, int64_t lddw, void* dX,
                           rb_dtype dx_dtype, int64_t lddx, float* dg, float* dh, void* ws, size_t ws_bytes,
                           void* stream) {
-  if (!dY || !X || !dW || !dX || !dg || !dh) return RB_ERR_INVALID_ARG;
+  if (!dY || !X || !dW || !dg || !dh) return RB_ERR_INVALID_ARG;
   rb_status st = check_qat_layer(N, K, k, g, h, planes, ldp, What, ldwh, a_dtype);
   if (st != RB_OK) return st;
   if (M < 1 || M > kMaxDim || lddy < N || lddy > kMaxDim || ldx < K || ldx > kMaxDim || lddw < K ||
-      lddw > kMaxDim || lddx < K || lddx > kMaxDim)
+      lddw > kMaxDim || (dX && (lddx < K || lddx > kMaxDim)))
     return RB_ERR_INVALID_ARG;
   if (!valid_dtype(dx_dtype)) return RB_ERR_INVALID_ARG;
   if (dx_dtype != RB_F32 && dx_dtype != a_dtype) return RB_ERR_UNSUPPORTED;
@@ -482,8 +501,77 @@ rb_status rb_qat_linear_backward(const void* dY, rb_dtype dy_dtype, int64_t M, i
                                              static_cast<hipStream_t>(stream)));
 }
 
-static bool norm_kind(int32_t k) { return k >= RB_NORM_NONE && k <= RB_NORM_LAYER; }
+// outputs of 2^40 elements and more pass a launch's count of tiles
+static bool tiles_fit(int64_t M, int64_t N) { return ((M + 63) / 64) * ((N + 127) / 128) <= kMaxDim; }
 static bool row_ld(int64_t ld, int64_t D) { return ld >= D && ld <= kMaxDim; }
+
+rb_status rb_qat_glu(const void* X, rb_dtype a_dtype, int64_t M, int64_t ldx, const void* Wg, int64_t ldwg, const void* Wu,
+                     int64_t ldwu, int64_t N, int64_t K, const float* bg, const float* bu, int32_t act, void* G,
+                     int64_t ldg, void* U, int64_t ldu, void* H, rb_dtype h_dtype, int64_t ldh, void* ws, size_t ws_bytes,
+                     void* stream) {
+  if (!X || !Wg || !Wu || !H || !act_kind(act)) return RB_ERR_INVALID_ARG;
+  if (N < 1 || K < 1 || M < 1 || N > kQatMaxDim || K > kQatMaxDim || M > kMaxDim) return RB_ERR_INVALID_ARG;
+  if (!row_ld(ldx, K) || !row_ld(ldwg, K) || !row_ld(ldwu, K) || !row_ld(ldh, N) || (G && !row_ld(ldg, N)) ||
+      (U && !row_ld(ldu, N)))
+    return RB_ERR_INVALID_ARG;
+  if (!valid_dtype(a_dtype) || !valid_dtype(h_dtype)) return RB_ERR_INVALID_ARG;
+  if (!act_dtype(a_dtype) || (h_dtype != RB_F32 && h_dtype != a_dtype) || !tiles_fit(M, N)) return RB_ERR_UNSUPPORTED;
+  if (!elem_aligned(X, a_dtype) || !elem_aligned(Wg, a_dtype) || !elem_aligned(Wu, a_dtype) || !elem_aligned(H, h_dtype) ||
+      !elem_aligned(G, a_dtype) || !elem_aligned(U, a_dtype) || !aligned(bg, 4) || !aligned(bu, 4))
+    return RB_ERR_MISALIGNED;
+  const size_t part = rb::glu_workspace_bytes(N, K, M);
+  if (part > 0 && (!ws || ws_bytes < rb::zero_region_bytes(N) + part)) return RB_ERR_WORKSPACE;
+  if (!aligned(ws, 16)) return RB_ERR_MISALIGNED;
+  log_call("rb_qat_glu", N, K, M, act);
+  return from_hip(rb::launch_glu(X, a_dtype, M, ldx, Wg, ldwg, Wu, ldwu, N, K, bg, bu, act, G, ldg, U, ldu, H, h_dtype, ldh,
+                                 part > 0 ? static_cast<char*>(ws) + rb::zero_region_bytes(N) : nullptr,
+                                 static_cast<hipStream_t>(stream)));
+}
+
+rb_status rb_qat_glu_backward(const void* dH, rb_dtype dh_dtype, int64_t M, int64_t N, int64_t lddh, const void* G,
+                              int64_t ldg, const void* U, int64_t ldu, rb_dtype a_dtype, int32_t act, void* dG,
+                              int64_t lddg, void* dU, int64_t lddu, float* dbg, float* dbu, void* ws, size_t ws_bytes,
+                              void* stream) {
+  if (!dH || !G || !U || !dG || !dU || dG == dU || !act_kind(act)) return RB_ERR_INVALID_ARG;
+  if (N < 1 || M < 1 || N > kQatMaxDim || M > kMaxDim) return RB_ERR_INVALID_ARG;
+  if (!row_ld(lddh, N) || !row_ld(ldg, N) || !row_ld(ldu, N) || !row_ld(lddg, N) || !row_ld(lddu, N))
+    return RB_ERR_INVALID_ARG;
+  if (!valid_dtype(a_dtype) || !valid_dtype(dh_dtype)) return RB_ERR_INVALID_ARG;
+  if (!act_dtype(a_dtype) || (dh_dtype != RB_F32 && dh_dtype != a_dtype)) return RB_ERR_UNSUPPORTED;
+  if (!elem_aligned(dH, dh_dtype) || !elem_aligned(G, a_dtype) || !elem_aligned(U, a_dtype) || !elem_aligned(dG, a_dtype) ||
+      !elem_aligned(dU, a_dtype) || !aligned(dbg, 4) || !aligned(dbu, 4))
+    return RB_ERR_MISALIGNED;
+  const size_t part = dbg || dbu ? rb::glu_backward_workspace_bytes(N, M) : 0;
+  if (part > 0 && (!ws || ws_bytes < rb::zero_region_bytes(N) + part)) return RB_ERR_WORKSPACE;
+  if (!aligned(ws, 16)) return RB_ERR_MISALIGNED;
+  log_call("rb_qat_glu_backward", N, 0, M, act);
+  return from_hip(rb::launch_glu_backward(dH, dh_dtype, M, N, lddh, G, ldg, U, ldu, a_dtype, act, dG, lddg, dU, lddu, dbg,
+                                          dbu, part > 0 ? static_cast<char*>(ws) + rb::zero_region_bytes(N) : nullptr,
+                                          static_cast<hipStream_t>(stream)));
+}
+
+rb_status rb_qat_glu_dx(const void* dG, int64_t lddg, const void* dU, int64_t lddu, rb_dtype a_dtype, int64_t M,
+                        const void* Wg, int64_t ldwg, const void* Wu, int64_t ldwu, int64_t N, int64_t K, void* dX,
+                        rb_dtype dx_dtype, int64_t lddx, void* ws, size_t ws_bytes, void* stream) {
+  if (!dG || !dU || !Wg || !Wu || !dX) return RB_ERR_INVALID_ARG;
+  if (N < 1 || K < 1 || M < 1 || N > kQatMaxDim || K > kQatMaxDim || M > kMaxDim) return RB_ERR_INVALID_ARG;
+  if (!row_ld(lddg, N) || !row_ld(lddu, N) || !row_ld(ldwg, K) || !row_ld(ldwu, K) || !row_ld(lddx, K))
+    return RB_ERR_INVALID_ARG;
+  if (!valid_dtype(a_dtype) || !valid_dtype(dx_dtype)) return RB_ERR_INVALID_ARG;
+  if (!act_dtype(a_dtype) || (dx_dtype != RB_F32 && dx_dtype != a_dtype) || !tiles_fit(M, K)) return RB_ERR_UNSUPPORTED;
+  if (!elem_aligned(dG, a_dtype) || !elem_aligned(dU, a_dtype) || !elem_aligned(Wg, a_dtype) || !elem_aligned(Wu, a_dtype) ||
+      !elem_aligned(dX, dx_dtype))
+    return RB_ERR_MISALIGNED;
+  const size_t part = rb::glu_dx_workspace_bytes(N, K, M);
+  if (part > 0 && (!ws || ws_bytes < rb::zero_region_bytes(N) + part)) return RB_ERR_WORKSPACE;
+  if (!aligned(ws, 16)) return RB_ERR_MISALIGNED;
+  log_call("rb_qat_glu_dx", N, K, M, 0);
+  return from_hip(rb::launch_glu_dx(dG, lddg, dU, lddu, a_dtype, M, Wg, ldwg, Wu, ldwu, N, K, dX, dx_dtype, lddx,
+                                    part > 0 ? static_cast<char*>(ws) + rb::zero_region_bytes(N) : nullptr,
+                                    static_cast<hipStream_t>(stream)));
+}
+
+static bool norm_kind(int32_t k) { return k >= RB_NORM_NONE && k <= RB_NORM_LAYER; }
 
 // shapes, types and vectors shared by the two directions
 static rb_status check_resnorm(rb_dtype a_dtype, rb_dtype s_dtype, int64_t M, int64_t D, const void* gate, int64_t ldg,
@@ -610,6 +698,95 @@ rb_status rb_adamw_step(const void* plan, int64_t chunks, int32_t state_bits, in
   log_call("rb_adamw_step", chunks, state_bits, 0, 0);
   return from_hip(rb::launch_adamw_step(plan, chunks, state_bits, step, lr, beta1, beta2, eps, grad_scale, skip, seed,
                                         static_cast<hipStream_t>(stream)));
+}
+
+rb_status rb_muon_step(float* W, int64_t ldw, const void* G, rb_dtype g_dtype, int64_t ldg, float* mom, int64_t ldm,
+                       int64_t N, int64_t K, double lr, double momentum, int32_t nesterov, double weight_decay,
+                       double scale, int32_t steps, double eps, const float* grad_scale, const int32_t* skip, void* O,
+                       rb_dtype o_dtype, int64_t ldo, void* ws, size_t ws_bytes, void* stream) {
+  if (!G || (!W && !O)) return RB_ERR_INVALID_ARG;
+  if (N < 1 || K < 1 || N > kMuonMaxDim || K > kMuonMaxDim || steps < 1 || steps > 16) return RB_ERR_INVALID_ARG;
+  if (!row_ld(ldg, K) || (W && !row_ld(ldw, K)) || (mom && !row_ld(ldm, K)) || (O && !row_ld(ldo, K)))
+    return RB_ERR_INVALID_ARG;
+  const auto factor = [](double x) { return std::isfinite(x) && x >= 0.0; };
+  if (!factor(lr) || !factor(weight_decay) || !factor(scale) || !(momentum >= 0.0 && momentum < 1.0))
+    return RB_ERR_INVALID_ARG;
+  if (!std::isfinite(eps) || !(static_cast<float>(eps) > 0.f)) return RB_ERR_INVALID_ARG;
+  if (!valid_dtype(g_dtype) || (O && !valid_dtype(o_dtype))) return RB_ERR_INVALID_ARG;
+  if (O && !act_dtype(o_dtype)) return RB_ERR_UNSUPPORTED;
+  if (!elem_aligned(G, g_dtype) || !aligned(W, 4) || !aligned(mom, 4) || (O && !elem_aligned(O, o_dtype)) ||
+      !aligned(grad_scale, 4) || !aligned(skip, 4))
+    return RB_ERR_MISALIGNED;
+  if (!ws || ws_bytes < rb::zero_region_bytes(N) + rb::muon_workspace_bytes(N, K)) return RB_ERR_WORKSPACE;
+  if (!aligned(ws, 16)) return RB_ERR_MISALIGNED;
+  log_call("rb_muon_step", N, K, 0, steps);
+  return from_hip(rb::launch_muon_step(W, ldw, G, g_dtype, ldg, mom, ldm, N, K, lr, momentum, nesterov != 0, weight_decay,
+                                       scale, steps, eps, grad_scale, skip, O, o_dtype, ldo,
+                                       static_cast<char*>(ws) + rb::zero_region_bytes(N), static_cast<hipStream_t>(stream)));
+}
+
+static bool q4_group(int32_t g) { return g == 32 || g == 64 || g == 128; }
+static rb_status check_q4(const uint32_t* codes, const void* s, const void* z, int64_t N, int64_t K, int32_t group) {
+  if (!codes || !s || N < 1 || K < 1 || N > kQatMaxDim || K > kQatMaxDim || !q4_group(group)) return RB_ERR_INVALID_ARG;
+  if (!aligned(codes, 16) || !aligned(s, 2) || !aligned(z, 2)) return RB_ERR_MISALIGNED;
+  return RB_OK;
+}
+
+size_t rb_q4_codes_bytes(int64_t N, int64_t K) {
+  if (N < 1 || K < 1 || N > kQatMaxDim || K > kQatMaxDim) return 0;
+  return (size_t)((N + 15) / 16) * (size_t)((K + 127) / 128) * 1024;
+}
+
+rb_status rb_q4_pack(const void* W, rb_dtype w_dtype, int64_t N, int64_t K, int64_t ldw, int32_t group, uint32_t* codes,
+                     void* s, void* z, int32_t* d_status, void* stream) {
+  if (!W || ldw < K || ldw > kMaxDim || !valid_dtype(w_dtype)) return RB_ERR_INVALID_ARG;
+  const rb_status st = check_q4(codes, s, z, N, K, group);
+  if (st != RB_OK) return st;
+  if (!elem_aligned(W, w_dtype) || !aligned(d_status, 4)) return RB_ERR_MISALIGNED;
+  log_call("rb_q4_pack", N, K, 0, group);
+  return from_hip(rb::launch_q4_pack(W, w_dtype, N, K, ldw, group, codes, s, z, d_status, static_cast<hipStream_t>(stream)));
+}
+
+rb_status rb_q4_dequant(const uint32_t* codes, const void* s, const void* z, int64_t N, int64_t K, int32_t group, void* What,
+                        rb_dtype w_dtype, int64_t ldw, void* stream) {
+  if (!What || ldw < K || ldw > kMaxDim || !valid_dtype(w_dtype)) return RB_ERR_INVALID_ARG;
+  const rb_status st = check_q4(codes, s, z, N, K, group);
+  if (st != RB_OK) return st;
+  if (!elem_aligned(What, w_dtype)) return RB_ERR_MISALIGNED;
+  log_call("rb_q4_dequant", N, K, 0, group);
+  return from_hip(rb::launch_q4_dequant(codes, s, z, N, K, group, What, w_dtype, ldw, static_cast<hipStream_t>(stream)));
+}
+
+static rb_status check_q4_rows(int64_t N, int64_t K, const void* x, rb_dtype x_dtype, int64_t M, int64_t ldx, const void* y,
+                               rb_dtype y_dtype, int64_t ldy) {
+  if (!x || !y || M < 1 || !row_ld(ldx, K) || !row_ld(ldy, N) || !valid_dtype(x_dtype) || !valid_dtype(y_dtype))
+    return RB_ERR_INVALID_ARG;
+  if (M > 16 || !act_dtype(x_dtype) || (y_dtype != RB_F32 && y_dtype != x_dtype)) return RB_ERR_UNSUPPORTED;
+  if (!elem_aligned(x, x_dtype) || !elem_aligned(y, y_dtype)) return RB_ERR_MISALIGNED;
+  return RB_OK;
+}
+
+rb_status rb_q4_gemv(const uint32_t* codes, const void* s, const void* z, int64_t N, int64_t K, int32_t group, const void* x,
+                     rb_dtype x_dtype, int64_t M, int64_t ldx, void* y, rb_dtype y_dtype, int64_t ldy, void* stream) {
+  rb_status st = check_q4(codes, s, z, N, K, group);
+  if (st == RB_OK) st = check_q4_rows(N, K, x, x_dtype, M, ldx, y, y_dtype, ldy);
+  if (st != RB_OK) return st;
+  log_call("rb_q4_gemv", N, K, M, group);
+  return from_hip(rb::launch_q4_product(codes, s, z, nullptr, nullptr, nullptr, N, K, group, RB_ACT_NONE, x, x_dtype, M, ldx,
+                                        y, y_dtype, ldy, static_cast<hipStream_t>(stream)));
+}
+
+rb_status rb_q4_glu(const uint32_t* codes_g, const void* s_g, const void* z_g, const uint32_t* codes_u, const void* s_u,
+                    const void* z_u, int64_t N, int64_t K, int32_t group, int32_t act, const void* x, rb_dtype x_dtype,
+                    int64_t M, int64_t ldx, void* y, rb_dtype y_dtype, int64_t ldy, void* stream) {
+  if (!act_kind(act)) return RB_ERR_INVALID_ARG;
+  rb_status st = check_q4(codes_g, s_g, z_g, N, K, group);
+  if (st == RB_OK) st = check_q4(codes_u, s_u, z_u, N, K, group);
+  if (st == RB_OK) st = check_q4_rows(N, K, x, x_dtype, M, ldx, y, y_dtype, ldy);
+  if (st != RB_OK) return st;
+  log_call("rb_q4_glu", N, K, M, group);
+  return from_hip(rb::launch_q4_product(codes_g, s_g, z_g, codes_u, s_u, z_u, N, K, group, act, x, x_dtype, M, ldx, y,
+                                        y_dtype, ldy, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -136,6 +136,20 @@ hipError_t launch_linear_backward(const void* dY, rb_dtype dy_dtype, int64_t M, 
                                   rb_dtype a_dtype, int64_t ldz, int act, void* dZ, int64_t lddz, float* db, void* ws,
                                   hipStream_t s);
 
+// a gated block's two products with their epilogue, the epilogue's backward and the input's gradient (rb_glu.hip)
+size_t glu_workspace_bytes(int64_t N, int64_t K, int64_t M);
+hipError_t launch_glu(const void* X, rb_dtype a_dtype, int64_t M, int64_t ldx, const void* Wg, int64_t ldwg, const void* Wu,
+                      int64_t ldwu, int64_t N, int64_t K, const float* bg, const float* bu, int act, void* G, int64_t ldg,
+                      void* U, int64_t ldu, void* H, rb_dtype h_dtype, int64_t ldh, void* ws, hipStream_t s);
+size_t glu_backward_workspace_bytes(int64_t N, int64_t M);
+hipError_t launch_glu_backward(const void* dH, rb_dtype dh_dtype, int64_t M, int64_t N, int64_t lddh, const void* G, int64_t ldg,
+                               const void* U, int64_t ldu, rb_dtype a_dtype, int act, void* dG, int64_t lddg, void* dU,
+                               int64_t lddu, float* dbg, float* dbu, void* ws, hipStream_t s);
+size_t glu_dx_workspace_bytes(int64_t N, int64_t K, int64_t M);
+hipError_t launch_glu_dx(const void* dG, int64_t lddg, const void* dU, int64_t lddu, rb_dtype a_dtype, int64_t M, const void* Wg,
+                         int64_t ldwg, const void* Wu, int64_t ldwu, int64_t N, int64_t K, void* dX, rb_dtype dx_dtype,
+                         int64_t lddx, void* ws, hipStream_t s);
+
 // norms between blocks (rb_resnorm.hip)
 size_t resnorm_backward_workspace_bytes(int64_t D, int64_t M);
 hipError_t launch_resnorm_forward(const void* Y, rb_dtype a_dtype, int64_t M, int64_t D, int64_t ldy, const void* R,
@@ -158,5 +172,21 @@ void adamw_fill_plan(const rb_adamw_tensor* t, int64_t count, int state_bits, vo
 hipError_t launch_adamw_step(const void* plan, int64_t chunks, int state_bits, int64_t step, double lr, double beta1,
                              double beta2, double eps, const float* grad_scale, const int32_t* skip, uint32_t seed,
                              hipStream_t s);
+
+// Newton-Schulz step of a matrix (rb_muon.hip)
+size_t muon_workspace_bytes(int64_t N, int64_t K);
+hipError_t launch_muon_step(float* W, int64_t ldw, const void* G, rb_dtype g_dtype, int64_t ldg, float* mom, int64_t ldm,
+                            int64_t N, int64_t K, double lr, double momentum, int nesterov, double weight_decay,
+                            double scale, int steps, double eps, const float* grad_scale, const int32_t* skip, void* O,
+                            rb_dtype o_dtype, int64_t ldo, void* ws, hipStream_t s);
+
+// 4-bit weights with group scales (rb_q4.hip); codes2 NULL: the plain product
+hipError_t launch_q4_pack(const void* W, rb_dtype w_dtype, int64_t N, int64_t K, int64_t ldw, int group, uint32_t* codes,
+                          void* s, void* z, int32_t* status, hipStream_t stream);
+hipError_t launch_q4_dequant(const uint32_t* codes, const void* s, const void* z, int64_t N, int64_t K, int group, void* W,
+                             rb_dtype w_dtype, int64_t ldw, hipStream_t stream);
+hipError_t launch_q4_product(const uint32_t* codes, const void* s, const void* z, const uint32_t* codes2, const void* s2,
+                             const void* z2, int64_t N, int64_t K, int group, int act, const void* x, rb_dtype x_dtype,
+                             int64_t M, int64_t ldx, void* y, rb_dtype y_dtype, int64_t ldy, hipStream_t stream);
 
 }  // namespace rb

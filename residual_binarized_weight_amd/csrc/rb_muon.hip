@@ -1,0 +1,426 @@
+// rb_muon.hip -- an optimizer step of a matrix by momentum and Newton-Schulz products.
+//
+//   m <- mu m + s g;  u = s g + mu m (nesterov) or m;  X = u / (|u|_F + eps), as its transpose where it is tall
+//   X <- a X + (b A + c A^2) X,  A = X X^T      a few times: the singular values go towards 1
+//   W <- W (1 - lr wd) - lr scale X
+//
+// With n = min(N, K) and m = max(N, K) an iteration is three products: A (symmetric, n x n over m), the polynomial
+// B = b A + c A^2 (symmetric, n x n over n) and X' = a X + B X (n x m over n).
+//
+// Arithmetic. The products take fp16 operands at fixed powers of two and sum in fp32: no entry of X exceeds 1.21 (the
+// polynomial's largest value over 0 .. 1.21, where the singular values stay), none of A 1.47, none of B 2.81, so X and
+// A are held times 2^15 and B times 2^14, all below fp16's largest, and an entry of X is near 2^15 / sqrt(n m),
+// far above its smallest normal one. X itself is held as the sum of two fp16 (22 bits): of the terms of X' only a X
+// carries the small singular values on, and each of the iterations multiplies them, and a rounding of X beside
+// them, by up to 3.44. With one fp16 the result of a matrix of low rank is off by 15 % (64 x 128 of rank 1) or
+// 3.5 % (128 x 256 of rank 16), with bf16 by all of it or 28 %; with two fp16 these are off by 0.07 and 0.08 %, and a
+// full-rank one by 0.13 to 0.21 %, the rounding of B and of X inside B X.
+//
+// Kernels of this file:
+//   muon_moment_kernel   m, and partial sums of u^2 (fp64);  muon_start_kernel  X from u and the norm
+//   muon_product_kernel  the three products, on the matrix cores;  muon_join_kernel  split tiles
+//   muon_apply_kernel    W and, where asked for, X itself
+#include "rb_internal.h"
+#include "rb_tile.hpp"
+
+namespace rb {
+namespace {
+
+using tile::f4;
+using tile::Source;
+using tile::Work;
+typedef _Float16 half_t;
+
+constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
+constexpr float kScaleX = 32768.f, kScaleA = 32768.f, kScaleB = 16384.f;
+constexpr int kMomentBlocks = 1024;
+
+// ---------------------------------------------------------------------------------------------
+// momentum and norm
+// ---------------------------------------------------------------------------------------------
+struct MomentArgs {
+  const void* g;
+  float* mom;
+  int64_t ldg, ldm;
+  int64_t N, K;
+  float mu, eps;
+  int nesterov;
+  const float* grad_scale;
+  const int32_t* skip;
+  double* part;  // [kMomentBlocks] sums of u^2
+  half_t *hi, *lo;  // X, n_pad rows of m_pad
+  int64_t m_pad, n_pad;
+  bool tall;  // X is u^T
+};
+// 8 elements of u = s g + mu m (or m) from the stored momentum
+template <typename TG>
+__device__ __forceinline__ void blend8(const MomentArgs& a, float s, int64_t row, int c, const float (&m)[8], float (&u)[8]) {
+  if (a.mom && !a.nesterov) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) u[j] = m[j];
+    return;
+  }
+  widen8<TG>(load8_any<TG>(static_cast<const TG*>(a.g) + row * a.ldg, c, (int)a.K), u);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) u[j] = a.mom ? fmaf(a.mu, m[j], s * u[j]) : s * u[j];
+}
+
+template <typename TG>
+__global__ __launch_bounds__(256) void muon_moment_kernel(MomentArgs a) {
+  __shared__ double sums[4];
+  if (a.skip && *a.skip) return;
+  const float s = a.grad_scale ? *a.grad_scale : 1.f;
+  const int64_t vecs = (a.K + 7) / 8, all = a.N * vecs;
+  double sum = 0.0;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = i / vecs;
+    const int c = (int)(i - row * vecs) * 8;
+    float g[8], m[8], u[8];
+    widen8<TG>(load8<TG>(static_cast<const TG*>(a.g) + row * a.ldg, c, (int)a.K), g);
+    if (a.mom) {
+      float* const mr = a.mom + row * a.ldm;
+      widen8<float>(load8<float>(mr, c, (int)a.K), m);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m[j] = fmaf(a.mu, m[j], s * g[j]);
+      store8<float>(mr, c, (int)a.K, m);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) u[j] = a.nesterov ? fmaf(a.mu, m[j], s * g[j]) : m[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) u[j] = s * g[j];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum += (double)u[j] * (double)u[j];
+  }
+  sum = wave_sum(sum);
+  if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) a.part[blockIdx.x] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+}
+
+// the two fp16 of a value of X
+__device__ __forceinline__ void split(float x, half_t& hi, half_t& lo) {
+  hi = (half_t)x;
+  lo = (half_t)(x - (float)hi);
+}
+
+// A block owns 64 x 64 of X. The norm is summed from the partial sums by every block (8 KB from the cache), in one order.
+template <typename TG>
+__global__ __launch_bounds__(256) void muon_start_kernel(MomentArgs a) {
+  __shared__ double sums[4];
+  __shared__ float tilev[64][65];
+  if (a.skip && *a.skip) return;
+  double sum = 0.0;
+  for (int i = threadIdx.x; i < kMomentBlocks; i += 256) sum += a.part[i];
+  sum = wave_sum(sum);
+  if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = sum;
+  __syncthreads();
+  const double inv = (double)kScaleX / (sqrt((sums[0] + sums[1]) + (sums[2] + sums[3])) + (double)a.eps);
+  const float s = a.grad_scale ? *a.grad_scale : 1.f;
+  // the block's rows and columns of u
+  const int64_t r0 = (a.tall ? (int64_t)blockIdx.x : (int64_t)blockIdx.y) * 64;
+  const int64_t c0 = (a.tall ? (int64_t)blockIdx.y : (int64_t)blockIdx.x) * 64;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int r = q * 32 + (threadIdx.x >> 3), c = (threadIdx.x & 7) * 8;
+    float u[8] = {};
+    if (r0 + r < a.N && c0 + c < a.K) {
+      float m[8] = {};
+      if (a.mom) widen8<float>(load8_any<float>(a.mom + (r0 + r) * a.ldm, (int)c0 + c, (int)a.K), m);
+      blend8<TG>(a, s, r0 + r, (int)c0 + c, m, u);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) tilev[r][c + j] = (float)((double)u[j] * inv);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int r = q * 32 + (threadIdx.x >> 3), c = (threadIdx.x & 7) * 8;  // of X
+    half_t hi[8], lo[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) split(a.tall ? tilev[c + j][r] : tilev[r][c + j], hi[j], lo[j]);
+    const int64_t at = ((int64_t)blockIdx.y * 64 + r) * a.m_pad + (int64_t)blockIdx.x * 64 + c;
+    *reinterpret_cast<tile::u4*>(a.hi + at) = *reinterpret_cast<const tile::u4*>(hi);
+    *reinterpret_cast<tile::u4*>(a.lo + at) = *reinterpret_cast<const tile::u4*>(lo);
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+// the products
+// ---------------------------------------------------------------------------------------------
+enum class Kind { kGram, kPoly, kNext };  // A = X X^T; B = b A + c A A; X' = a X + B X
+
+struct ProductArgs {
+  Source<half_t> src[1];
+  int M, N;  // of the output
+  Work work;
+  float* part;
+  const half_t* A;         // kPoly: A
+  const half_t *hi, *lo;   // kNext: X
+  half_t *out, *out_lo;
+  int64_t ld;
+  const int32_t* skip;
+};
+
+// 8 columns of a row from their sums, into the output's fp16
+template <Kind kind>
+__device__ __forceinline__ void finish8(const ProductArgs& a, const float (&v)[8], int64_t m, int n) {
+  const int64_t at = m * a.ld + n;
+  half_t o[8];
+  if constexpr (kind == Kind::kGram) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = (half_t)(v[j] * (kScaleA / (kScaleX * kScaleX)));
+  } else if constexpr (kind == Kind::kPoly) {
+    const Vec8<half_t>::Raw g = *reinterpret_cast<const Vec8<half_t>::Raw*>(a.A + at);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      o[j] = (half_t)fmaf(kB * (kScaleB / kScaleA), Vec8<half_t>::get(g, j), v[j] * (kC * (kScaleB / (kScaleA * kScaleA))));
+  } else {
+    const Vec8<half_t>::Raw h = *reinterpret_cast<const Vec8<half_t>::Raw*>(a.hi + at);
+    const Vec8<half_t>::Raw l = *reinterpret_cast<const Vec8<half_t>::Raw*>(a.lo + at);
+    half_t o2[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float x = Vec8<half_t>::get(h, j) + Vec8<half_t>::get(l, j);
+      split(fmaf(kA, x, v[j] * (1.f / kScaleB)), o[j], o2[j]);
+    }
+    *reinterpret_cast<tile::u4*>(a.out_lo + at) = *reinterpret_cast<const tile::u4*>(o2);
+  }
+  *reinterpret_cast<tile::u4*>(a.out + at) = *reinterpret_cast<const tile::u4*>(o);
+}
+
+// The tile of a symmetric output: those on and below the diagonal, row by row.
+__device__ __forceinline__ void place_lower(uint32_t t, uint32_t& m, uint32_t& n) {
+  uint32_t r = (uint32_t)((sqrtf(8.f * (float)t + 1.f) - 1.f) * 0.5f);
+  while (r * (r + 1) / 2 > t) --r;
+  while ((r + 1) * (r + 2) / 2 <= t) ++r;
+  m = r, n = t - r * (r + 1) / 2;
+}
+template <typename C, Kind kind>
+__device__ __forceinline__ typename C::Where where(const ProductArgs& a, uint32_t t) {
+  if constexpr (kind == Kind::kNext) {
+    return C::where(a.work, t, a.M, a.N);
+  } else {
+    uint32_t m, n;
+    place_lower(t, m, n);
+    typename C::Where at;
+    at.m0 = (int64_t)__builtin_amdgcn_readfirstlane(m) * C::BM;
+    at.n0 = (int)__builtin_amdgcn_readfirstlane(n) * C::BN;
+    at.mrows = a.M - (int)at.m0 < C::BM ? a.M - (int)at.m0 : C::BM;
+    at.ncols = a.N - at.n0 < C::BN ? a.N - at.n0 : C::BN;
+    return at;
+  }
+}
+
+template <typename C, Kind kind>
+__global__ __launch_bounds__(C::kThreads, 2) void muon_product_kernel(ProductArgs a) {
+  extern __shared__ __align__(16) uint8_t t_smem[];
+  if (a.skip && *a.skip) return;
+  tile::share(a.work, [&](uint32_t t, int s0, int s1, int slot) {
+    const typename C::Where at = where<C, kind>(a, t);
+    typename C::Acc acc;
+    C::run(a.src, at, a.N, s0, s1, t_smem, acc);
+    float* const part = slot < 0 ? nullptr : a.part + (int64_t)slot * C::BM * C::BN;
+    const bool mirror = kind != Kind::kNext && at.m0 != at.n0;
+    C::rows(acc, t_smem, [&](int r, int c, const float* p) {
+      float v[8];
+      tile::eight(p, v);
+      if (part) {
+        store8<float>(part + r * C::BN, c, C::BN, v);
+      } else if (r < at.mrows && c < at.ncols) {
+        finish8<kind>(a, v, at.m0 + r, at.n0 + c);
+      }
+    }, [&](int r0, int c0, const float* p) {
+      if (!mirror || part || r0 >= at.mrows) return;
+      // 16 rows of the tile are 16 columns of its mirror image
+      for (int c = (threadIdx.x & 63); c < C::kWaveN; c += 64) {
+        if (c0 + c >= at.ncols) continue;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float v[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = p[(8 * h + j) * C::kPad + c];
+          finish8<kind>(a, v, at.n0 + c0 + c, (int)at.m0 + r0 + 8 * h);
+        }
+      }
+    });
+    __syncthreads();
+  });
+}
+
+// Split tiles: a block takes 16 rows by 128 columns, 8 columns a thread, and adds the parts in the order of the sum
+template <typename C, Kind kind>
+__global__ __launch_bounds__(256) void muon_join_kernel(ProductArgs a) {
+  __shared__ float turn[16][132];
+  if (a.skip && *a.skip) return;
+  const typename C::Where at = where<C, kind>(a, a.work.full + blockIdx.x);
+  const int r0 = (int)blockIdx.y / (C::BN / 128) * 16, c0 = (int)blockIdx.y % (C::BN / 128) * 128;
+  const int r = threadIdx.x >> 4, c = (threadIdx.x & 15) * 8;
+  float v[8] = {};
+  tile::parts(a.work, blockIdx.x, [&](uint32_t slot) {
+    float p[8];
+    tile::eight(a.part + ((int64_t)slot * C::BM + r0 + r) * C::BN + c0 + c, p);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += p[j];
+  });
+  if (r0 + r < at.mrows && c0 + c < at.ncols) finish8<kind>(a, v, at.m0 + r0 + r, at.n0 + c0 + c);
+  if (kind == Kind::kNext || at.m0 == at.n0 || r0 >= at.mrows) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) turn[r][c + j] = v[j];
+  __syncthreads();
+  const int mc = threadIdx.x >> 1, h = (threadIdx.x & 1) * 8;
+  if (c0 + mc >= at.ncols) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = turn[h + j][mc];
+  finish8<kind>(a, v, at.n0 + c0 + mc, (int)at.m0 + r0 + h);
+}
+
+// ---------------------------------------------------------------------------------------------
+// the update
+// ---------------------------------------------------------------------------------------------
+struct ApplyArgs {
+  const half_t *hi, *lo;
+  int64_t m_pad;
+  float* W;
+  void* O;
+  int64_t ldw, ldo, N, K;
+  float keep, rate;  // W <- keep W - rate X
+  bool tall;
+  const int32_t* skip;
+};
+// A block owns 64 x 64 of W; a tall matrix reads X's block turned.
+template <typename TO>
+__global__ __launch_bounds__(256) void muon_apply_kernel(ApplyArgs a) {
+  __shared__ float tilev[64][65];
+  if (a.skip && *a.skip) return;
+  const int64_t r0 = (int64_t)blockIdx.y * 64, c0 = (int64_t)blockIdx.x * 64;  // of W
+  const int64_t xr = a.tall ? c0 : r0, xc = a.tall ? r0 : c0;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int r = q * 32 + (threadIdx.x >> 3), c = (threadIdx.x & 7) * 8;
+    const int64_t at = (xr + r) * a.m_pad + xc + c;
+    const Vec8<half_t>::Raw h = *reinterpret_cast<const Vec8<half_t>::Raw*>(a.hi + at);
+    const Vec8<half_t>::Raw l = *reinterpret_cast<const Vec8<half_t>::Raw*>(a.lo + at);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) tilev[r][c + j] = (Vec8<half_t>::get(h, j) + Vec8<half_t>::get(l, j)) * (1.f / kScaleX);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int r = q * 32 + (threadIdx.x >> 3), c = (threadIdx.x & 7) * 8;
+    if (r0 + r >= a.N || c0 + c >= a.K) continue;
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = a.tall ? tilev[c + j][r] : tilev[r][c + j];
+    if (a.O) store8<TO>(static_cast<TO*>(a.O) + (r0 + r) * a.ldo, (int)c0 + c, (int)a.K, x);
+    if (a.W) {
+      float w[8];
+      float* const row = a.W + (r0 + r) * a.ldw;
+      widen8<float>(load8<float>(row, (int)c0 + c, (int)a.K), w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = fmaf(a.keep, w[j], -a.rate * x[j]);
+      store8<float>(row, (int)c0 + c, (int)a.K, w);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------------------------
+typedef tile::Tile<half_t, 4, 2, 4, 8, 2, false, 0, 1, true> CSym;   // 256 x 256, rows along the sum
+typedef tile::Tile<half_t, 4, 2, 4, 8, 2, true, 0, 1, true> CNext;   // 256 x 256, [R][N]
+
+// Where everything lies in the workspace; n and m are padded to whole steps with zeros.
+struct Buffers {
+  int64_t n, m;
+  size_t part, x[4], a, b, sums, bytes;
+  tile::Lay gram, poly, next;
+};
+Buffers buffers(int64_t N, int64_t K) {
+  Buffers b{};
+  b.n = ((N < K ? N : K) + 63) / 64 * 64;
+  b.m = ((N < K ? K : N) + 63) / 64 * 64;
+  const int64_t tn = (b.n + 255) / 256, tm = (b.m + 255) / 256, tri = tn * (tn + 1) / 2;
+  constexpr double kStep = 1.3;  // us of a step of 256 x 256 tiles on every unit
+  b.gram = tile::lay(1, tri, b.m / 64, kStep, 256 * 1024);
+  b.poly = tile::lay(1, tri, b.n / 64, kStep, 256 * 1024);
+  b.next = tile::lay(tn, tm, b.n / 64, kStep, 256 * 1024);
+  const auto take = [&](size_t bytes) {
+    const size_t at = b.bytes;
+    b.bytes += (bytes + 255) / 256 * 256;
+    return at;
+  };
+  b.part = take(kMomentBlocks * sizeof(double));
+  for (size_t& x : b.x) x = take((size_t)b.n * (size_t)b.m * 2);
+  b.a = take((size_t)b.n * (size_t)b.n * 2);
+  b.b = take((size_t)b.n * (size_t)b.n * 2);
+  size_t most = b.gram.part_bytes > b.poly.part_bytes ? b.gram.part_bytes : b.poly.part_bytes;
+  most = b.next.part_bytes > most ? b.next.part_bytes : most;
+  b.sums = take(most);
+  return b;
+}
+
+template <typename C, Kind kind>
+hipError_t launch_product(const ProductArgs& a, hipStream_t s) {
+  static const hipError_t attr = hipFuncSetAttribute((const void*)muon_product_kernel<C, kind>,
+                                                     hipFuncAttributeMaxDynamicSharedMemorySize, C::kLds);
+  if (attr != hipSuccess) return attr;
+  muon_product_kernel<C, kind><<<a.work.grid, C::kThreads, C::kLds, s>>>(a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.work.full == a.work.tiles) return e;
+  muon_join_kernel<C, kind><<<dim3(a.work.tiles - a.work.full, C::BM / 16 * (C::BN / 128)), 256, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <typename TG>
+hipError_t launch_start(const MomentArgs& a, hipStream_t s) {
+  muon_moment_kernel<TG><<<kMomentBlocks, 256, 0, s>>>(a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  muon_start_kernel<TG><<<dim3((uint32_t)(a.m_pad / 64), (uint32_t)(a.n_pad / 64)), 256, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t muon_workspace_bytes(int64_t N, int64_t K) { return buffers(N, K).bytes; }
+
+hipError_t launch_muon_step(float* W, int64_t ldw, const void* G, rb_dtype g_dtype, int64_t ldg, float* mom, int64_t ldm,
+                            int64_t N, int64_t K, double lr, double momentum, int nesterov, double weight_decay,
+                            double scale, int steps, double eps, const float* grad_scale, const int32_t* skip, void* O,
+                            rb_dtype o_dtype, int64_t ldo, void* ws, hipStream_t s) {
+  const Buffers b = buffers(N, K);
+  char* const base = static_cast<char*>(ws);
+  const auto half_at = [&](size_t at) { return reinterpret_cast<half_t*>(base + at); };
+  half_t *hi = half_at(b.x[0]), *lo = half_at(b.x[1]), *hi2 = half_at(b.x[2]), *lo2 = half_at(b.x[3]);
+  half_t *const A = half_at(b.a), *const B = half_at(b.b);
+  float* const part = reinterpret_cast<float*>(base + b.sums);
+  const MomentArgs m{G, mom, ldg, ldm, N, K, (float)momentum, (float)eps, nesterov, grad_scale, skip,
+                     reinterpret_cast<double*>(base + b.part), hi, lo, b.m, b.n, N > K};
+  hipError_t e = g_dtype == RB_F32 ? launch_start<float>(m, s)
+                 : g_dtype == RB_F16 ? launch_start<_Float16>(m, s) : launch_start<__bf16>(m, s);
+  if (e != hipSuccess) return e;
+  const int n = (int)b.n, cols = (int)b.m;
+  for (int i = 0; i < steps; ++i) {
+    const ProductArgs gram{{{hi, hi, nullptr, b.m, b.m, 0, cols, cols / 64}}, n, n, b.gram.work, part, nullptr, nullptr,
+                           nullptr, A, nullptr, b.n, skip};
+    const ProductArgs poly{{{A, A, nullptr, b.n, b.n, 0, n, n / 64}}, n, n, b.poly.work, part, A, nullptr, nullptr, B,
+                           nullptr, b.n, skip};
+    const ProductArgs next{{{B, hi, nullptr, b.n, b.m, 0, n, n / 64}}, n, cols, b.next.work, part, nullptr, hi, lo, hi2,
+                           lo2, b.m, skip};
+    if ((e = launch_product<CSym, Kind::kGram>(gram, s)) != hipSuccess) return e;
+    if ((e = launch_product<CSym, Kind::kPoly>(poly, s)) != hipSuccess) return e;
+    if ((e = launch_product<CNext, Kind::kNext>(next, s)) != hipSuccess) return e;
+    half_t* t = hi; hi = hi2, hi2 = t;
+    t = lo, lo = lo2, lo2 = t;
+  }
+  const ApplyArgs p{hi, lo, b.m, W, O, ldw, ldo, N, K, (float)(1.0 - lr * weight_decay), (float)(lr * scale), N > K, skip};
+  const dim3 grid((uint32_t)((K + 63) / 64), (uint32_t)((N + 63) / 64));
+  if (o_dtype == RB_F16)
+    muon_apply_kernel<_Float16><<<grid, 256, 0, s>>>(p);
+  else
+    muon_apply_kernel<__bf16><<<grid, 256, 0, s>>>(p);
+  return hipGetLastError();
+}
+
+}  // namespace rb

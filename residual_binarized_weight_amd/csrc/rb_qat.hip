@@ -561,8 +561,10 @@ hipError_t launch_qat_backward(const void* dY, rb_dtype a_dtype, int64_t M, int6
     if (e != hipSuccess) return e;
     e = gemm_locked(hd, dev, shape_dw(a_dtype, M, ldx, lddy, N, K, lddw), X, dY, dW);
     if (e != hipSuccess) return e;
-    e = gemm_locked(hd, dev, shape_dx(a_dtype, M, ldwh, lddy, N, K, dx_dtype, lddx), What, dY, dX);
-    if (e != hipSuccess) return e;
+    if (dX) {
+      e = gemm_locked(hd, dev, shape_dx(a_dtype, M, ldwh, lddy, N, K, dx_dtype, lddx), What, dY, dX);
+      if (e != hipSuccess) return e;
+    }
   }
   switch (k) {
     case 1: return scale_grad_kp<1>(dW, N, K, lddw, planes, ldp, g, h, dg, dh, ws, stream);

@@ -1,0 +1,420 @@
+// rb_tile.hpp -- a tile of a dense product on the matrix cores, and how a product's tiles are laid over the GPU.
+//
+//   out [M][N] = A [M][R] B,   B given as [N][R] (rows along the sum) or as [R][N] (columns along it), 16-bit operands,
+//   fp32 sums; optionally two weight matrices side by side (their tiles' columns interleaved, so that one lane holds
+//   both values of an output), or two products whose sums run on from one another.
+//
+// The kernels that use it own their epilogues: rb_glu.hip, rb_muon.hip.
+#pragma once
+
+#include "rb_elem.hpp"
+
+namespace rb {
+namespace tile {
+
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+typedef __bf16 b8 __attribute__((ext_vector_type(8)));
+typedef float f4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+typedef short s4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) u4 lds_u4;
+typedef __attribute__((address_space(3))) s4 lds_s4;
+typedef __attribute__((address_space(3))) void lds_void;
+
+__device__ __forceinline__ f4 mfma(_Float16, u4 a, u4 b, f4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, a), __builtin_bit_cast(h8, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ f4 mfma(__bf16, u4 a, u4 b, f4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b8, a), __builtin_bit_cast(b8, b), c, 0, 0, 0);
+}
+
+// 16 bytes per lane from the buffer to LDS (lane l's at base + 16 l). The whole offset is the lane's, so that the
+// range check sees all of it.
+__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t r, uint8_t* base, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)base, 16, off, 0, 0, 0);
+}
+
+constexpr int kTK = 64;            // terms of the sum per step
+constexpr int kRowB = kTK * 2;     // bytes of a staged row along the sum
+constexpr uint32_t kOob = 0x80000000u;
+constexpr int kXcds = 8;
+constexpr int kUnits = 256;        // compute units, and blocks of a full grid
+
+// s_waitcnt immediates: vmcnt in bits 3:0 and 15:14, expcnt 6:4, lgkmcnt 11:8
+constexpr int kWaitLds = 15 | (3 << 14) | (7 << 4);  // lgkmcnt = 0 alone
+constexpr int wait_vmcnt(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8); }
+
+// One product: A rows along the sum; B, B2 as the tile's template says; R terms in `steps` steps of 64.
+template <typename T>
+struct Source {
+  const T *A, *B, *B2;
+  int64_t lda, ldb, ldb2;
+  int R, steps;
+};
+
+// How `tiles` tiles of `steps` steps are laid over a grid of `grid` blocks (a multiple of 8): the first `full` of them
+// whole, in rounds of the grid; the steps of the others in equal runs of `per` to the blocks, whose partial sums
+// a second kernel joins (two partial tiles a block: its run starts in one tile and may end in the next).
+struct Work {
+  uint32_t tiles, tiles_m, full, grid;
+  int steps, per;
+};
+// the m and n of a tile: panels of 8 tiles along m, so that the 32 tiles that an XCD's units work on at a time
+// share 8 blocks of A's rows and 4 of B's in its L2
+__device__ __forceinline__ void place(uint32_t t, uint32_t tiles_m, uint32_t tiles, uint32_t& m, uint32_t& n) {
+  const uint32_t tiles_n = tiles / tiles_m, panel = 8 * tiles_n, p = t / panel, r = t % panel;
+  const uint32_t high = tiles_m - 8 * p < 8 ? tiles_m - 8 * p : 8;
+  m = 8 * p + r % high;
+  n = r / high;
+}
+// a block's number with the blocks of one XCD next to each other
+__device__ __forceinline__ uint32_t block_of(uint32_t grid) { return blockIdx.x % kXcds * (grid / kXcds) + blockIdx.x / kXcds; }
+
+// WM x WN waves, each TM x TN accumulators of v_mfma_f32_16x16x32: a tile of 16 WM TM rows by 16 WN TN columns. A step
+// of 64 terms is one LDS stage of a ring of kS, and is two phases of 32 terms; a phase's fragments are read while
+// the phase before it multiplies. In the middle of step s (the second phase's fragments are then in registers,
+// so its stage is free) a wave waits for its own loads of step s + 1, the barrier makes everyone's visible, and
+// the loads of step s + kS go into the freed stage.
+//
+// kNN: B is [R][N]; its fragments are read from LDS by the transposing read, whose 16 lanes take 4 rows by 16 columns.
+// kHalf: of each wave's columns the first kHalf are B's and the others, for the same outputs, B2's; 0: B alone.
+// kSrc: products whose sums run on from one another.
+// kAl: rows of both operands are 16-byte aligned, R (and N where kNN) a multiple of 8: the rows go to LDS directly
+// (buffer loads, which give 0 past a tile's rows and past the sum's end). Otherwise they pass through
+// registers one step ahead, by 16-byte loads at any address; the vector that holds the end of a row is read 8
+// elements before it and shifted.
+template <typename T, int kWM, int kWN, int kTM, int kTN, int kS, bool kNN, int kHalf, int kSrc, bool kAl>
+struct Tile {
+  static constexpr int kWaves = kWM * kWN, kThreads = 64 * kWaves;
+  static constexpr int BM = 16 * kWM * kTM, BN = 16 * kWN * kTN;       // staged rows of A and rows (columns) of B
+  static constexpr int kOutN = kHalf ? BN / 2 : BN;                    // columns of the output
+  static constexpr int kWaveN = kHalf ? kHalf : 16 * kTN;              // ... of one wave
+  static constexpr int kStageA = BM * kRowB, kStage = kStageA + BN * kRowB;
+  static constexpr int kPerA = BM / 8 / kWaves, kPerB = BN / 8 / kWaves, kPer = kPerA + kPerB;  // 1 KB groups per wave and step
+  static constexpr int kRowNN = BN * 2;                                // bytes of a staged row of [R][N]
+  static constexpr int kPad = 16 * kTN + 4;                            // floats of a row in the epilogue's LDS area
+  static constexpr int kTurn = kWaves * 16 * kPad * 4;
+  static constexpr int kLds = kS * kStage > kTurn ? kS * kStage : kTurn;
+  static_assert(BM / 8 % kWaves == 0 && BN / 8 % kWaves == 0, "a load instruction has one operand");
+  static_assert(kAl || kS == 2, "through registers a step is written two steps ahead");
+  static_assert(!kHalf || (2 * kHalf == 16 * kTN && !kNN), "a wave holds both values of an output");
+  static_assert(!kNN || BN == 256, "the transposing read's rows are 512 bytes");
+  static_assert(kLds <= 160 * 1024, "LDS of a compute unit");
+
+  static constexpr int kHalfN = kHalf;
+  typedef f4 Acc[kTM][kTN];
+
+  struct Where {
+    int64_t m0;
+    int n0, mrows, ncols;  // rows and columns that lie inside; n0, ncols count outputs
+  };
+  __device__ static __forceinline__ Where where(const Work& k, uint32_t t, int64_t M, int N) {
+    uint32_t tm, tn;
+    place(t, k.tiles_m, k.tiles, tm, tn);
+    Where at;
+    at.m0 = (int64_t)__builtin_amdgcn_readfirstlane(tm) * BM;
+    at.n0 = (int)__builtin_amdgcn_readfirstlane(tn) * kOutN;
+    at.mrows = M - at.m0 < BM ? (int)(M - at.m0) : BM;
+    at.ncols = N - at.n0 < kOutN ? N - at.n0 : kOutN;
+    return at;
+  }
+
+  // the sum's steps s0 .. s1 - 1 of the tile at `at` into acc. LDS is free for use before and after.
+  __device__ static __forceinline__ void run(const Source<T> (&src)[kSrc], const Where& at, int N, int s0, int s1, uint8_t* smem,
+                                             f4 (&acc)[kTM][kTN]) {
+    const int lane = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int wm = w % kWM, wn = w / kWM;
+    const int lr = lane & 15, lj = lane >> 4;
+
+    // Rows along the sum: 1 KB groups of 8 rows; lane l fills slot l % 8 of row l / 8 with the 16-byte chunk
+    // (l % 8) ^ (row % 8), so that the 8 rows of a fragment read's phase lie in 8 bank groups.
+    // Rows of [R][N]: groups of 2 rows of 512 bytes; the 32-byte piece p of row k lies at p ^ ((k % 4) + 4 (k / 8 % 2)),
+    // so that the 8 rows that 32 lanes of a transposing read take lie in 8 bank groups.
+    const int xc = (lane & 7) ^ (lane >> 3);
+    const int kr = lane >> 5;
+    const int xn = (lane & 31) ^ (((2 * w + kr) & 3) | (w & 4)) * 2;
+    const auto group_row = [&](int i) { return 8 * (i * kWaves + w); };  // of A, or of B with rows along the sum
+    // B's rows: the wave that they belong to, which of two matrices, and the row counted in outputs
+    const auto second = [&](int r) { return kHalf && (r / (kHalf ? kHalf : 1) & 1); };
+    const auto out_row = [&](int r) { return kHalf ? r / (2 * kHalf) * kHalf + r % kHalf : r; };
+
+    const auto dma = [&](int s, int stage) {
+      const bool live = s < s1, next = kSrc == 2 && s >= src[0].steps;
+      const Source<T>& q = src[kSrc == 2 && next ? kSrc - 1 : 0];
+      const int k0 = (next ? s - src[0].steps : s) * kTK;
+      const bool ok = live && k0 + 8 * xc < q.R;
+      uint8_t* const base = smem + stage * kStage;
+      const uint32_t la = (uint32_t)q.lda * 2, lb = (uint32_t)q.ldb * 2;
+      const __amdgpu_buffer_rsrc_t ra =
+          buffer_rsrc(q.A + at.m0 * q.lda, (uint32_t)((at.mrows - 1) * (int)la + q.R * 2));
+      const uint32_t va = (uint32_t)(lane >> 3) * la + 16u * xc + (uint32_t)k0 * 2;
+#pragma unroll
+      for (int i = 0; i < kPerA; ++i)
+        load_to_lds(ra, base + (i * kWaves + w) * 1024, ok ? va + (uint32_t)group_row(i) * la : kOob);
+      if constexpr (kNN) {
+        const int rows = q.R - k0;
+        const __amdgpu_buffer_rsrc_t rb = buffer_rsrc(
+            q.B + (live ? (int64_t)k0 * q.ldb : 0),
+            live && rows > 0 ? (uint32_t)(((rows < kTK ? rows : kTK) - 1) * (int)lb + N * 2) : 0u);
+        const uint32_t vb = (uint32_t)kr * lb + 16u * xn + (uint32_t)at.n0 * 2;
+#pragma unroll
+        for (int i = 0; i < kPerB; ++i)
+          load_to_lds(rb, base + kStageA + (i * kWaves + w) * 1024, vb + (uint32_t)(2 * (i * kWaves + w)) * lb);
+      } else {
+        const __amdgpu_buffer_rsrc_t rb =
+            buffer_rsrc(q.B + (int64_t)at.n0 * q.ldb, (uint32_t)((at.ncols - 1) * (int)lb + q.R * 2));
+        const uint32_t lb2 = kHalf ? (uint32_t)q.ldb2 * 2 : lb;
+        const __amdgpu_buffer_rsrc_t rb2 =
+            kHalf ? buffer_rsrc(q.B2 + (int64_t)at.n0 * q.ldb2, (uint32_t)((at.ncols - 1) * (int)lb2 + q.R * 2)) : rb;
+        const uint32_t vb = (uint32_t)(lane >> 3) * lb + 16u * xc + (uint32_t)k0 * 2;
+        const uint32_t vb2 = (uint32_t)(lane >> 3) * lb2 + 16u * xc + (uint32_t)k0 * 2;
+#pragma unroll
+        for (int i = 0; i < kPerB; ++i) {
+          const int r = group_row(i);
+          const bool two = second(r);
+          load_to_lds(two ? rb2 : rb, base + kStageA + (i * kWaves + w) * 1024,
+                      ok ? (two ? vb2 + (uint32_t)out_row(r) * lb2 : vb + (uint32_t)out_row(r) * lb) : kOob);
+        }
+      }
+    };
+
+    u4 hold[kAl ? 1 : kPer];
+    // a vector of a row of n elements at c, zeros past its end
+    const auto vec = [](const T* row, int c, int n) {
+      typename Vec8<T>::Raw r = {};
+      if (n >= 8) {
+        load8_long<T>(r, row, c, n);
+        if (c < n && c + 8 > n) shift_down(r, 8 - n % 8);
+      } else {
+        r = load8<T>(row, c, n);
+      }
+      return __builtin_bit_cast(u4, r);
+    };
+    const auto fetch = [&](int s, u4 (&hold)[kAl ? 1 : kPer]) {
+      const bool next = kSrc == 2 && s >= src[0].steps;
+      const Source<T>& q = src[kSrc == 2 && next ? kSrc - 1 : 0];
+      const int k0 = (next ? s - src[0].steps : s) * kTK, c = k0 + 8 * xc;
+      const bool whole = k0 + kTK <= q.R;
+#pragma unroll
+      for (int i = 0; i < kPerA; ++i) {  // a row past the last one repeats it: its outputs are not stored
+        const int r = group_row(i) + (lane >> 3);
+        const T* const row = q.A + (at.m0 + (r < at.mrows ? r : at.mrows - 1)) * q.lda;
+        hold[i] = whole ? __builtin_bit_cast(u4, *reinterpret_cast<const typename Vec8<T>::Raw*>(row + c)) : vec(row, c, q.R);
+      }
+#pragma unroll
+      for (int i = 0; i < kPerB; ++i) {
+        if constexpr (kNN) {  // a row past the sum's end is zero
+          const int k = k0 + 2 * (i * kWaves + w) + kr, col = at.n0 + 8 * xn;
+          const u4 v = k < q.R ? vec(q.B + (int64_t)k * q.ldb, col, N) : (u4){0, 0, 0, 0};
+          hold[kPerA + i] = v;
+        } else {
+          const int g = group_row(i), r = out_row(g) + (lane >> 3);
+          const bool two = second(g);
+          const T* const row = (two ? q.B2 : q.B) + (int64_t)(at.n0 + (r < at.ncols ? r : at.ncols - 1)) * (two ? q.ldb2 : q.ldb);
+          hold[kPerA + i] = whole ? __builtin_bit_cast(u4, *reinterpret_cast<const typename Vec8<T>::Raw*>(row + c)) : vec(row, c, q.R);
+        }
+      }
+    };
+    const auto put = [&](int stage, const u4 (&hold)[kAl ? 1 : kPer]) {
+#pragma unroll
+      for (int i = 0; i < (kAl ? 1 : kPer); ++i)
+        *reinterpret_cast<u4*>(smem + stage * kStage + (i < kPerA ? 0 : kStageA) + ((i < kPerA ? i : i - kPerA) * kWaves + w) * 1024 +
+                               lane * 16) = hold[i];
+    };
+
+#pragma unroll
+    for (int i = 0; i < kTM; ++i)
+#pragma unroll
+      for (int j = 0; j < kTN; ++j) acc[i][j] = (f4){0.f, 0.f, 0.f, 0.f};
+
+    const uint32_t lds0 = (uint32_t)(size_t)(__attribute__((address_space(3))) uint8_t*)smem;
+    const uint32_t f0 = lr * kRowB + 16u * ((uint32_t)lj ^ (lr & 7u)), f1 = lr * kRowB + 16u * ((4u + lj) ^ (lr & 7u));
+    const uint32_t aa = lds0 + wm * kTM * 16 * kRowB;
+    const uint32_t ab = lds0 + kStageA + (kNN ? (8 * lj + (lr >> 2)) * kRowNN + 8 * (lr & 3) : wn * kTN * 16 * kRowB);
+    const uint32_t turn_nn = (lr >> 2) | (lj & 1) << 2;
+    u4 xf[2][kTM], wf[2][kTN];
+    const auto read = [&](int kh, int stage) {  // the fragments of half kh of a stage
+#pragma unroll
+      for (int j = 0; j < kTN; ++j) {
+        if constexpr (kNN) {
+          const uint32_t p = ab + stage * kStage + kh * 32 * kRowNN + 32 * (((uint32_t)(wn * kTN + j)) ^ turn_nn);
+          const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(size_t)p);
+          const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(size_t)(p + 4 * kRowNN));
+          wf[kh][j] = __builtin_bit_cast(u4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        } else {
+          wf[kh][j] = *(lds_u4*)(size_t)(ab + stage * kStage + j * 16 * kRowB + (kh ? f1 : f0));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kTM; ++i)
+        xf[kh][i] = *(lds_u4*)(size_t)(aa + stage * kStage + i * 16 * kRowB + (kh ? f1 : f0));
+    };
+    const auto multiply = [&](int kh) {
+#pragma unroll
+      for (int i = 0; i < kTM; ++i)
+#pragma unroll
+        for (int j = 0; j < kTN; ++j) acc[i][j] = mfma(T(0), wf[kh][j], xf[kh][i], acc[i][j]);
+    };
+    constexpr int kReads = kTM + kTN * (kNN ? 2 : 1);
+    const auto spread = [] {  // the reads over the products
+#pragma unroll
+      for (int r = 0; r < kReads; ++r) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // MFMA
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // LDS read
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    const auto barrier = [] {  // the raw barrier: __syncthreads would also wait for every load in flight
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+    };
+
+    if constexpr (kAl) {
+#pragma unroll
+      for (int s = 0; s < kS; ++s) dma(s0 + s, s);
+      __builtin_amdgcn_s_waitcnt(wait_vmcnt((kS - 1) * kPer));
+    } else {
+      u4 ahead[kAl ? 1 : kPer];
+      fetch(s0, hold);
+      fetch(s0 + 1, ahead);
+      put(0, hold);
+      put(1, ahead);
+      fetch(s0 + 2, hold);
+      __builtin_amdgcn_s_waitcnt(kWaitLds);
+    }
+    barrier();
+    read(0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    int st = 0;
+    for (int s = s0; s < s1; ++s) {
+      read(1, st);
+      multiply(0);
+      spread();
+      const int next = st + 1 == kS ? 0 : st + 1;
+      __builtin_amdgcn_s_waitcnt(kAl ? wait_vmcnt((kS - 2) * kPer) & kWaitLds : kWaitLds);
+      barrier();
+      if constexpr (kAl) {
+        dma(s + kS, st);
+      } else {
+        put(st, hold);
+        fetch(s + 3, hold);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      read(0, next);
+      multiply(1);
+      spread();
+      st = next;
+    }
+    // loads past the last step (out of range, zeros) end before LDS is used again
+    __builtin_amdgcn_s_waitcnt(wait_vmcnt(0));
+    __syncthreads();
+  }
+
+  // The accumulators by rows: 16 rows at a time through the wave's own LDS area, so that consecutive lanes hold
+  // consecutive columns and whole lines are read and written. f(row, column, p): the tile's row, the output column
+  // counted from n0 (a multiple of 8), and p[0 .. 7] its fp32 sums (p[kHalf .. kHalf + 7] the second matrix's).
+  // D of the product: lane l holds columns 4 (l / 16) .. + 3 of row l % 16. `turned`(row, p) is called once for 16 rows
+  // and sees all of them (row stride kPad). LDS must be free; the block synchronises before its next use.
+  template <typename F, typename G>
+  __device__ static __forceinline__ void rows(const f4 (&acc)[kTM][kTN], uint8_t* smem, F f, G turned) {
+    const int lane = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int wm = w % kWM, wn = w / kWM;
+    const int lr = lane & 15, lj = lane >> 4;
+    float* const turn = reinterpret_cast<float*>(smem) + w * (16 * kPad);
+    constexpr int kLanes = kWaveN / 8, kAtOnce = 64 / kLanes;  // lanes of a row, rows at once
+#pragma unroll 1
+    for (int i = 0; i < kTM; ++i) {
+#pragma unroll
+      for (int q = 0; q < kTM; ++q)
+        if (q == i) {
+#pragma unroll
+          for (int j = 0; j < kTN; ++j) *reinterpret_cast<f4*>(turn + lr * kPad + 16 * j + 4 * lj) = acc[q][j];
+        }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll 1
+      for (int s = 0; s < 16 / kAtOnce; ++s) {
+        const int r = kAtOnce * s + lane / kLanes, c = 8 * (lane % kLanes);
+        f((wm * kTM + i) * 16 + r, wn * kWaveN + c, turn + r * kPad + c);
+      }
+      turned((wm * kTM + i) * 16, wn * kWaveN, turn);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+  }
+};
+
+__device__ __forceinline__ void eight(const float* p, float (&v)[8]) {
+  const f4 lo = *reinterpret_cast<const f4*>(p), hi = *reinterpret_cast<const f4*>(p + 4);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = lo[j], v[4 + j] = hi[j];
+}
+
+// A block's share of the work, tile by tile: body(tile, first step, end step, slot): slot -1 for a whole tile, else the
+// partial tile in the workspace that takes the sums.
+template <typename F>
+__device__ __forceinline__ void share(const Work& k, F body) {
+  const uint32_t lb = block_of(k.grid);
+  uint32_t t = lb, it = lb * (uint32_t)k.per, slot = 2 * lb;
+  const uint32_t all = (k.tiles - k.full) * (uint32_t)k.steps;
+  const uint32_t end = it + (uint32_t)k.per < all ? it + (uint32_t)k.per : all;
+  for (;;) {
+    uint32_t tile = t;
+    int s0 = 0, s1 = k.steps, to = -1;
+    if (t < k.full) {
+      t += k.grid;
+    } else if (it < end) {
+      const uint32_t q = it / (uint32_t)k.steps;
+      tile = k.full + q;
+      s0 = (int)(it - q * (uint32_t)k.steps);
+      if (k.steps - s0 > (int)(end - it)) s1 = s0 + (int)(end - it);
+      to = (int)slot++;
+      it += (uint32_t)(s1 - s0);
+    } else {
+      break;
+    }
+    body(tile, s0, s1, to);
+  }
+}
+
+// The partial tiles of split tile q (counted from `full`), in the order of the sum: f(slot) for each.
+template <typename F>
+__device__ __forceinline__ void parts(const Work& k, uint32_t q, F f) {
+  const uint32_t a = q * (uint32_t)k.steps, b = a + (uint32_t)k.steps, per = (uint32_t)k.per;
+  for (uint32_t lb = a / per; lb * per < b; ++lb) f(2 * lb + (lb * per < a ? 1 : 0));
+}
+
+// The rest of a product's tiles that does not fill a round of the grid, in equal runs of steps where that is estimated
+// to take less time than one more round: a run is 4 steps at least; a split costs its partial tiles' way to memory and
+// back (5 MB / us) and 4 us for the second launch. `step`: us of one step when every unit works.
+struct Lay {
+  Work work;
+  double est;
+  size_t part_bytes;  // of the partial tiles
+};
+inline Lay lay(int64_t tiles_m, int64_t tiles_n, int64_t steps, double step, int64_t tile_bytes) {
+  const int64_t tiles = tiles_m * tiles_n, rounds = tiles / kUnits, rest = tiles % kUnits;
+  const auto eights = [](int64_t n) { return (uint32_t)((n + kXcds - 1) / kXcds * kXcds); };
+  Lay l{};
+  l.work.tiles = (uint32_t)tiles, l.work.tiles_m = (uint32_t)tiles_m, l.work.steps = (int)steps;
+  l.work.full = (uint32_t)tiles;
+  l.work.grid = rounds > 0 ? (uint32_t)kUnits : eights(rest);
+  l.est = 5.0 + (double)(rounds + (rest > 0)) * (double)(steps + 3) * step;
+  if (rest == 0 || rest * steps >= (int64_t)1 << 31) return l;
+  const int64_t total = rest * steps, most = (total + 3) / 4;
+  const int64_t grid = rounds > 0 || most >= kUnits ? kUnits : eights(most), per = (total + grid - 1) / grid;
+  if (per >= steps) return l;
+  const int64_t bytes = 2 * grid * tile_bytes, moved = ((total + per - 1) / per + rest) * tile_bytes;
+  const double est = 9.0 + (double)rounds * (double)(steps + 3) * step + (double)(per + 3) * step + (double)moved * 2 / 5e6;
+  if (est >= l.est) return l;
+  l.work.full = (uint32_t)(tiles - rest), l.work.grid = (uint32_t)grid, l.work.per = (int)per;
+  l.est = est, l.part_bytes = (size_t)bytes;
+  return l;
+}
+
+inline bool rows16(const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0; }
+inline bool lines(const void* p, int64_t ld, int size) { return reinterpret_cast<uintptr_t>(p) % 128 == 0 && ld * size % 128 == 0; }
+
+}  // namespace tile
+}  // namespace rb
