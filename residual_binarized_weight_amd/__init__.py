@@ -734,9 +734,14 @@ def orthogonalize(G: torch.Tensor, steps: int = 5, eps: float = 1e-7, o_dtype=to
     return O
 
 
+@functools.lru_cache(maxsize=4096)
+def _q4_words(N: int, K: int) -> int:
+    return lib.rb_q4_codes_bytes(N, K) // 4
+
+
 def _q4(name: str, codes: torch.Tensor, s: torch.Tensor, z: torch.Tensor | None, N: int, K: int, group: int):
     """Pointers of one 4-bit weight, its shapes checked."""
-    if codes.dtype is not torch.int32 or codes.numel() * 4 != lib.rb_q4_codes_bytes(N, K):
+    if codes.dtype is not torch.int32 or codes.numel() != _q4_words(N, K):
         raise ValueError(f"{name}: codes are int32 [ceil(N / 16)][ceil(K / 128)][64][4]")
     for t in (s, z):
         if t is not None and (t.dtype is not torch.float16 or t.numel() != -(-K // group) * N):

@@ -7,17 +7,14 @@
 // lane 16 j + r of a tile holds row r; its word i holds columns 32 i + 8 j .. + 7, column c of those in the four bits
 // from 16 (c % 2) + 4 (c / 2) on, so that a shift and a mask leave columns 2 p and 2 p + 1 in the halves of a register.
 //
-// Kernels of this file: q4_pack_kernel, q4_dequant_kernel (a wave per tile), q4_product_kernel.
-#include "rb_act.hpp"
-#include "rb_internal.h"
-#include "rb_tile.hpp"
+// Kernels of this file: q4_pack_kernel, q4_dequant_kernel (a wave per tile). The products: rb_q4_product.hpp.
+#include "rb_elem.hpp"
+#include "rb_q4_product.hpp"
 
 namespace rb {
 namespace {
 
-using tile::f4;
-using tile::u4;
-
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 constexpr int kTileN = 16, kTileK = 128;
 
 // ---------------------------------------------------------------------------------------------
@@ -123,155 +120,6 @@ __global__ __launch_bounds__(256) void q4_dequant_kernel(DequantArgs a) {
   }
 }
 
-// ---------------------------------------------------------------------------------------------
-// the product: a block owns 16 weight rows (of both weights of a pair); its 8 waves take the 128-column tiles in turn
-// and join in LDS in their order. HBM's rate for the codes is the bound. A code becomes a number of the activations'
-// type without arithmetic: in the top four fraction bits above 16, it reads 16 + q. So a group's sum of products is
-// s (D - 24 S), or s D + (z - 16 s) S with offsets, with D the matrix instructions' sum over 16 + q and S the sum of the
-// group's x, which an instruction with ones for weights gives in the same lanes. All sums are fp32; 16 + q against
-// q - 8 costs about two bits of them.
-// ---------------------------------------------------------------------------------------------
-struct Q4Weights {
-  const uint32_t* codes;
-  const _Float16 *s, *z;
-};
-struct Q4Args {
-  Q4Weights w[2];
-  const void* x;
-  void* y;
-  int64_t ldx, ldy, N, first;
-  int M, K, steps, act;
-};
-
-template <typename T> struct Nib;
-template <> struct Nib<_Float16> {  // 16 + q: 0x4c00 with q in bits 9 .. 6
-  static constexpr uint32_t kOne = 0x3c003c00u;
-  __device__ static __forceinline__ u4 widen(uint32_t w) {
-    const uint32_t m = 0x03c003c0u, b = 0x4c004c00u;
-    return (u4){(w << 6 & m) | b, (w << 2 & m) | b, (w >> 2 & m) | b, (w >> 6 & m) | b};
-  }
-};
-template <> struct Nib<__bf16> {  // 16 + q: 0x4180 with q in bits 6 .. 3
-  static constexpr uint32_t kOne = 0x3f803f80u;
-  __device__ static __forceinline__ u4 widen(uint32_t w) {
-    const uint32_t m = 0x00780078u, b = 0x41804180u;
-    return (u4){(w << 3 & m) | b, (w >> 1 & m) | b, (w >> 5 & m) | b, (w >> 9 & m) | b};
-  }
-};
-
-// four rows' scales, n .. n + 3, of a group
-__device__ __forceinline__ f4 scales4(const _Float16* s, int64_t n, int64_t N) {
-  typedef uint32_t u2 __attribute__((ext_vector_type(2), aligned(2)));
-  typedef _Float16 q4 __attribute__((ext_vector_type(4)));
-  if (n + 4 <= N) {
-    const u2 v = *reinterpret_cast<const u2*>(s + n);
-    const q4 h = __builtin_bit_cast(q4, v);
-    return (f4){(float)h[0], (float)h[1], (float)h[2], (float)h[3]};
-  }
-  f4 v;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) v[e] = (float)s[n + e < N ? n + e : N - 1];  // a row past the last one repeats it
-  return v;
-}
-
-template <typename T, typename TY, int kGroup, bool kPair>
-__global__ __launch_bounds__(512) void q4_product_kernel(Q4Args a) {
-  constexpr int kWaves = 8, kAhead = 2, kMat = kPair ? 2 : 1;
-  constexpr int kGroups = kTileK / kGroup, kEach = kGroup / 32;
-  __shared__ __align__(16) float sums[kMat][kWaves][256];
-  const int lane = threadIdx.x & 63, lr = lane & 15, lj = lane >> 4;
-  const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int64_t tile_n = a.first + blockIdx.x, n0 = tile_n * kTileN;
-  const T* const x = static_cast<const T*>(a.x) + (lr < a.M ? lr : 0) * a.ldx;
-  f4 total[kMat];
-#pragma unroll
-  for (int q = 0; q < kMat; ++q) total[q] = (f4){0.f, 0.f, 0.f, 0.f};
-  const u4 ones = {Nib<T>::kOne, Nib<T>::kOne, Nib<T>::kOne, Nib<T>::kOne};
-  for (int k0 = w; k0 < a.steps; k0 += kWaves * kAhead) {
-    u4 code[kAhead][kMat];
-    u4 xf[kAhead][4];
-    f4 s[kAhead][kMat][kGroups], z[kAhead][kMat][kGroups];
-#pragma unroll
-    for (int p = 0; p < kAhead; ++p) {
-      const int k = k0 + p * kWaves;
-      if (k >= a.steps) break;
-#pragma unroll
-      for (int q = 0; q < kMat; ++q) {
-        code[p][q] = *reinterpret_cast<const u4*>(a.w[q].codes + ((tile_n * a.steps + k) * 64 + lane) * 4);
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          // the last tile's groups past the columns repeat the last one: their x are zero
-          const int64_t groups = (a.K + kGroup - 1) / kGroup, at = (int64_t)k * kGroups + g;
-          const int64_t off = (at < groups ? at : groups - 1) * a.N;
-          s[p][q][g] = scales4(a.w[q].s + off, n0 + 4 * lj, a.N);
-          if (a.w[q].z) z[p][q][g] = scales4(a.w[q].z + off, n0 + 4 * lj, a.N);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        xf[p][i] = lr < a.M ? __builtin_bit_cast(u4, load8_any<T>(x, k * kTileK + 32 * i + 8 * lj, a.K)) : (u4){0, 0, 0, 0};
-    }
-#pragma unroll
-    for (int p = 0; p < kAhead; ++p) {
-      if (k0 + p * kWaves >= a.steps) break;
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g) {
-        f4 d[kMat], xs = (f4){0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int q = 0; q < kMat; ++q) d[q] = (f4){0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = g * kEach; i < (g + 1) * kEach; ++i) {
-          xs = tile::mfma(T(0), ones, xf[p][i], xs);
-#pragma unroll
-          for (int q = 0; q < kMat; ++q) d[q] = tile::mfma(T(0), Nib<T>::widen(code[p][q][i]), xf[p][i], d[q]);
-        }
-#pragma unroll
-        for (int q = 0; q < kMat; ++q)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float sc = s[p][q][g][e];
-            const float off = a.w[q].z ? z[p][q][g][e] - 16.f * sc : -24.f * sc;
-            total[q][e] = fmaf(sc, d[q][e], fmaf(off, xs[e], total[q][e]));
-          }
-      }
-    }
-  }
-#pragma unroll
-  for (int q = 0; q < kMat; ++q) *reinterpret_cast<f4*>(&sums[q][w][lane * 4]) = total[q];
-  __syncthreads();
-  // thread 16 m + n: D's lane 16 (n / 4) + m holds weight row n in element n % 4
-  if (threadIdx.x >= 256) return;
-  const int m = threadIdx.x >> 4, nn = threadIdx.x & 15;
-  const int64_t n = n0 + nn;
-  if (m >= a.M || n >= a.N) return;
-  float v[kMat];
-#pragma unroll
-  for (int q = 0; q < kMat; ++q) {
-    v[q] = 0.f;
-#pragma unroll
-    for (int i = 0; i < kWaves; ++i) v[q] += sums[q][i][((nn >> 2) * 16 + m) * 4 + (nn & 3)];
-  }
-  static_cast<TY*>(a.y)[m * a.ldy + n] = Vec8<TY>::narrow(kPair ? act_value(v[0], a.act) * v[kMat - 1] : v[0]);
-}
-
-template <typename T, typename TY, bool kPair>
-hipError_t launch_grouped(Q4Args a, int group, hipStream_t s) {
-  return launch_in_parts((a.N + kTileN - 1) / kTileN, [&](int64_t first, uint32_t blocks) {
-    a.first = first;
-    if (group == 32)
-      q4_product_kernel<T, TY, 32, kPair><<<blocks, 512, 0, s>>>(a);
-    else if (group == 64)
-      q4_product_kernel<T, TY, 64, kPair><<<blocks, 512, 0, s>>>(a);
-    else
-      q4_product_kernel<T, TY, 128, kPair><<<blocks, 512, 0, s>>>(a);
-  });
-}
-template <typename T>
-hipError_t launch_typed(const Q4Args& a, int group, bool pair, rb_dtype y_dtype, hipStream_t s) {
-  if (pair) return y_dtype == RB_F32 ? launch_grouped<T, float, true>(a, group, s) : launch_grouped<T, T, true>(a, group, s);
-  return y_dtype == RB_F32 ? launch_grouped<T, float, false>(a, group, s) : launch_grouped<T, T, false>(a, group, s);
-}
-
 template <typename TW>
 hipError_t launch_pack_typed(PackArgs a, int group, hipStream_t s) {
   return launch_in_parts((a.all + 3) / 4, [&](int64_t first, uint32_t blocks) {
@@ -317,10 +165,9 @@ hipError_t launch_q4_product(const uint32_t* codes, const void* s, const void* z
                              const void* z2, int64_t N, int64_t K, int group, int act, const void* x, rb_dtype x_dtype,
                              int64_t M, int64_t ldx, void* y, rb_dtype y_dtype, int64_t ldy, hipStream_t stream) {
   const auto half_of = [](const void* p) { return static_cast<const _Float16*>(p); };
-  const Q4Args a{{{codes, half_of(s), half_of(z)}, {codes2, half_of(s2), half_of(z2)}}, x, y, ldx, ldy, N, 0, (int)M, (int)K,
-                 (int)((K + kTileK - 1) / kTileK), act};
-  return x_dtype == RB_F16 ? launch_typed<_Float16>(a, group, codes2 != nullptr, y_dtype, stream)
-                           : launch_typed<__bf16>(a, group, codes2 != nullptr, y_dtype, stream);
+  const q4::Args a{{{codes, half_of(s), half_of(z)}, {codes2, half_of(s2), half_of(z2)}}, x, y, ldx, ldy, N, 0, (int)M, (int)K,
+                 (int)((K + kTileK - 1) / kTileK), act, y_dtype == RB_F32};
+  return x_dtype == RB_F16 ? q4::launch_f16(a, group, codes2 != nullptr, stream) : q4::launch_bf16(a, group, codes2 != nullptr, stream);
 }
 
 }  // namespace rb
