@@ -48,7 +48,7 @@ struct MomentArgs {
   const float* grad_scale;
   const int32_t* skip;
   double* part;  // [kMomentBlocks] sums of u^2
-  half_t *hi, *lo;  // X, n_pad rows of m_pad
+  half_t *hi, *lo, *t;  // X, n_pad rows of m_pad, and its first half's transpose
   int64_t m_pad, n_pad;
   bool tall;  // X is u^T
 };
@@ -135,18 +135,25 @@ __global__ __launch_bounds__(256) void muon_start_kernel(MomentArgs a) {
   __syncthreads();
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    const int r = q * 32 + (threadIdx.x >> 3), c = (threadIdx.x & 7) * 8;  // of X
-    half_t hi[8], lo[8];
+    const int r = q * 32 + (threadIdx.x >> 3), c = (threadIdx.x & 7) * 8;  // of X, and of its transpose
+    half_t hi[8], lo[8], t[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) split(a.tall ? tilev[c + j][r] : tilev[r][c + j], hi[j], lo[j]);
-    const int64_t at = ((int64_t)blockIdx.y * 64 + r) * a.m_pad + (int64_t)blockIdx.x * 64 + c;
+    for (int j = 0; j < 8; ++j) {
+      const float along = tilev[r][c + j], across = tilev[c + j][r];
+      split(a.tall ? across : along, hi[j], lo[j]);
+      t[j] = (half_t)(a.tall ? along : across);
+    }
+    const int64_t xr = (int64_t)blockIdx.y * 64, xc = (int64_t)blockIdx.x * 64;
+    const int64_t at = (xr + r) * a.m_pad + xc + c;
     *reinterpret_cast<tile::u4*>(a.hi + at) = *reinterpret_cast<const tile::u4*>(hi);
     *reinterpret_cast<tile::u4*>(a.lo + at) = *reinterpret_cast<const tile::u4*>(lo);
+    *reinterpret_cast<tile::u4*>(a.t + (xc + r) * a.n_pad + xr + c) = *reinterpret_cast<const tile::u4*>(t);
   }
 }
 
 // ---------------------------------------------------------------------------------------------
-// the products
+// the products, all of rows along the sum: X is kept with its first half's transpose, which X' = a X + B X takes (the
+// transposing LDS read of rows across the sum takes 18 % more time than the transpose costs to write)
 // ---------------------------------------------------------------------------------------------
 enum class Kind { kGram, kPoly, kNext };  // A = X X^T; B = b A + c A A; X' = a X + B X
 
@@ -158,13 +165,14 @@ struct ProductArgs {
   const half_t* A;         // kPoly: A
   const half_t *hi, *lo;   // kNext: X
   half_t *out, *out_lo;
-  int64_t ld;
+  half_t* out_t;           // the output's (first half's) transpose: for the symmetric ones the output itself; or NULL
+  int64_t ld, ld_t;
   const int32_t* skip;
 };
 
-// 8 columns of a row from their sums, into the output's fp16
+// 8 columns of a row from their sums, into the output's fp16; v becomes what its transpose takes
 template <Kind kind>
-__device__ __forceinline__ void finish8(const ProductArgs& a, const float (&v)[8], int64_t m, int n) {
+__device__ __forceinline__ void finish8(const ProductArgs& a, float (&v)[8], int64_t m, int n) {
   const int64_t at = m * a.ld + n;
   half_t o[8];
   if constexpr (kind == Kind::kGram) {
@@ -187,6 +195,15 @@ __device__ __forceinline__ void finish8(const ProductArgs& a, const float (&v)[8
     *reinterpret_cast<tile::u4*>(a.out_lo + at) = *reinterpret_cast<const tile::u4*>(o2);
   }
   *reinterpret_cast<tile::u4*>(a.out + at) = *reinterpret_cast<const tile::u4*>(o);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = (float)o[j];
+}
+// 8 rows of a column of what finish8 left, as a piece of the transpose
+__device__ __forceinline__ void put_turned(const ProductArgs& a, const float* p, int stride, int64_t n, int64_t m) {
+  half_t o[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) o[j] = (half_t)p[j * stride];
+  *reinterpret_cast<tile::u4*>(a.out_t + n * a.ld_t + m) = *reinterpret_cast<const tile::u4*>(o);
 }
 
 // The tile of a symmetric output: those on and below the diagonal, row by row.
@@ -214,6 +231,7 @@ __device__ __forceinline__ typename C::Where where(const ProductArgs& a, uint32_
 
 template <typename C, Kind kind>
 __global__ __launch_bounds__(C::kThreads, 2) void muon_product_kernel(ProductArgs a) {
+  static_assert(C::BM == C::BN, "a symmetric output's tiles mirror each other");
   extern __shared__ __align__(16) uint8_t t_smem[];
   if (a.skip && *a.skip) return;
   tile::share(a.work, [&](uint32_t t, int s0, int s1, int slot) {
@@ -221,41 +239,40 @@ __global__ __launch_bounds__(C::kThreads, 2) void muon_product_kernel(ProductArg
     typename C::Acc acc;
     C::run(a.src, at, a.N, s0, s1, t_smem, acc);
     float* const part = slot < 0 ? nullptr : a.part + (int64_t)slot * C::BM * C::BN;
-    const bool mirror = kind != Kind::kNext && at.m0 != at.n0;
-    C::rows(acc, t_smem, [&](int r, int c, const float* p) {
+    const bool turn = !part && a.out_t && (kind == Kind::kNext || at.m0 != at.n0);
+    C::rows(acc, t_smem, [&](int r, int c, float* p) {
       float v[8];
       tile::eight(p, v);
       if (part) {
         store8<float>(part + r * C::BN, c, C::BN, v);
       } else if (r < at.mrows && c < at.ncols) {
         finish8<kind>(a, v, at.m0 + r, at.n0 + c);
+        if (turn) {
+          *reinterpret_cast<f4*>(p) = (f4){v[0], v[1], v[2], v[3]};
+          *reinterpret_cast<f4*>(p + 4) = (f4){v[4], v[5], v[6], v[7]};
+        }
       }
     }, [&](int r0, int c0, const float* p) {
-      if (!mirror || part || r0 >= at.mrows) return;
-      // 16 rows of the tile are 16 columns of its mirror image
-      for (int c = (threadIdx.x & 63); c < C::kWaveN; c += 64) {
-        if (c0 + c >= at.ncols) continue;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float v[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = p[(8 * h + j) * C::kPad + c];
-          finish8<kind>(a, v, at.n0 + c0 + c, (int)at.m0 + r0 + 8 * h);
-        }
+      if (!turn || r0 >= at.mrows) return;
+      for (int i = threadIdx.x & 63; i < 2 * C::kWaveN; i += 64) {
+        const int c = i % C::kWaveN, h = i / C::kWaveN * 8;
+        if (c0 + c < at.ncols) put_turned(a, p + h * C::kPad + c, C::kPad, at.n0 + c0 + c, at.m0 + r0 + h);
       }
     });
     __syncthreads();
   });
 }
 
-// Split tiles: a block takes 16 rows by 128 columns, 8 columns a thread, and adds the parts in the order of the sum
+// Split tiles: a block takes 16 rows by kCols columns, 8 columns a thread, and adds the parts in the order of the sum
+template <typename C> constexpr int join_cols() { return C::BN < 128 ? C::BN : 128; }
 template <typename C, Kind kind>
-__global__ __launch_bounds__(256) void muon_join_kernel(ProductArgs a) {
-  __shared__ float turn[16][132];
+__global__ __launch_bounds__(2 * join_cols<C>()) void muon_join_kernel(ProductArgs a) {
+  constexpr int kCols = join_cols<C>(), kPad = kCols + 4;
+  __shared__ __align__(16) float turn[16 * kPad];
   if (a.skip && *a.skip) return;
   const typename C::Where at = where<C, kind>(a, a.work.full + blockIdx.x);
-  const int r0 = (int)blockIdx.y / (C::BN / 128) * 16, c0 = (int)blockIdx.y % (C::BN / 128) * 128;
-  const int r = threadIdx.x >> 4, c = (threadIdx.x & 15) * 8;
+  const int r0 = (int)blockIdx.y / (C::BN / kCols) * 16, c0 = (int)blockIdx.y % (C::BN / kCols) * kCols;
+  const int r = threadIdx.x / (kCols / 8), c = threadIdx.x % (kCols / 8) * 8;
   float v[8] = {};
   tile::parts(a.work, blockIdx.x, [&](uint32_t slot) {
     float p[8];
@@ -264,15 +281,12 @@ __global__ __launch_bounds__(256) void muon_join_kernel(ProductArgs a) {
     for (int j = 0; j < 8; ++j) v[j] += p[j];
   });
   if (r0 + r < at.mrows && c0 + c < at.ncols) finish8<kind>(a, v, at.m0 + r0 + r, at.n0 + c0 + c);
-  if (kind == Kind::kNext || at.m0 == at.n0 || r0 >= at.mrows) return;
+  if (!a.out_t || (kind != Kind::kNext && at.m0 == at.n0) || r0 >= at.mrows) return;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) turn[r][c + j] = v[j];
+  for (int j = 0; j < 8; ++j) turn[r * kPad + c + j] = v[j];
   __syncthreads();
-  const int mc = threadIdx.x >> 1, h = (threadIdx.x & 1) * 8;
-  if (c0 + mc >= at.ncols) return;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = turn[h + j][mc];
-  finish8<kind>(a, v, at.n0 + c0 + mc, (int)at.m0 + r0 + h);
+  const int tc = threadIdx.x % kCols, h = threadIdx.x / kCols * 8;
+  if (c0 + tc < at.ncols) put_turned(a, turn + h * kPad + tc, kPad, at.n0 + c0 + tc, at.m0 + r0 + h);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -327,24 +341,39 @@ __global__ __launch_bounds__(256) void muon_apply_kernel(ApplyArgs a) {
 // ---------------------------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------------------------
-typedef tile::Tile<half_t, 4, 2, 4, 8, 2, false, 0, 1, true> CSym;   // 256 x 256, rows along the sum
-typedef tile::Tile<half_t, 4, 2, 4, 8, 2, true, 0, 1, true> CNext;   // 256 x 256, [R][N]
+// Tiles of 64, 128 and 256 square, chosen for each product by estimate: us of a step of such tiles on every unit.
+template <int kSize> struct Square;
+template <> struct Square<64> { typedef tile::Tile<half_t, 2, 2, 2, 2, 4, false, 0, 1, true> C; };
+template <> struct Square<128> { typedef tile::Tile<half_t, 2, 2, 4, 4, 3, false, 0, 1, true> C; };
+template <> struct Square<256> { typedef tile::Tile<half_t, 4, 2, 4, 8, 2, false, 0, 1, true> C; };
+struct Choice {
+  int size;
+  tile::Lay lay;
+};
+Choice choose(int64_t M, int64_t N, int64_t steps, bool symmetric) {
+  constexpr struct { int size; double step; } kinds[3] = {{64, 0.30}, {128, 0.60}, {256, 1.6}};
+  Choice best{};
+  for (const auto& k : kinds) {
+    const int64_t tm = (M + k.size - 1) / k.size, tn = (N + k.size - 1) / k.size;
+    const tile::Lay l = tile::lay(symmetric ? 1 : tm, symmetric ? tm * (tm + 1) / 2 : tn, steps, k.step, (int64_t)k.size * k.size * 4);
+    if (best.size == 0 || l.est < best.lay.est) best = Choice{k.size, l};
+  }
+  return best;
+}
 
 // Where everything lies in the workspace; n and m are padded to whole steps with zeros.
 struct Buffers {
   int64_t n, m;
-  size_t part, x[4], a, b, sums, bytes;
-  tile::Lay gram, poly, next;
+  size_t part, x[6], a, b, sums, bytes;
+  Choice gram, poly, next;
 };
 Buffers buffers(int64_t N, int64_t K) {
   Buffers b{};
   b.n = ((N < K ? N : K) + 63) / 64 * 64;
   b.m = ((N < K ? K : N) + 63) / 64 * 64;
-  const int64_t tn = (b.n + 255) / 256, tm = (b.m + 255) / 256, tri = tn * (tn + 1) / 2;
-  constexpr double kStep = 1.3;  // us of a step of 256 x 256 tiles on every unit
-  b.gram = tile::lay(1, tri, b.m / 64, kStep, 256 * 1024);
-  b.poly = tile::lay(1, tri, b.n / 64, kStep, 256 * 1024);
-  b.next = tile::lay(tn, tm, b.n / 64, kStep, 256 * 1024);
+  b.gram = choose(b.n, b.n, b.m / 64, true);
+  b.poly = choose(b.n, b.n, b.n / 64, true);
+  b.next = choose(b.n, b.m, b.n / 64, false);
   const auto take = [&](size_t bytes) {
     const size_t at = b.bytes;
     b.bytes += (bytes + 255) / 256 * 256;
@@ -354,22 +383,28 @@ Buffers buffers(int64_t N, int64_t K) {
   for (size_t& x : b.x) x = take((size_t)b.n * (size_t)b.m * 2);
   b.a = take((size_t)b.n * (size_t)b.n * 2);
   b.b = take((size_t)b.n * (size_t)b.n * 2);
-  size_t most = b.gram.part_bytes > b.poly.part_bytes ? b.gram.part_bytes : b.poly.part_bytes;
-  most = b.next.part_bytes > most ? b.next.part_bytes : most;
+  size_t most = 0;
+  for (const Choice* c : {&b.gram, &b.poly, &b.next}) most = c->lay.part_bytes > most ? c->lay.part_bytes : most;
   b.sums = take(most);
   return b;
 }
 
-template <typename C, Kind kind>
-hipError_t launch_product(const ProductArgs& a, hipStream_t s) {
+template <int kSize, Kind kind>
+hipError_t launch_size(const ProductArgs& a, hipStream_t s) {
+  typedef typename Square<kSize>::C C;
   static const hipError_t attr = hipFuncSetAttribute((const void*)muon_product_kernel<C, kind>,
                                                      hipFuncAttributeMaxDynamicSharedMemorySize, C::kLds);
   if (attr != hipSuccess) return attr;
   muon_product_kernel<C, kind><<<a.work.grid, C::kThreads, C::kLds, s>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.work.full == a.work.tiles) return e;
-  muon_join_kernel<C, kind><<<dim3(a.work.tiles - a.work.full, C::BM / 16 * (C::BN / 128)), 256, 0, s>>>(a);
+  constexpr int cols = join_cols<C>();
+  muon_join_kernel<C, kind><<<dim3(a.work.tiles - a.work.full, C::BM / 16 * (C::BN / cols)), 2 * cols, 0, s>>>(a);
   return hipGetLastError();
+}
+template <Kind kind>
+hipError_t launch_product(const Choice& c, const ProductArgs& a, hipStream_t s) {
+  return c.size == 64 ? launch_size<64, kind>(a, s) : c.size == 128 ? launch_size<128, kind>(a, s) : launch_size<256, kind>(a, s);
 }
 
 template <typename TG>
@@ -392,29 +427,30 @@ hipError_t launch_muon_step(float* W, int64_t ldw, const void* G, rb_dtype g_dty
   const Buffers b = buffers(N, K);
   char* const base = static_cast<char*>(ws);
   const auto half_at = [&](size_t at) { return reinterpret_cast<half_t*>(base + at); };
-  half_t *hi = half_at(b.x[0]), *lo = half_at(b.x[1]), *hi2 = half_at(b.x[2]), *lo2 = half_at(b.x[3]);
+  struct Held { half_t *hi, *lo, *t; } x{half_at(b.x[0]), half_at(b.x[1]), half_at(b.x[2])},
+      y{half_at(b.x[3]), half_at(b.x[4]), half_at(b.x[5])};
   half_t *const A = half_at(b.a), *const B = half_at(b.b);
   float* const part = reinterpret_cast<float*>(base + b.sums);
   const MomentArgs m{G, mom, ldg, ldm, N, K, (float)momentum, (float)eps, nesterov, grad_scale, skip,
-                     reinterpret_cast<double*>(base + b.part), hi, lo, b.m, b.n, N > K};
+                     reinterpret_cast<double*>(base + b.part), x.hi, x.lo, x.t, b.m, b.n, N > K};
   hipError_t e = g_dtype == RB_F32 ? launch_start<float>(m, s)
                  : g_dtype == RB_F16 ? launch_start<_Float16>(m, s) : launch_start<__bf16>(m, s);
   if (e != hipSuccess) return e;
   const int n = (int)b.n, cols = (int)b.m;
   for (int i = 0; i < steps; ++i) {
-    const ProductArgs gram{{{hi, hi, nullptr, b.m, b.m, 0, cols, cols / 64}}, n, n, b.gram.work, part, nullptr, nullptr,
-                           nullptr, A, nullptr, b.n, skip};
-    const ProductArgs poly{{{A, A, nullptr, b.n, b.n, 0, n, n / 64}}, n, n, b.poly.work, part, A, nullptr, nullptr, B,
-                           nullptr, b.n, skip};
-    const ProductArgs next{{{B, hi, nullptr, b.n, b.m, 0, n, n / 64}}, n, cols, b.next.work, part, nullptr, hi, lo, hi2,
-                           lo2, b.m, skip};
-    if ((e = launch_product<CSym, Kind::kGram>(gram, s)) != hipSuccess) return e;
-    if ((e = launch_product<CSym, Kind::kPoly>(poly, s)) != hipSuccess) return e;
-    if ((e = launch_product<CNext, Kind::kNext>(next, s)) != hipSuccess) return e;
-    half_t* t = hi; hi = hi2, hi2 = t;
-    t = lo, lo = lo2, lo2 = t;
+    const ProductArgs gram{{{x.hi, x.hi, nullptr, b.m, b.m, 0, cols, cols / 64}}, n, n, b.gram.lay.work, part, nullptr, nullptr,
+                           nullptr, A, nullptr, A, b.n, b.n, skip};
+    const ProductArgs poly{{{A, A, nullptr, b.n, b.n, 0, n, n / 64}}, n, n, b.poly.lay.work, part, A, nullptr, nullptr, B,
+                           nullptr, B, b.n, b.n, skip};
+    const ProductArgs next{{{B, x.t, nullptr, b.n, b.n, 0, n, n / 64}}, n, cols, b.next.lay.work, part, nullptr, x.hi, x.lo,
+                           y.hi, y.lo, i + 1 < steps ? y.t : nullptr, b.m, b.n, skip};
+    if ((e = launch_product<Kind::kGram>(b.gram, gram, s)) != hipSuccess) return e;
+    if ((e = launch_product<Kind::kPoly>(b.poly, poly, s)) != hipSuccess) return e;
+    if ((e = launch_product<Kind::kNext>(b.next, next, s)) != hipSuccess) return e;
+    const Held t = x;
+    x = y, y = t;
   }
-  const ApplyArgs p{hi, lo, b.m, W, O, ldw, ldo, N, K, (float)(1.0 - lr * weight_decay), (float)(lr * scale), N > K, skip};
+  const ApplyArgs p{x.hi, x.lo, b.m, W, O, ldw, ldo, N, K, (float)(1.0 - lr * weight_decay), (float)(lr * scale), N > K, skip};
   const dim3 grid((uint32_t)((K + 63) / 64), (uint32_t)((N + 63) / 64));
   if (o_dtype == RB_F16)
     muon_apply_kernel<_Float16><<<grid, 256, 0, s>>>(p);

@@ -29,10 +29,33 @@ __device__ __forceinline__ f4 mfma(__bf16, u4 a, u4 b, f4 c) {
 }
 
 // 16 bytes per lane from the buffer to LDS (lane l's at base + 16 l). The whole offset is the lane's, so that the
-// range check sees all of it.
-__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t r, uint8_t* base, uint32_t off) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)base, 16, off, 0, 0, 0);
-}
+// range check sees all of it. Two forms of the same instruction: the compiler takes the transposing reads of LDS for
+// dependent on every load to LDS in flight and has them wait for all of these (2048 x 4096 over 2 x 11008 in 411 us
+// with the builtin), so where those reads are used the load is written out. It has no register outputs; its LDS writes
+// are ordered by the kernel's own waits and barriers, as with the builtin. m0 has no other user in those kernels. The waits in front: one state from the
+// write of m0, five from a descriptor word that comes from a vector register.
+template <bool kWritten> struct Rows {  // a buffer resource over [base, base + bytes)
+  __amdgpu_buffer_rsrc_t r;
+  Rows() = default;
+  __device__ __forceinline__ Rows(const void* base, uint32_t bytes) : r(buffer_rsrc(base, bytes)) {}
+  __device__ __forceinline__ void load(uint8_t* to, uint32_t off) const {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)to, 16, off, 0, 0, 0);
+  }
+};
+template <> struct Rows<true> {
+  u4 r;
+  Rows() = default;
+  __device__ __forceinline__ Rows(const void* base, uint32_t bytes) {
+    const uint64_t p = reinterpret_cast<uint64_t>(base);
+    r = (u4){(uint32_t)p, (uint32_t)(p >> 32) & 0xffffu, bytes, 0x00020000u};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = __builtin_amdgcn_readfirstlane(r[i]);
+  }
+  __device__ __forceinline__ void load(uint8_t* to, uint32_t off) const {
+    const uint32_t m0 = __builtin_amdgcn_readfirstlane((uint32_t)(size_t)(lds_void*)to);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(m0), "v"(off), "s"(r) : "memory");
+  }
+};
 
 constexpr int kTK = 64;            // terms of the sum per step
 constexpr int kRowB = kTK * 2;     // bytes of a staged row along the sum
@@ -94,7 +117,11 @@ struct Tile {
   static constexpr int kRowNN = BN * 2;                                // bytes of a staged row of [R][N]
   static constexpr int kPad = 16 * kTN + 4;                            // floats of a row in the epilogue's LDS area
   static constexpr int kTurn = kWaves * 16 * kPad * 4;
-  static constexpr int kLds = kS * kStage > kTurn ? kS * kStage : kTurn;
+  // Two stages of 256 x 256 leave room for half a stage: then an operand's part of a stage is a slot of its own, five of
+  // them, which hold A and B of steps 0, 1, 2, ... in turn.
+  static constexpr bool kFive = kAl && kS == 2 && kStageA * 2 == kStage && 5 * kStageA <= 160 * 1024;
+  static constexpr int kSlots = kFive ? 5 * kStageA : kS * kStage;
+  static constexpr int kLds = kSlots > kTurn ? kSlots : kTurn;
   static_assert(BM / 8 % kWaves == 0 && BN / 8 % kWaves == 0, "a load instruction has one operand");
   static_assert(kAl || kS == 2, "through registers a step is written two steps ahead");
   static_assert(!kHalf || (2 * kHalf == 16 * kTN && !kNN), "a wave holds both values of an output");
@@ -139,44 +166,77 @@ struct Tile {
     const auto second = [&](int r) { return kHalf && (r / (kHalf ? kHalf : 1) & 1); };
     const auto out_row = [&](int r) { return kHalf ? r / (2 * kHalf) * kHalf + r % kHalf : r; };
 
-    const auto dma = [&](int s, int stage) {
-      const bool live = s < s1, next = kSrc == 2 && s >= src[0].steps;
-      const Source<T>& q = src[kSrc == 2 && next ? kSrc - 1 : 0];
+    // the loads of a step's A or B to LDS at `base`: what they have in common, and the i-th of a wave
+    struct Loads {
+      Rows<kNN> r, r2;
+      uint32_t v, v2, ld, ld2;
+      bool ok;
+      uint8_t* base;
+    };
+    const auto part_of = [&](int s, bool& next) -> const Source<T>& {
+      next = kSrc == 2 && s >= src[0].steps;
+      return src[kSrc == 2 && next ? kSrc - 1 : 0];
+    };
+    const auto loads_a = [&](int s, uint8_t* base) {
+      bool next;
+      const Source<T>& q = part_of(s, next);
       const int k0 = (next ? s - src[0].steps : s) * kTK;
-      const bool ok = live && k0 + 8 * xc < q.R;
-      uint8_t* const base = smem + stage * kStage;
-      const uint32_t la = (uint32_t)q.lda * 2, lb = (uint32_t)q.ldb * 2;
-      const __amdgpu_buffer_rsrc_t ra =
-          buffer_rsrc(q.A + at.m0 * q.lda, (uint32_t)((at.mrows - 1) * (int)la + q.R * 2));
-      const uint32_t va = (uint32_t)(lane >> 3) * la + 16u * xc + (uint32_t)k0 * 2;
-#pragma unroll
-      for (int i = 0; i < kPerA; ++i)
-        load_to_lds(ra, base + (i * kWaves + w) * 1024, ok ? va + (uint32_t)group_row(i) * la : kOob);
+      Loads l;
+      l.ok = s < s1 && k0 + 8 * xc < q.R;
+      l.base = base;
+      l.ld = (uint32_t)q.lda * 2;
+      l.r = Rows<kNN>(q.A + at.m0 * q.lda, (uint32_t)((at.mrows - 1) * (int)l.ld + q.R * 2));
+      l.v = (uint32_t)(lane >> 3) * l.ld + 16u * xc + (uint32_t)k0 * 2;
+      return l;
+    };
+    const auto loads_b = [&](int s, uint8_t* base) {
+      bool next;
+      const Source<T>& q = part_of(s, next);
+      const int k0 = (next ? s - src[0].steps : s) * kTK;
+      Loads l;
+      l.ok = s < s1 && k0 + 8 * xc < q.R;
+      l.base = base;
+      l.ld = (uint32_t)q.ldb * 2;
       if constexpr (kNN) {
-        const int rows = q.R - k0;
-        const __amdgpu_buffer_rsrc_t rb = buffer_rsrc(
-            q.B + (live ? (int64_t)k0 * q.ldb : 0),
-            live && rows > 0 ? (uint32_t)(((rows < kTK ? rows : kTK) - 1) * (int)lb + N * 2) : 0u);
-        const uint32_t vb = (uint32_t)kr * lb + 16u * xn + (uint32_t)at.n0 * 2;
-#pragma unroll
-        for (int i = 0; i < kPerB; ++i)
-          load_to_lds(rb, base + kStageA + (i * kWaves + w) * 1024, vb + (uint32_t)(2 * (i * kWaves + w)) * lb);
+        const int rows = s < s1 ? q.R - k0 : 0;
+        l.r = Rows<kNN>(q.B + (rows > 0 ? (int64_t)k0 * q.ldb : 0),
+                          rows > 0 ? (uint32_t)(((rows < kTK ? rows : kTK) - 1) * (int)l.ld + N * 2) : 0u);
+        l.v = (uint32_t)kr * l.ld + 16u * xn + (uint32_t)at.n0 * 2;
       } else {
-        const __amdgpu_buffer_rsrc_t rb =
-            buffer_rsrc(q.B + (int64_t)at.n0 * q.ldb, (uint32_t)((at.ncols - 1) * (int)lb + q.R * 2));
-        const uint32_t lb2 = kHalf ? (uint32_t)q.ldb2 * 2 : lb;
-        const __amdgpu_buffer_rsrc_t rb2 =
-            kHalf ? buffer_rsrc(q.B2 + (int64_t)at.n0 * q.ldb2, (uint32_t)((at.ncols - 1) * (int)lb2 + q.R * 2)) : rb;
-        const uint32_t vb = (uint32_t)(lane >> 3) * lb + 16u * xc + (uint32_t)k0 * 2;
-        const uint32_t vb2 = (uint32_t)(lane >> 3) * lb2 + 16u * xc + (uint32_t)k0 * 2;
-#pragma unroll
-        for (int i = 0; i < kPerB; ++i) {
-          const int r = group_row(i);
-          const bool two = second(r);
-          load_to_lds(two ? rb2 : rb, base + kStageA + (i * kWaves + w) * 1024,
-                      ok ? (two ? vb2 + (uint32_t)out_row(r) * lb2 : vb + (uint32_t)out_row(r) * lb) : kOob);
+        l.r = Rows<kNN>(q.B + (int64_t)at.n0 * q.ldb, (uint32_t)((at.ncols - 1) * (int)l.ld + q.R * 2));
+        l.v = (uint32_t)(lane >> 3) * l.ld + 16u * xc + (uint32_t)k0 * 2;
+        if constexpr (kHalf) {
+          l.ld2 = (uint32_t)q.ldb2 * 2;
+          l.r2 = Rows<kNN>(q.B2 + (int64_t)at.n0 * q.ldb2, (uint32_t)((at.ncols - 1) * (int)l.ld2 + q.R * 2));
+          l.v2 = (uint32_t)(lane >> 3) * l.ld2 + 16u * xc + (uint32_t)k0 * 2;
         }
       }
+      return l;
+    };
+    const auto load_a = [&](const Loads& l, int i) {
+      l.r.load(l.base + (i * kWaves + w) * 1024, l.ok ? l.v + (uint32_t)group_row(i) * l.ld : kOob);
+    };
+    const auto load_b = [&](const Loads& l, int i) {
+      uint8_t* const to = l.base + (i * kWaves + w) * 1024;
+      if constexpr (kNN) {
+        l.r.load(to, l.v + (uint32_t)(2 * (i * kWaves + w)) * l.ld);
+      } else {
+        const int r = group_row(i);
+        if (second(r))
+          l.r2.load(to, l.ok ? l.v2 + (uint32_t)out_row(r) * l.ld2 : kOob);
+        else
+          l.r.load(to, l.ok ? l.v + (uint32_t)out_row(r) * l.ld : kOob);
+      }
+    };
+    const auto all_a = [&](int s, int at) {
+      const Loads l = loads_a(s, smem + at);
+#pragma unroll
+      for (int i = 0; i < kPerA; ++i) load_a(l, i);
+    };
+    const auto all_b = [&](int s, int at) {
+      const Loads l = loads_b(s, smem + at);
+#pragma unroll
+      for (int i = 0; i < kPerB; ++i) load_b(l, i);
     };
 
     u4 hold[kAl ? 1 : kPer];
@@ -231,39 +291,38 @@ struct Tile {
     const uint32_t lds0 = (uint32_t)(size_t)(__attribute__((address_space(3))) uint8_t*)smem;
     const uint32_t f0 = lr * kRowB + 16u * ((uint32_t)lj ^ (lr & 7u)), f1 = lr * kRowB + 16u * ((4u + lj) ^ (lr & 7u));
     const uint32_t aa = lds0 + wm * kTM * 16 * kRowB;
-    const uint32_t ab = lds0 + kStageA + (kNN ? (8 * lj + (lr >> 2)) * kRowNN + 8 * (lr & 3) : wn * kTN * 16 * kRowB);
+    const uint32_t ab = lds0 + (kNN ? (8 * lj + (lr >> 2)) * kRowNN + 8 * (lr & 3) : wn * kTN * 16 * kRowB);
     const uint32_t turn_nn = (lr >> 2) | (lj & 1) << 2;
     u4 xf[2][kTM], wf[2][kTN];
-    const auto read = [&](int kh, int stage) {  // the fragments of half kh of a stage
-#pragma unroll
-      for (int j = 0; j < kTN; ++j) {
-        if constexpr (kNN) {
-          const uint32_t p = ab + stage * kStage + kh * 32 * kRowNN + 32 * (((uint32_t)(wn * kTN + j)) ^ turn_nn);
-          const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(size_t)p);
-          const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(size_t)(p + 4 * kRowNN));
-          wf[kh][j] = __builtin_bit_cast(u4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-        } else {
-          wf[kh][j] = *(lds_u4*)(size_t)(ab + stage * kStage + j * 16 * kRowB + (kh ? f1 : f0));
-        }
+    constexpr int kReads = kTM + kTN, kProducts = kTM * kTN;
+    constexpr int kReadSpan = kProducts < 2 * kReads ? kProducts : kProducts / 2;  // products that the reads are spread over
+    const auto read_one = [&](int kh, int in_a, int in_b, int r) {  // the r-th fragment of half kh of the step whose A and B lie there
+      if (r >= kTN) {
+        xf[kh][r - kTN] = *(lds_u4*)(size_t)(aa + in_a + (r - kTN) * 16 * kRowB + (kh ? f1 : f0));
+      } else if constexpr (kNN) {
+        const uint32_t p = ab + in_b + kh * 32 * kRowNN + 32 * (((uint32_t)(wn * kTN + r)) ^ turn_nn);
+        const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(size_t)p);
+        const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(size_t)(p + 4 * kRowNN));
+        wf[kh][r] = __builtin_bit_cast(u4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+      } else {
+        wf[kh][r] = *(lds_u4*)(size_t)(ab + in_b + r * 16 * kRowB + (kh ? f1 : f0));
       }
-#pragma unroll
-      for (int i = 0; i < kTM; ++i)
-        xf[kh][i] = *(lds_u4*)(size_t)(aa + stage * kStage + i * 16 * kRowB + (kh ? f1 : f0));
     };
-    const auto multiply = [&](int kh) {
+    // The products of half kh with the reads of the other half (of the step that lies at in_a, in_b) and the wave's loads
+    // among them, in this order: the compiler takes a load to LDS and a read of LDS for dependent and would put all of one before the other,
+    // and the products behind both. Issued together, the loads of 8 waves hold each wave up until the memory pipeline
+    // has taken them, 16 cycles each.
+    const auto phase = [&](int kh, int in_a, int in_b, int loads, auto load) {
 #pragma unroll
-      for (int i = 0; i < kTM; ++i)
+      for (int p = 0; p < kProducts; ++p) {
+        const int i = p / kTN, j = p % kTN;
+        acc[i][j] = mfma(T(0), wf[kh][j], xf[kh][i], acc[i][j]);
 #pragma unroll
-        for (int j = 0; j < kTN; ++j) acc[i][j] = mfma(T(0), wf[kh][j], xf[kh][i], acc[i][j]);
-    };
-    constexpr int kReads = kTM + kTN * (kNN ? 2 : 1);
-    const auto spread = [] {  // the reads over the products
+        for (int r = p * kReads / kReadSpan; r < (p + 1) * kReads / kReadSpan && r < kReads; ++r) read_one(kh ^ 1, in_a, in_b, r);
 #pragma unroll
-      for (int r = 0; r < kReads; ++r) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // MFMA
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // LDS read
+        for (int l = p * loads / kProducts; l < (p + 1) * loads / kProducts; ++l) load(l);
+        __builtin_amdgcn_sched_barrier(0);
       }
-      __builtin_amdgcn_sched_barrier(0);
     };
     const auto barrier = [] {  // the raw barrier: __syncthreads would also wait for every load in flight
       asm volatile("" ::: "memory");
@@ -271,9 +330,16 @@ struct Tile {
       asm volatile("" ::: "memory");
     };
 
-    if constexpr (kAl) {
+    // where A and B of a step lie: slots 2 s and 2 s + 1 (mod 5) from s0 on, or the stages of the ring
+    const auto bump = [](int x, int by) { return x + by >= kSlots ? x + by - kSlots : x + by; };
+    constexpr int kStep = kFive ? 2 * kStageA : kStage;
+    int in_a = 0, in_b = kStageA;
+    if constexpr (kFive) {
+      all_a(s0, 0), all_b(s0, kStageA), all_a(s0 + 1, 2 * kStageA), all_b(s0 + 1, 3 * kStageA), all_a(s0 + 2, 4 * kStageA);
+      __builtin_amdgcn_s_waitcnt(wait_vmcnt(2 * kPerA + kPerB));
+    } else if constexpr (kAl) {
 #pragma unroll
-      for (int s = 0; s < kS; ++s) dma(s0 + s, s);
+      for (int s = 0; s < kS; ++s) all_a(s0 + s, s * kStage), all_b(s0 + s, s * kStage + kStageA);
       __builtin_amdgcn_s_waitcnt(wait_vmcnt((kS - 1) * kPer));
     } else {
       u4 ahead[kAl ? 1 : kPer];
@@ -285,27 +351,31 @@ struct Tile {
       __builtin_amdgcn_s_waitcnt(kWaitLds);
     }
     barrier();
-    read(0, 0);
+#pragma unroll
+    for (int r = 0; r < kReads; ++r) read_one(0, in_a, in_b, r);
     __builtin_amdgcn_sched_barrier(0);
-    int st = 0;
     for (int s = s0; s < s1; ++s) {
-      read(1, st);
-      multiply(0);
-      spread();
-      const int next = st + 1 == kS ? 0 : st + 1;
-      __builtin_amdgcn_s_waitcnt(kAl ? wait_vmcnt((kS - 2) * kPer) & kWaitLds : kWaitLds);
+      phase(0, in_a, in_b, 0, [](int) {});
+      const int free_a = in_a, free_b = in_b;
+      in_a = bump(in_a, kStep), in_b = bump(in_b, kStep);
+      __builtin_amdgcn_s_waitcnt(kFive ? wait_vmcnt(kPerA) & kWaitLds : kAl ? wait_vmcnt((kS - 2) * kPer) & kWaitLds : kWaitLds);
       barrier();
-      if constexpr (kAl) {
-        dma(s + kS, st);
+      if constexpr (kFive) {
+        // five slots: B of step s + 2 goes where A of step s was, A of step s + 3 where its B was, so that half of what
+        // the next wait is for has been on its way for two steps
+        const Loads lb = loads_b(s + 2, smem + free_a), la = loads_a(s + 3, smem + free_b);
+        __builtin_amdgcn_sched_barrier(0);
+        phase(1, in_a, in_b, kPer, [&](int i) { i < kPerB ? load_b(lb, i) : load_a(la, i - kPerB); });
+      } else if constexpr (kAl) {
+        const Loads la = loads_a(s + kS, smem + free_a), lb = loads_b(s + kS, smem + free_b);
+        __builtin_amdgcn_sched_barrier(0);
+        phase(1, in_a, in_b, kPer, [&](int i) { i < kPerA ? load_a(la, i) : load_b(lb, i - kPerA); });
       } else {
-        put(st, hold);
+        put(free_a / kStage, hold);
         fetch(s + 3, hold);
+        __builtin_amdgcn_sched_barrier(0);
+        phase(1, in_a, in_b, 0, [](int) {});
       }
-      __builtin_amdgcn_sched_barrier(0);
-      read(0, next);
-      multiply(1);
-      spread();
-      st = next;
     }
     // loads past the last step (out of range, zeros) end before LDS is used again
     __builtin_amdgcn_s_waitcnt(wait_vmcnt(0));
@@ -314,9 +384,10 @@ struct Tile {
 
   // The accumulators by rows: 16 rows at a time through the wave's own LDS area, so that consecutive lanes hold
   // consecutive columns and whole lines are read and written. f(row, column, p): the tile's row, the output column
-  // counted from n0 (a multiple of 8), and p[0 .. 7] its fp32 sums (p[kHalf .. kHalf + 7] the second matrix's).
-  // D of the product: lane l holds columns 4 (l / 16) .. + 3 of row l % 16. `turned`(row, p) is called once for 16 rows
-  // and sees all of them (row stride kPad). LDS must be free; the block synchronises before its next use.
+  // counted from n0 (a multiple of 8), and p[0 .. 7] its fp32 sums (p[kHalf .. kHalf + 7] the second matrix's), which it
+  // may change. D of the product: lane l holds columns 4 (l / 16) .. + 3 of row l % 16. turned(row, column, p) is called
+  // once for 16 rows and all of the wave's columns and sees what f left (row stride kPad). LDS must be free; the block
+  // synchronises before its next use.
   template <typename F, typename G>
   __device__ static __forceinline__ void rows(const f4 (&acc)[kTM][kTN], uint8_t* smem, F f, G turned) {
     const int lane = threadIdx.x & 63;
@@ -339,6 +410,7 @@ struct Tile {
         const int r = kAtOnce * s + lane / kLanes, c = 8 * (lane % kLanes);
         f((wm * kTM + i) * 16 + r, wn * kWaveN + c, turn + r * kPad + c);
       }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       turned((wm * kTM + i) * 16, wn * kWaveN, turn);
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
