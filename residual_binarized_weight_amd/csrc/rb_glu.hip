@@ -323,13 +323,16 @@ struct Choice {
   int bm;
   tile::Lay lay;
 };
-// the tile height by estimate: us of a step of a tile of each height when every unit works
-Choice choose(int64_t M, int64_t out_n, int per_tile, int64_t steps, bool aligned) {
-  struct { int bm; double step; } const kinds[2][3] = {{{64, 0.8}, {128, 1.3}, {0, 0}}, {{64, 0.5}, {128, 0.8}, {256, 1.3}}};
+// The tile height by estimate: us of a step of a tile of each height when every unit works, measured at 2048 x 16384
+// outputs (staged) of 64 steps; the transposing reads of dX's products take a tenth longer. Rows that are not aligned: the
+// same from odd rows. 128 rows take 0.97 where 256 take 1.69: what a byte brought to LDS serves.
+Choice choose(int64_t M, int64_t out_n, int per_tile, int64_t steps, bool aligned, bool across) {
+  struct { int bm; double step; } const kinds[2][3] = {{{64, 0.95}, {128, 1.5}, {0, 0}}, {{64, 0.64}, {128, 0.97}, {256, 1.69}}};
   Choice best{};
   for (const auto& k : kinds[aligned]) {
     if (k.bm == 0) continue;
-    const tile::Lay l = tile::lay((M + k.bm - 1) / k.bm, (out_n + per_tile - 1) / per_tile, steps, k.step, (int64_t)k.bm * 1024);
+    const tile::Lay l = tile::lay((M + k.bm - 1) / k.bm, (out_n + per_tile - 1) / per_tile, steps, k.step * (across ? 1.13 : 1.0),
+                                  (int64_t)k.bm * 1024);
     if (best.bm == 0 || l.est < best.lay.est) best = Choice{k.bm, l};
   }
   return best;
@@ -373,7 +376,7 @@ hipError_t launch_glu_product(GluArgs<T> a, void* ws, hipStream_t s) {
   if (rows_form(a.M, q.R)) return launch_glu_rows<T, TH>(a, s);
   const bool al = tile::rows16(q.A, q.lda) && tile::rows16(q.B, q.ldb) && tile::rows16(q.B2, q.ldb2) && q.R % 8 == 0 &&
                   small_ld(q.lda) && small_ld(q.ldb) && small_ld(q.ldb2);
-  const Choice c = choose(a.M, a.N, 128, q.steps, al);
+  const Choice c = choose(a.M, a.N, 128, q.steps, al, false);
   a.work = c.lay.work;
   a.part = static_cast<float*>(ws);
   if (c.bm == 256) return launch_glu_tile<T, TH, 256, true>(a, s);
@@ -405,7 +408,7 @@ hipError_t launch_dx_product(DxArgs<T> a, void* ws, hipStream_t s) {
   bool al = a.src[0].R % 8 == 0 && a.N % 8 == 0;
   for (const Source<T>& q : a.src)
     al = al && tile::rows16(q.A, q.lda) && tile::rows16(q.B, q.ldb) && small_ld(q.lda) && small_ld(q.ldb);
-  const Choice c = choose(a.M, a.N, 256, 2 * a.src[0].steps, al);
+  const Choice c = choose(a.M, a.N, 256, 2 * a.src[0].steps, al, true);
   a.work = c.lay.work;
   a.part = static_cast<float*>(ws);
   if (c.bm == 256) return launch_dx_tile<T, TX, 256, true>(a, s);
@@ -435,7 +438,8 @@ int grad_strip(int64_t M, int64_t N) {
 
 size_t glu_workspace_bytes(int64_t N, int64_t K, int64_t M) {
   if (rows_form(M, K)) return 0;
-  const size_t a = choose(M, N, 128, steps_of(K), false).lay.part_bytes, b = choose(M, N, 128, steps_of(K), true).lay.part_bytes;
+  const size_t a = choose(M, N, 128, steps_of(K), false, false).lay.part_bytes;
+  const size_t b = choose(M, N, 128, steps_of(K), true, false).lay.part_bytes;
   return a > b ? a : b;
 }
 
@@ -480,8 +484,8 @@ hipError_t launch_glu_backward(const void* dH, rb_dtype dh_dtype, int64_t M, int
 }
 
 size_t glu_dx_workspace_bytes(int64_t N, int64_t K, int64_t M) {
-  const size_t a = choose(M, K, 256, 2 * steps_of(N), false).lay.part_bytes;
-  const size_t b = choose(M, K, 256, 2 * steps_of(N), true).lay.part_bytes;
+  const size_t a = choose(M, K, 256, 2 * steps_of(N), false, true).lay.part_bytes;
+  const size_t b = choose(M, K, 256, 2 * steps_of(N), true, true).lay.part_bytes;
   return a > b ? a : b;
 }
 

@@ -351,7 +351,7 @@ struct Choice {
   tile::Lay lay;
 };
 Choice choose(int64_t M, int64_t N, int64_t steps, bool symmetric) {
-  constexpr struct { int size; double step; } kinds[3] = {{64, 0.30}, {128, 0.60}, {256, 1.6}};
+  constexpr struct { int size; double step; } kinds[3] = {{64, 0.30}, {128, 0.60}, {256, 1.69}};
   Choice best{};
   for (const auto& k : kinds) {
     const int64_t tm = (M + k.size - 1) / k.size, tn = (N + k.size - 1) / k.size;

@@ -140,7 +140,10 @@ struct Kernel {
   __device__ __forceinline__ void run(const Args& a, uint8_t* smem) {
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int64_t tile_n = a.first + blockIdx.x, n0 = tile_n * kTileN;
+    // an XCD's blocks take one run of row tiles: four of them share the lines of the scales, 64 rows each
+    const uint32_t run = gridDim.x / tile::kXcds, mine = blockIdx.x % tile::kXcds * run + blockIdx.x / tile::kXcds;
+    const int64_t tile_n = a.first + mine, n0 = tile_n * kTileN;
+    if (n0 >= a.N) return;
     // one instruction for mask and base needs them in registers: as constants they would be two
     uint32_t m = Nib<T>::kMask, b = Nib<T>::kBase;
     asm("" : "+s"(m));
@@ -226,7 +229,8 @@ hipError_t launch_one(Args a, hipStream_t s) {
   if (attr != hipSuccess) return attr;
   return launch_in_parts((a.N + kTileN - 1) / kTileN, [&](int64_t first, uint32_t blocks) {
     a.first = first;
-    q4_product_kernel<T, kGroup, kPair, kM, kWaves><<<blocks, 64 * kWaves, lds, s>>>(a);
+    const uint32_t grid = (blocks + tile::kXcds - 1) / tile::kXcds * tile::kXcds;
+    q4_product_kernel<T, kGroup, kPair, kM, kWaves><<<grid, 64 * kWaves, lds, s>>>(a);
   });
 }
 // A unit holds 16 waves of these: one block of 16, or two of 8 where there are more blocks than units.

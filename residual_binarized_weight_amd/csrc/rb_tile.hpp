@@ -75,12 +75,15 @@ struct Source {
   int R, steps;
 };
 
-// How `tiles` tiles of `steps` steps are laid over a grid of `grid` blocks (a multiple of 8): the first `full` of them
-// whole, in rounds of the grid; the steps of the others in equal runs of `per` to the blocks, whose partial sums
-// a second kernel joins (two partial tiles a block: its run starts in one tile and may end in the next).
+// How `tiles` tiles of `steps` steps are laid over a grid of `grid` blocks (a multiple of 8). The first `full` of them
+// are taken whole, in rounds of the grid; the next `cut` in runs of `chunk` steps, a block each, those of one run next
+// to each other: the blocks of an XCD then pass the same steps at the same time and share what they load in
+// its L2; the steps of the others in equal runs of `per` to all blocks, wherever these begin. Partial sums are joined by
+// a second kernel: of a cut tile one for each run, of the others two partial tiles a block (its run starts in one
+// tile and may end in the next).
 struct Work {
-  uint32_t tiles, tiles_m, full, grid;
-  int steps, per;
+  uint32_t tiles, tiles_m, full, cut, grid;
+  int steps, chunk, per;
 };
 // the m and n of a tile: panels of 8 tiles along m, so that the 32 tiles that an XCD's units work on at a time
 // share 8 blocks of A's rows and 4 of B's in its L2
@@ -104,8 +107,7 @@ __device__ __forceinline__ uint32_t block_of(uint32_t grid) { return blockIdx.x 
 // kSrc: products whose sums run on from one another.
 // kAl: rows of both operands are 16-byte aligned, R (and N where kNN) a multiple of 8: the rows go to LDS directly
 // (buffer loads, which give 0 past a tile's rows and past the sum's end). Otherwise they pass through
-// registers one step ahead, by 16-byte loads at any address; the vector that holds the end of a row is read 8
-// elements before it and shifted.
+// registers one step ahead, by 16-byte loads at any address.
 template <typename T, int kWM, int kWN, int kTM, int kTN, int kS, bool kNN, int kHalf, int kSrc, bool kAl>
 struct Tile {
   static constexpr int kWaves = kWM * kWN, kThreads = 64 * kWaves;
@@ -239,48 +241,69 @@ struct Tile {
       for (int i = 0; i < kPerB; ++i) load_b(l, i);
     };
 
+    // Through registers: a step's loads, all at addresses inside the rows (the vector that holds a row's end, and those
+    // behind it, 8 elements before the end), so that none waits for another; when they are stored to LDS the vector at the
+    // end is shifted and what lies behind the end becomes zero. Rows shorter than a vector are read by elements.
     u4 hold[kAl ? 1 : kPer];
-    // a vector of a row of n elements at c, zeros past its end
-    const auto vec = [](const T* row, int c, int n) {
-      typename Vec8<T>::Raw r = {};
-      if (n >= 8) {
-        load8_long<T>(r, row, c, n);
-        if (c < n && c + 8 > n) shift_down(r, 8 - n % 8);
-      } else {
-        r = load8<T>(row, c, n);
-      }
-      return __builtin_bit_cast(u4, r);
-    };
+    const bool short_n = kNN && N < 8;
     const auto fetch = [&](int s, u4 (&hold)[kAl ? 1 : kPer]) {
       const bool next = kSrc == 2 && s >= src[0].steps;
       const Source<T>& q = src[kSrc == 2 && next ? kSrc - 1 : 0];
       const int k0 = (next ? s - src[0].steps : s) * kTK, c = k0 + 8 * xc;
-      const bool whole = k0 + kTK <= q.R;
+      const int ca = c < q.R - 8 ? c : q.R - 8, col = at.n0 + 8 * xn, cb = col < N - 8 ? col : N - 8;
+      const auto rows = [&](auto load_k, auto load_n) {  // load_k(row): along the sum; load_n(row): across it
 #pragma unroll
-      for (int i = 0; i < kPerA; ++i) {  // a row past the last one repeats it: its outputs are not stored
-        const int r = group_row(i) + (lane >> 3);
-        const T* const row = q.A + (at.m0 + (r < at.mrows ? r : at.mrows - 1)) * q.lda;
-        hold[i] = whole ? __builtin_bit_cast(u4, *reinterpret_cast<const typename Vec8<T>::Raw*>(row + c)) : vec(row, c, q.R);
-      }
-#pragma unroll
-      for (int i = 0; i < kPerB; ++i) {
-        if constexpr (kNN) {  // a row past the sum's end is zero
-          const int k = k0 + 2 * (i * kWaves + w) + kr, col = at.n0 + 8 * xn;
-          const u4 v = k < q.R ? vec(q.B + (int64_t)k * q.ldb, col, N) : (u4){0, 0, 0, 0};
-          hold[kPerA + i] = v;
-        } else {
-          const int g = group_row(i), r = out_row(g) + (lane >> 3);
-          const bool two = second(g);
-          const T* const row = (two ? q.B2 : q.B) + (int64_t)(at.n0 + (r < at.ncols ? r : at.ncols - 1)) * (two ? q.ldb2 : q.ldb);
-          hold[kPerA + i] = whole ? __builtin_bit_cast(u4, *reinterpret_cast<const typename Vec8<T>::Raw*>(row + c)) : vec(row, c, q.R);
+        for (int i = 0; i < kPerA; ++i) {  // a row past the last one repeats it: its outputs are not stored
+          const int r = group_row(i) + (lane >> 3);
+          hold[i] = load_k(q.A + (at.m0 + (r < at.mrows ? r : at.mrows - 1)) * q.lda);
         }
-      }
-    };
-    const auto put = [&](int stage, const u4 (&hold)[kAl ? 1 : kPer]) {
 #pragma unroll
-      for (int i = 0; i < (kAl ? 1 : kPer); ++i)
-        *reinterpret_cast<u4*>(smem + stage * kStage + (i < kPerA ? 0 : kStageA) + ((i < kPerA ? i : i - kPerA) * kWaves + w) * 1024 +
-                               lane * 16) = hold[i];
+        for (int i = 0; i < kPerB; ++i) {
+          if constexpr (kNN) {
+            const int k = k0 + 2 * (i * kWaves + w) + kr;
+            hold[kPerA + i] = load_n(q.B + (int64_t)(k < q.R ? k : q.R - 1) * q.ldb);
+          } else {
+            const int g = group_row(i), r = out_row(g) + (lane >> 3);
+            const int64_t n = at.n0 + (r < at.ncols ? r : at.ncols - 1);
+            hold[kPerA + i] = load_k(second(g) ? q.B2 + n * q.ldb2 : q.B + n * q.ldb);
+          }
+        }
+      };
+      const auto vec = [](const T* p) { return __builtin_bit_cast(u4, *reinterpret_cast<const typename Vec8<T>::Raw*>(p)); };
+      const auto few = [](const T* row, int c, int n) { return __builtin_bit_cast(u4, load8<T>(row, c, n)); };
+      if (q.R >= 8 && !short_n)
+        rows([&](const T* row) { return vec(row + ca); }, [&](const T* row) { return vec(row + cb); });
+      else
+        rows([&](const T* row) { return few(row, c, q.R); }, [&](const T* row) { return few(row, col, N); });
+    };
+    const auto put = [&](int s, int stage, const u4 (&hold)[kAl ? 1 : kPer]) {
+      const bool next = kSrc == 2 && s >= src[0].steps;
+      const Source<T>& q = src[kSrc == 2 && next ? kSrc - 1 : 0];
+      const int k0 = (next ? s - src[0].steps : s) * kTK, c = k0 + 8 * xc, col = at.n0 + 8 * xn;
+      const bool ends_k = k0 + kTK > q.R, ends_n = kNN && at.n0 + BN > N;  // uniform
+      const bool by_elements = q.R < 8 || short_n;
+      const auto fix = [&](u4 v, int c, int n) {
+        if (by_elements) return v;
+        typename Vec8<T>::Raw r = __builtin_bit_cast(typename Vec8<T>::Raw, v);
+        shift_down(r, 8 - n % 8);
+        const u4 t = __builtin_bit_cast(u4, r), zero = {0, 0, 0, 0};
+        return c + 8 <= n ? v : c < n ? t : zero;
+      };
+      const auto store = [&](auto value) {
+#pragma unroll
+        for (int i = 0; i < (kAl ? 1 : kPer); ++i)
+          *reinterpret_cast<u4*>(smem + stage * kStage + (i < kPerA ? 0 : kStageA) +
+                                 ((i < kPerA ? i : i - kPerA) * kWaves + w) * 1024 + lane * 16) = value(i);
+      };
+      if (!ends_k && !ends_n) {
+        store([&](int i) { return hold[i]; });
+      } else {
+        store([&](int i) {
+          if (!kNN || i < kPerA) return fix(hold[i], c, q.R);
+          const bool past = k0 + 2 * ((i - kPerA) * kWaves + w) + kr >= q.R;
+          return past ? (u4){0, 0, 0, 0} : fix(hold[i], col, N);
+        });
+      }
     };
 
 #pragma unroll
@@ -345,8 +368,8 @@ struct Tile {
       u4 ahead[kAl ? 1 : kPer];
       fetch(s0, hold);
       fetch(s0 + 1, ahead);
-      put(0, hold);
-      put(1, ahead);
+      put(s0, 0, hold);
+      put(s0 + 1, 1, ahead);
       fetch(s0 + 2, hold);
       __builtin_amdgcn_s_waitcnt(kWaitLds);
     }
@@ -371,7 +394,7 @@ struct Tile {
         __builtin_amdgcn_sched_barrier(0);
         phase(1, in_a, in_b, kPer, [&](int i) { i < kPerA ? load_a(la, i) : load_b(lb, i - kPerA); });
       } else {
-        put(free_a / kStage, hold);
+        put(s + 2, free_a / kStage, hold);
         fetch(s + 3, hold);
         __builtin_amdgcn_sched_barrier(0);
         phase(1, in_a, in_b, 0, [](int) {});
@@ -428,17 +451,25 @@ __device__ __forceinline__ void eight(const float* p, float (&v)[8]) {
 template <typename F>
 __device__ __forceinline__ void share(const Work& k, F body) {
   const uint32_t lb = block_of(k.grid);
-  uint32_t t = lb, it = lb * (uint32_t)k.per, slot = 2 * lb;
-  const uint32_t all = (k.tiles - k.full) * (uint32_t)k.steps;
+  const uint32_t rest = k.tiles - k.full - k.cut;
+  uint32_t t = lb, it = lb * (uint32_t)k.per, slot = k.grid + 2 * lb;
+  bool cut = k.cut > 0 && (int64_t)(lb / k.cut) * k.chunk < k.steps;
+  const uint32_t all = rest * (uint32_t)k.steps;
   const uint32_t end = it + (uint32_t)k.per < all ? it + (uint32_t)k.per : all;
   for (;;) {
     uint32_t tile = t;
     int s0 = 0, s1 = k.steps, to = -1;
     if (t < k.full) {
       t += k.grid;
+    } else if (cut) {
+      cut = false;
+      tile = k.full + lb % k.cut;
+      s0 = (int)(lb / k.cut) * k.chunk;
+      if (k.steps - s0 > k.chunk) s1 = s0 + k.chunk;
+      to = (int)lb;
     } else if (it < end) {
       const uint32_t q = it / (uint32_t)k.steps;
-      tile = k.full + q;
+      tile = k.full + k.cut + q;
       s0 = (int)(it - q * (uint32_t)k.steps);
       if (k.steps - s0 > (int)(end - it)) s1 = s0 + (int)(end - it);
       to = (int)slot++;
@@ -453,13 +484,19 @@ __device__ __forceinline__ void share(const Work& k, F body) {
 // The partial tiles of split tile q (counted from `full`), in the order of the sum: f(slot) for each.
 template <typename F>
 __device__ __forceinline__ void parts(const Work& k, uint32_t q, F f) {
-  const uint32_t a = q * (uint32_t)k.steps, b = a + (uint32_t)k.steps, per = (uint32_t)k.per;
-  for (uint32_t lb = a / per; lb * per < b; ++lb) f(2 * lb + (lb * per < a ? 1 : 0));
+  if (q < k.cut) {
+    for (int s0 = 0; s0 < k.steps; s0 += k.chunk, q += k.cut) f(q);
+    return;
+  }
+  const uint32_t a = (q - k.cut) * (uint32_t)k.steps, b = a + (uint32_t)k.steps, per = (uint32_t)k.per;
+  for (uint32_t lb = a / per; lb * per < b; ++lb) f(k.grid + 2 * lb + (lb * per < a ? 1 : 0));
 }
 
-// The rest of a product's tiles that does not fill a round of the grid, in equal runs of steps where that is estimated
-// to take less time than one more round: a run is 4 steps at least; a split costs its partial tiles' way to memory and
-// back (5 MB / us) and 4 us for the second launch. `step`: us of one step when every unit works.
+// The rest of a product's tiles that does not fill a round of the grid is split where that is estimated to take less
+// time than one more round: into as many equal runs each as there are blocks for, or into one run more where that leaves
+// some of the tiles over, whose steps are then shared by all. A run is 4 steps at least; a split costs its partial
+// tiles' way to memory and back (5 MB / us) and 4 us for the second launch; a tile's ends cost 4 us; a step that is not shared in the L2 costs half
+// as much again. `step`: us of one step when every unit works.
 struct Lay {
   Work work;
   double est;
@@ -472,16 +509,31 @@ inline Lay lay(int64_t tiles_m, int64_t tiles_n, int64_t steps, double step, int
   l.work.tiles = (uint32_t)tiles, l.work.tiles_m = (uint32_t)tiles_m, l.work.steps = (int)steps;
   l.work.full = (uint32_t)tiles;
   l.work.grid = rounds > 0 ? (uint32_t)kUnits : eights(rest);
-  l.est = 5.0 + (double)(rounds + (rest > 0)) * (double)(steps + 3) * step;
+  constexpr double kTile = 4.0;  // us of a tile's beginning and end
+  l.est = 3.0 + (double)(rounds + (rest > 0)) * ((double)steps * step + kTile);
   if (rest == 0 || rest * steps >= (int64_t)1 << 31) return l;
-  const int64_t total = rest * steps, most = (total + 3) / 4;
-  const int64_t grid = rounds > 0 || most >= kUnits ? kUnits : eights(most), per = (total + grid - 1) / grid;
-  if (per >= steps) return l;
-  const int64_t bytes = 2 * grid * tile_bytes, moved = ((total + per - 1) / per + rest) * tile_bytes;
-  const double est = 9.0 + (double)rounds * (double)(steps + 3) * step + (double)(per + 3) * step + (double)moved * 2 / 5e6;
-  if (est >= l.est) return l;
-  l.work.full = (uint32_t)(tiles - rest), l.work.grid = (uint32_t)grid, l.work.per = (int)per;
-  l.est = est, l.part_bytes = (size_t)bytes;
+  const int64_t most = (steps + 3) / 4 > 1 ? (steps + 3) / 4 : 1;  // runs of a tile
+  for (int64_t runs = kUnits / rest; runs <= kUnits / rest + 1; ++runs) {
+    if (runs < 2 || runs > most) {
+      if (runs < 2 || kUnits / rest < most) continue;
+      runs = most;  // few tiles of few steps: not every unit gets a run
+      if (runs < 2) break;
+    }
+    const int64_t chunk = (steps + runs - 1) / runs, each = (steps + chunk - 1) / chunk;
+    const int64_t cut = each * rest <= kUnits ? rest : kUnits / each, left = rest - cut;
+    const int64_t per = (left * steps + kUnits - 1) / kUnits;
+    if (chunk >= steps || cut < 1 || per >= steps) break;
+    const int64_t blocks = left > 0 || rounds > 0 ? kUnits : eights(cut * each);
+    const int64_t kept = left > 0 ? 3 * blocks : cut * each, moved = 2 * (cut * each + (left > 0 ? kUnits + left : 0));
+    const double est = 7.0 + (double)rounds * ((double)steps * step + kTile) + (double)chunk * step + kTile +
+                       (left > 0 ? (double)per * 1.5 * step + kTile : 0.0) + (double)(moved * tile_bytes) / 5e6;
+    if (est < l.est) {
+      l.work.full = (uint32_t)(tiles - rest), l.work.cut = (uint32_t)cut, l.work.chunk = (int)chunk;
+      l.work.per = (int)per, l.work.grid = (uint32_t)blocks;
+      l.est = est, l.part_bytes = (size_t)(kept * tile_bytes);
+    }
+    if (runs == most) break;
+  }
   return l;
 }
 

@@ -253,7 +253,8 @@ def test_dx_edges(M, N, K):
 
 
 @pytest.mark.parametrize("M", [1, 5, 64, 100, 130])
-@pytest.mark.parametrize("N,K", [(1, 1), (3, 5), (7, 64), (63, 9), (65, 257), (997, 300), (64, 250), (66, 256)])
+@pytest.mark.parametrize("N,K", [(1, 1), (3, 5), (7, 64), (63, 9), (65, 257), (997, 300), (64, 250), (66, 256),
+                                 (100, 1), (65, 7), (203, 5), (5, 203), (7, 1000)])
 def test_dx_edges_unaligned(M, N, K):
     dx_case(2, M, N, K, "f16", "f32")
 
