@@ -170,28 +170,38 @@ struct ProductArgs {
   const int32_t* skip;
 };
 
+// what an output's 8 columns are made of beside their sums: A, or the two halves of X
+struct Beside {
+  Vec8<half_t>::Raw a, b;
+};
+template <Kind kind>
+__device__ __forceinline__ Beside beside(const ProductArgs& a, int64_t m, int n) {
+  const int64_t at = m * a.ld + n;
+  Beside x{};
+  if constexpr (kind == Kind::kPoly) x.a = *reinterpret_cast<const Vec8<half_t>::Raw*>(a.A + at);
+  if constexpr (kind == Kind::kNext) {
+    x.a = *reinterpret_cast<const Vec8<half_t>::Raw*>(a.hi + at);
+    x.b = *reinterpret_cast<const Vec8<half_t>::Raw*>(a.lo + at);
+  }
+  return x;
+}
 // 8 columns of a row from their sums, into the output's fp16; v becomes what its transpose takes
 template <Kind kind>
-__device__ __forceinline__ void finish8(const ProductArgs& a, float (&v)[8], int64_t m, int n) {
+__device__ __forceinline__ void finish8(const ProductArgs& a, const Beside& x, float (&v)[8], int64_t m, int n) {
   const int64_t at = m * a.ld + n;
   half_t o[8];
   if constexpr (kind == Kind::kGram) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) o[j] = (half_t)(v[j] * (kScaleA / (kScaleX * kScaleX)));
   } else if constexpr (kind == Kind::kPoly) {
-    const Vec8<half_t>::Raw g = *reinterpret_cast<const Vec8<half_t>::Raw*>(a.A + at);
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      o[j] = (half_t)fmaf(kB * (kScaleB / kScaleA), Vec8<half_t>::get(g, j), v[j] * (kC * (kScaleB / (kScaleA * kScaleA))));
+      o[j] = (half_t)fmaf(kB * (kScaleB / kScaleA), Vec8<half_t>::get(x.a, j), v[j] * (kC * (kScaleB / (kScaleA * kScaleA))));
   } else {
-    const Vec8<half_t>::Raw h = *reinterpret_cast<const Vec8<half_t>::Raw*>(a.hi + at);
-    const Vec8<half_t>::Raw l = *reinterpret_cast<const Vec8<half_t>::Raw*>(a.lo + at);
     half_t o2[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float x = Vec8<half_t>::get(h, j) + Vec8<half_t>::get(l, j);
-      split(fmaf(kA, x, v[j] * (1.f / kScaleB)), o[j], o2[j]);
-    }
+    for (int j = 0; j < 8; ++j)
+      split(fmaf(kA, Vec8<half_t>::get(x.a, j) + Vec8<half_t>::get(x.b, j), v[j] * (1.f / kScaleB)), o[j], o2[j]);
     *reinterpret_cast<tile::u4*>(a.out_lo + at) = *reinterpret_cast<const tile::u4*>(o2);
   }
   *reinterpret_cast<tile::u4*>(a.out + at) = *reinterpret_cast<const tile::u4*>(o);
@@ -240,13 +250,16 @@ __global__ __launch_bounds__(C::kThreads, 2) void muon_product_kernel(ProductArg
     C::run(a.src, at, a.N, s0, s1, t_smem, acc);
     float* const part = slot < 0 ? nullptr : a.part + (int64_t)slot * C::BM * C::BN;
     const bool turn = !part && a.out_t && (kind == Kind::kNext || at.m0 != at.n0);
-    C::rows(acc, t_smem, [&](int r, int c, float* p) {
+    Beside x[C::kPasses];  // on its way from memory before it is needed
+    C::rows_ahead(acc, t_smem, [&](int s, int r, int c) {
+      if (!part && r < at.mrows && c < at.ncols) x[s] = beside<kind>(a, at.m0 + r, at.n0 + c);
+    }, [&](int s, int r, int c, float* p) {
       float v[8];
       tile::eight(p, v);
       if (part) {
         store8<float>(part + r * C::BN, c, C::BN, v);
       } else if (r < at.mrows && c < at.ncols) {
-        finish8<kind>(a, v, at.m0 + r, at.n0 + c);
+        finish8<kind>(a, x[s], v, at.m0 + r, at.n0 + c);
         if (turn) {
           *reinterpret_cast<f4*>(p) = (f4){v[0], v[1], v[2], v[3]};
           *reinterpret_cast<f4*>(p + 4) = (f4){v[4], v[5], v[6], v[7]};
@@ -280,7 +293,11 @@ __global__ __launch_bounds__(2 * join_cols<C>()) void muon_join_kernel(ProductAr
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] += p[j];
   });
-  if (r0 + r < at.mrows && c0 + c < at.ncols) finish8<kind>(a, v, at.m0 + r0 + r, at.n0 + c0 + c);
+  if (r0 + r < at.mrows && c0 + c < at.ncols) {
+    const int64_t m = at.m0 + r0 + r;
+    const int n = at.n0 + c0 + c;
+    finish8<kind>(a, beside<kind>(a, m, n), v, m, n);
+  }
   if (!a.out_t || (kind != Kind::kNext && at.m0 == at.n0) || r0 >= at.mrows) return;
 #pragma unroll
   for (int j = 0; j < 8; ++j) turn[r * kPad + c + j] = v[j];

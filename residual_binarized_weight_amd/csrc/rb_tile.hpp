@@ -411,16 +411,40 @@ struct Tile {
   // may change. D of the product: lane l holds columns 4 (l / 16) .. + 3 of row l % 16. turned(row, column, p) is called
   // once for 16 rows and all of the wave's columns and sees what f left (row stride kPad). LDS must be free; the block
   // synchronises before its next use.
+  // ahead(s, row, column) is called before the 16 rows are turned, for what f will read at the s-th of its kPasses places.
+  static constexpr int kLanes = kWaveN / 8, kAtOnce = 64 / kLanes, kPasses = 16 / kAtOnce;  // lanes of a row, rows at once
+  template <typename A, typename F, typename G>
+  __device__ static __forceinline__ void rows_ahead(const f4 (&acc)[kTM][kTN], uint8_t* smem, A ahead, F f, G turned) {
+    walk(acc, smem, ahead, [&](int i, int w, int lane, float* turn) {
+#pragma unroll
+      for (int s = 0; s < kPasses; ++s) pass(i, s, w, lane, turn, f);
+    }, turned);
+  }
   template <typename F, typename G>
   __device__ static __forceinline__ void rows(const f4 (&acc)[kTM][kTN], uint8_t* smem, F f, G turned) {
+    walk(acc, smem, [](int, int, int) {}, [&](int i, int w, int lane, float* turn) {
+#pragma unroll 1
+      for (int s = 0; s < kPasses; ++s) pass(i, s, w, lane, turn, [&](int, int r, int c, float* p) { f(r, c, p); });
+    }, turned);
+  }
+
+ private:
+  template <typename F>
+  __device__ static __forceinline__ void pass(int i, int s, int w, int lane, float* turn, F f) {
+    const int r = kAtOnce * s + lane / kLanes, c = 8 * (lane % kLanes);
+    f(s, ((w % kWM) * kTM + i) * 16 + r, (w / kWM) * kWaveN + c, turn + r * kPad + c);
+  }
+  template <typename A, typename P, typename G>
+  __device__ static __forceinline__ void walk(const f4 (&acc)[kTM][kTN], uint8_t* smem, A ahead, P passes, G turned) {
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int wm = w % kWM, wn = w / kWM;
     const int lr = lane & 15, lj = lane >> 4;
     float* const turn = reinterpret_cast<float*>(smem) + w * (16 * kPad);
-    constexpr int kLanes = kWaveN / 8, kAtOnce = 64 / kLanes;  // lanes of a row, rows at once
 #pragma unroll 1
     for (int i = 0; i < kTM; ++i) {
+#pragma unroll
+      for (int s = 0; s < kPasses; ++s)
+        pass(i, s, w, lane, turn, [&](int s, int r, int c, float*) { ahead(s, r, c); });
 #pragma unroll
       for (int q = 0; q < kTM; ++q)
         if (q == i) {
@@ -428,13 +452,9 @@ struct Tile {
           for (int j = 0; j < kTN; ++j) *reinterpret_cast<f4*>(turn + lr * kPad + 16 * j + 4 * lj) = acc[q][j];
         }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-#pragma unroll 1
-      for (int s = 0; s < 16 / kAtOnce; ++s) {
-        const int r = kAtOnce * s + lane / kLanes, c = 8 * (lane % kLanes);
-        f((wm * kTM + i) * 16 + r, wn * kWaveN + c, turn + r * kPad + c);
-      }
+      passes(i, w, lane, turn);
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      turned((wm * kTM + i) * 16, wn * kWaveN, turn);
+      turned(((w % kWM) * kTM + i) * 16, (w / kWM) * kWaveN, turn);
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
   }
