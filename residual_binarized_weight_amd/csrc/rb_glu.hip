@@ -8,6 +8,7 @@
 //   glu_tile_kernel     a tile of batch rows by rows of both weights, on the matrix cores; glu_join_kernel the sums of
 //                       split tiles, and the epilogue
 //   glu_rows_kernel     up to 4 batch rows, on the vector units: a wave streams a row of each weight
+//   glu_few_kernel      small products of 5 to 256 batch rows, on the matrix cores, a block's waves splitting the columns
 //   glu_grad_kernel     dG, dU and, per strip of rows, partial column sums; glu_grad_sum_kernel adds them
 //   glu_dx_kernel       a tile of dX, both products in one run of sums; glu_dx_join_kernel for split tiles
 #include "rb_act.hpp"
@@ -61,6 +62,17 @@ __device__ __forceinline__ void finish8(const GluOut& o, float (&g)[8], float (&
 #pragma unroll
   for (int j = 0; j < 8; ++j) g[j] *= u[j];
   store_out<TH>(static_cast<TH*>(o.H) + m * o.ldh, n, N, g, o.line_h);
+}
+
+// ... and one of them
+template <typename T, typename TH>
+__device__ __forceinline__ void finish1(const GluOut& o, float g, float u, int64_t m, int n) {
+  if (o.bg) g += o.bg[n];
+  if (o.bu) u += o.bu[n];
+  if (o.G) static_cast<T*>(o.G)[m * o.ldg + n] = Vec8<T>::narrow(g);
+  if (o.U) static_cast<T*>(o.U)[m * o.ldu + n] = Vec8<T>::narrow(u);
+  if (o.act != RB_ACT_NONE) g = act_value(g, o.act);
+  static_cast<TH*>(o.H)[m * o.ldh + n] = Vec8<TH>::narrow(g * u);
 }
 
 template <typename T>
@@ -172,14 +184,67 @@ __global__ __launch_bounds__(256) void glu_rows_kernel(GluArgs<T> a) {
     g = lane == m ? x : g;
     u = lane == m ? y : u;
   }
-  if (lane >= MR || lane >= a.M) return;
-  const GluOut& o = a.out;
-  if (o.bg) g += o.bg[n];
-  if (o.bu) u += o.bu[n];
-  if (o.G) static_cast<T*>(o.G)[lane * o.ldg + n] = Vec8<T>::narrow(g);
-  if (o.U) static_cast<T*>(o.U)[lane * o.ldu + n] = Vec8<T>::narrow(u);
-  if (o.act != RB_ACT_NONE) g = act_value(g, o.act);
-  static_cast<TH*>(o.H)[lane * o.ldh + n] = Vec8<TH>::narrow(g * u);
+  if (lane < MR && lane < a.M) finish1<T, TH>(a.out, g, u, lane, n);
+}
+
+// Small products: one launch on the matrix cores, without partial sums in memory. A block owns 16 rows of each weight by
+// 16 batch rows; its 8 waves take the 64-column steps in turn, each with its fragments straight from memory, and join
+// in LDS in their order. The fragments' 16-byte pieces cost the address unit a piece each, which bounds the rate.
+constexpr int kFewRows = 256;
+constexpr double kFewStep = 0.2, kFewStepOdd = 0.5;  // us of a step of 64 columns in 256 blocks
+
+template <typename T, typename TH>
+__global__ __launch_bounds__(512) void glu_few_kernel(GluArgs<T> a) {
+  constexpr int kWaves = 8, kAhead = 4;  // steps whose loads a wave has in flight
+  __shared__ __align__(16) float sums[2][kWaves][256];
+  const Source<T>& q = a.src[0];
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int lr = lane & 15, lj = lane >> 4;
+  const int n0 = blockIdx.x * 16;
+  const int64_t m0 = (int64_t)blockIdx.y * 16;
+  // rows past the last one repeat it: their outputs are not stored
+  const int64_t n = n0 + lr < a.N ? n0 + lr : a.N - 1;
+  const T* const row[3] = {q.B + n * q.ldb, q.B2 + n * q.ldb2, q.A + (m0 + lr < a.M ? m0 + lr : a.M - 1) * q.lda};
+  f4 acc[2] = {};
+  for (int k0 = w * tile::kTK; k0 < q.R; k0 += kAhead * kWaves * tile::kTK) {
+    typename Vec8<T>::Raw f[kAhead][2][3] = {};
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 3; ++i) load8_long<T>(f[s][h][i], row[i], k0 + s * kWaves * tile::kTK + 32 * h + 8 * lj, q.R);
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int c = k0 + s * kWaves * tile::kTK + 32 * h + 8 * lj;
+        if (c < q.R && c + 8 > q.R) {  // the vector at the end of the columns
+#pragma unroll
+          for (int i = 0; i < 3; ++i) shift_down(f[s][h][i], c + 8 - q.R);
+        }
+        const tile::u4 x = __builtin_bit_cast(tile::u4, f[s][h][2]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) acc[i] = tile::mfma(T(0), __builtin_bit_cast(tile::u4, f[s][h][i]), x, acc[i]);
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) *reinterpret_cast<f4*>(&sums[i][w][lane * 4]) = acc[i];
+  __syncthreads();
+  // thread 16 m + n: D's lane 16 (n / 4) + m holds weight row n in element n % 4
+  if (threadIdx.x >= 256) return;
+  const int mm = threadIdx.x >> 4, nn = threadIdx.x & 15, on = n0 + nn;
+  const int64_t m = m0 + mm;
+  if (m >= a.M || on >= a.N) return;
+  float g = 0.f, u = 0.f;
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) {
+    const int at = ((nn >> 2) * 16 + mm) * 4 + (nn & 3);
+    g += sums[0][i][at];
+    u += sums[1][i][at];
+  }
+  finish1<T, TH>(a.out, g, u, m, on);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -340,18 +405,14 @@ Choice choose(int64_t M, int64_t out_n, int per_tile, int64_t steps, bool aligne
 int64_t steps_of(int64_t R) { return (R + tile::kTK - 1) / tile::kTK; }
 bool small_ld(int64_t ld) { return ld < (1 << 21); }  // a tile's rows lie within 2^31 bytes, the out-of-range marker
 
-template <typename K>
-hipError_t lds_for(K kernel, int bytes) {
-  return hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-}
-
 template <typename T, typename TH, int kBM, bool kAl>
 hipError_t launch_glu_tile(const GluArgs<T>& a, hipStream_t s) {
   typedef typename Shape<T, false, kBM, kAl>::C C;
-  static const hipError_t attr = lds_for(glu_tile_kernel<T, TH, C>, C::kLds);
-  if (attr != hipSuccess) return attr;
+  static std::atomic<uint64_t> done;
+  hipError_t e = tile::allow_lds(done, glu_tile_kernel<T, TH, C>, C::kLds);
+  if (e != hipSuccess) return e;
   glu_tile_kernel<T, TH, C><<<a.work.grid, C::kThreads, C::kLds, s>>>(a);
-  hipError_t e = hipGetLastError();
+  e = hipGetLastError();
   if (e != hipSuccess || a.work.full == a.work.tiles) return e;
   glu_join_kernel<T, TH, C><<<dim3(a.work.tiles - a.work.full, C::BM * C::kOutN / 8 / 256), 256, 0, s>>>(a);
   return hipGetLastError();
@@ -368,14 +429,32 @@ hipError_t launch_glu_rows(GluArgs<T> a, hipStream_t s) {
   });
 }
 
-bool rows_form(int64_t M, int64_t K) { return M <= kMaxRows && K >= 8; }
+// The forms without tiles; both read 8 columns at least. Up to 4 rows the vector units' products cost nothing beside
+// the weights. The one-launch form on the matrix cores is taken by its estimate against the tiles', up to the 256 rows
+// that the estimate holds for (us, one launch / tiles: 5 x 1000 x 1000 4.1 / 12.5, 16 x 2048 x 2048 8.5 / 15.3, 64 x 1408 x
+// 1024 8.6 / 13.3, 64 x 2048 x 2048 14.2 / 17.4, 64 x 4096 x 4096 53 / 27, 256 x 512 x 512 5.6 / 10.8; rows not aligned: 5 x
+// 1000 x 1001 7.3 / 15.7, 61 x 1411 x 1027 14.2 / 17.0, 16 x 2047 x 2047 21.4 / 19.4, 128 x 1023 x 1023 21.7 / 17.2).
+enum class Small { kNone, kRows, kFew };
+Small small_form(int64_t M, int64_t N, int64_t K, bool aligned) {
+  if (K < 8 || M > kFewRows) return Small::kNone;
+  if (M <= kMaxRows) return Small::kRows;
+  const double blocks = (double)((N + 15) / 16 * ((M + 15) / 16)), rounds = blocks < 256 ? 1.0 : blocks / 256;
+  return 2.6 + rounds * (double)steps_of(K) * (aligned ? kFewStep : kFewStepOdd) < choose(M, N, 128, steps_of(K), aligned, false).lay.est
+             ? Small::kFew : Small::kNone;
+}
 
 template <typename T, typename TH>
 hipError_t launch_glu_product(GluArgs<T> a, void* ws, hipStream_t s) {
   const Source<T>& q = a.src[0];
-  if (rows_form(a.M, q.R)) return launch_glu_rows<T, TH>(a, s);
   const bool al = tile::rows16(q.A, q.lda) && tile::rows16(q.B, q.ldb) && tile::rows16(q.B2, q.ldb2) && q.R % 8 == 0 &&
                   small_ld(q.lda) && small_ld(q.ldb) && small_ld(q.ldb2);
+  switch (small_form(a.M, a.N, q.R, al)) {
+    case Small::kRows: return launch_glu_rows<T, TH>(a, s);
+    case Small::kFew:
+      glu_few_kernel<T, TH><<<dim3((uint32_t)((a.N + 15) / 16), (uint32_t)((a.M + 15) / 16)), 512, 0, s>>>(a);
+      return hipGetLastError();
+    case Small::kNone: break;
+  }
   const Choice c = choose(a.M, a.N, 128, q.steps, al, false);
   a.work = c.lay.work;
   a.part = static_cast<float*>(ws);
@@ -395,10 +474,11 @@ hipError_t launch_glu_typed(const void* X, int64_t M, int64_t ldx, const void* W
 template <typename T, typename TX, int kBM, bool kAl>
 hipError_t launch_dx_tile(const DxArgs<T>& a, hipStream_t s) {
   typedef typename Shape<T, true, kBM, kAl>::C C;
-  static const hipError_t attr = lds_for(glu_dx_kernel<T, TX, C>, C::kLds);
-  if (attr != hipSuccess) return attr;
+  static std::atomic<uint64_t> done;
+  hipError_t e = tile::allow_lds(done, glu_dx_kernel<T, TX, C>, C::kLds);
+  if (e != hipSuccess) return e;
   glu_dx_kernel<T, TX, C><<<a.work.grid, C::kThreads, C::kLds, s>>>(a);
-  hipError_t e = hipGetLastError();
+  e = hipGetLastError();
   if (e != hipSuccess || a.work.full == a.work.tiles) return e;
   glu_dx_join_kernel<T, TX, C><<<dim3(a.work.tiles - a.work.full, C::BM * C::kOutN / 8 / 256), 256, 0, s>>>(a);
   return hipGetLastError();
@@ -437,10 +517,13 @@ int grad_strip(int64_t M, int64_t N) {
 }  // namespace
 
 size_t glu_workspace_bytes(int64_t N, int64_t K, int64_t M) {
-  if (rows_form(M, K)) return 0;
-  const size_t a = choose(M, N, 128, steps_of(K), false, false).lay.part_bytes;
-  const size_t b = choose(M, N, 128, steps_of(K), true, false).lay.part_bytes;
-  return a > b ? a : b;
+  size_t most = 0;
+  for (const bool al : {false, true}) {
+    if (small_form(M, N, K, al) != Small::kNone) continue;
+    const size_t b = choose(M, N, 128, steps_of(K), al, false).lay.part_bytes;
+    most = b > most ? b : most;
+  }
+  return most;
 }
 
 hipError_t launch_glu(const void* X, rb_dtype a_dtype, int64_t M, int64_t ldx, const void* Wg, int64_t ldwg, const void* Wu,

@@ -409,11 +409,11 @@ Buffers buffers(int64_t N, int64_t K) {
 template <int kSize, Kind kind>
 hipError_t launch_size(const ProductArgs& a, hipStream_t s) {
   typedef typename Square<kSize>::C C;
-  static const hipError_t attr = hipFuncSetAttribute((const void*)muon_product_kernel<C, kind>,
-                                                     hipFuncAttributeMaxDynamicSharedMemorySize, C::kLds);
-  if (attr != hipSuccess) return attr;
+  static std::atomic<uint64_t> done;
+  hipError_t e = tile::allow_lds(done, muon_product_kernel<C, kind>, C::kLds);
+  if (e != hipSuccess) return e;
   muon_product_kernel<C, kind><<<a.work.grid, C::kThreads, C::kLds, s>>>(a);
-  const hipError_t e = hipGetLastError();
+  e = hipGetLastError();
   if (e != hipSuccess || a.work.full == a.work.tiles) return e;
   constexpr int cols = join_cols<C>();
   muon_join_kernel<C, kind><<<dim3(a.work.tiles - a.work.full, C::BM / 16 * (C::BN / cols)), 2 * cols, 0, s>>>(a);

@@ -224,9 +224,8 @@ __global__ __launch_bounds__(64 * kWaves) void q4_product_kernel(Args a) {
 template <typename T, int kGroup, bool kPair, int kM, int kWaves>
 hipError_t launch_one(Args a, hipStream_t s) {
   constexpr int lds = Kernel<T, kGroup, kPair, kM, kWaves>::kLds;
-  static const hipError_t attr = hipFuncSetAttribute((const void*)q4_product_kernel<T, kGroup, kPair, kM, kWaves>,
-                                                     hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-  if (attr != hipSuccess) return attr;
+  static std::atomic<uint64_t> done;
+  if (const hipError_t e = tile::allow_lds(done, q4_product_kernel<T, kGroup, kPair, kM, kWaves>, lds); e != hipSuccess) return e;
   return launch_in_parts((a.N + kTileN - 1) / kTileN, [&](int64_t first, uint32_t blocks) {
     a.first = first;
     const uint32_t grid = (blocks + tile::kXcds - 1) / tile::kXcds * tile::kXcds;

@@ -7,6 +7,8 @@
 // The kernels that use it own their epilogues: rb_glu.hip, rb_muon.hip.
 #pragma once
 
+#include <atomic>
+
 #include "rb_elem.hpp"
 
 namespace rb {
@@ -555,6 +557,18 @@ inline Lay lay(int64_t tiles_m, int64_t tiles_n, int64_t steps, double step, int
     if (runs == most) break;
   }
   return l;
+}
+
+// Lets a kernel take `bytes` of dynamic LDS on the current device; `done` holds a bit for every device where it may.
+template <typename K>
+hipError_t allow_lds(std::atomic<uint64_t>& done, K kernel, int bytes) {
+  int device = 0;
+  if (const hipError_t e = hipGetDevice(&device); e != hipSuccess) return e;
+  const uint64_t bit = device < 64 ? uint64_t(1) << device : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return hipSuccess;
+  const hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 inline bool rows16(const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0; }

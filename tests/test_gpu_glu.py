@@ -102,9 +102,28 @@ def test_tile_edges_unaligned(M, N, K):
     case(2, M, N, K, "f16", bias=True, hdt="f32", save=True)
 
 
+# the same where more rows, or longer ones, bring the tiles
+@pytest.mark.parametrize("M", [257, 271, 320, 385])
+@pytest.mark.parametrize("N,K", [(1, 8), (31, 64), (129, 72), (300, 1000)])
+def test_tile_edges_of_more_rows(M, N, K):
+    case(7, M, N, K, "bf16", bias=True, hdt="f32", save=True)
+
+
+@pytest.mark.parametrize("M", [257, 300, 400])
+@pytest.mark.parametrize("N,K", [(1, 1), (5, 3), (64, 7), (63, 9), (130, 63), (100, 997)])
+def test_tile_edges_unaligned_of_more_rows(M, N, K):
+    case(8, M, N, K, "f16", bias=True, hdt="f32", save=True)
+
+
+@pytest.mark.parametrize("M", [5, 20, 64, 100])
+@pytest.mark.parametrize("N,K", [(33, 20000), (129, 20001), (2000, 4104)])
+def test_long_rows(M, N, K):
+    case(9, M, N, K, "bf16", bias=True, hdt="f32", save=True)
+
+
 @pytest.mark.parametrize("pad,off", [(8, 0), (8, 8), (3, 0), (0, 1), (1, 5)])
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
-@pytest.mark.parametrize("M,K", [(1, 200), (3, 1032), (40, 264), (150, 328)])
+@pytest.mark.parametrize("M,K", [(1, 200), (3, 1032), (40, 264), (150, 328), (300, 264), (40, 9000)])
 def test_strides_and_offsets(pad, off, dt, M, K):
     case(3, M, 70, K, dt, bias=True, save=True, pad=pad, off=off)
 
@@ -115,7 +134,8 @@ def test_strides_and_offsets(pad, off, dt, M, K):
 def test_epilogues(act, dt, hdt, bias, save):
     case(4, 2, 130, 160, dt, act, bias, hdt, save)
     case(5, 37, 130, 160, dt, act, bias, hdt, save)
-    case(6, 37, 260, 3000, dt, act, bias, hdt, save)   # split tiles: the join's epilogue
+    case(6, 270, 130, 160, dt, act, bias, hdt, save)   # tiles
+    case(10, 37, 260, 20000, dt, act, bias, hdt, save)  # split tiles: the join's epilogue
 
 
 # rows enough for the 256-row tiles, a rest that is split, and rounds of whole tiles with a rest
@@ -142,8 +162,8 @@ def test_one_weight_without_the_other_bias():
             check(X, Wg, Wu, bg, bu, "gelu", H, G, None)
 
 
-@pytest.mark.parametrize("M,K", [(2, 64), (70, 64), (70, 4096), (300, 512)])
-def test_infinities_stay_in_their_rows_and_columns(M, K):
+@pytest.mark.parametrize("M,K", [(2, 64), (70, 64), (70, 20000), (300, 512)])
+def test_infinities_stay_in_their_rows_and_columns(M, K):  # in each of the forms
     r = np.random.default_rng(933)
     X, Wg, Wu = mat(r, M, K, "f16"), mat(r, 150, K, "f16", 0.1), mat(r, 150, K, "f16", 0.1)
     want, _, _ = rb.qat_glu(X, Wg, Wu, h_dtype=torch.float32)
@@ -313,7 +333,7 @@ def everything(seed=7, M=200, N=700, K=1032):
 def test_equal_calls_give_equal_results_whatever_the_workspace_held():
     r = np.random.default_rng(961)
     X, Wg, Wu = mat(r, 70, 5000, "bf16"), mat(r, 300, 5000, "bf16", 0.05), mat(r, 300, 5000, "bf16", 0.05)
-    n = rb.workspace_bytes(rb.RB_OP_QAT_GLU, 1, 300, 5000, 70)
+    n = rb.workspace_bytes(rb.RB_OP_QAT_GLU, 1, 300, 5000, 70)  # split tiles
     m = rb.workspace_bytes(rb.RB_OP_QAT_GLU_DX, 1, 300, 5000, 70)
     assert n > 0
     first = None
