@@ -19,6 +19,7 @@
 // Kernels of this file:
 //   muon_moment_kernel   m, and partial sums of u^2 (fp64);  muon_start_kernel  X from u and the norm
 //   muon_product_kernel  the three products, on the matrix cores;  muon_join_kernel  split tiles
+//   muon_few_kernel      the same for small matrices, a block's waves splitting the sum
 //   muon_apply_kernel    W and, where asked for, X itself
 #include "rb_internal.h"
 #include "rb_tile.hpp"
@@ -306,6 +307,69 @@ __global__ __launch_bounds__(2 * join_cols<C>()) void muon_join_kernel(ProductAr
   if (c0 + tc < at.ncols) put_turned(a, turn + h * kPad + tc, kPad, at.n0 + c0 + tc, at.m0 + r0 + h);
 }
 
+// Small matrices, whose steps are as many launches as products: a block owns 16 x 16 outputs; its 8 waves take the 64-term
+// steps in turn, each with its fragments straight from memory, and join in LDS in their order. Launches and
+// latency bound it (a wave has the loads of up to four of its steps in flight at once): 256 x 512, medians traced, 3.8 us for
+// A, 3.6 for B and 4.3 for the next X against 5.9, 5.9 and 5.6 on tiles of 64; the whole step 64 us against 85. From
+// 512 x 512 on the tiles are as fast or faster. Every size is a multiple of 64 here.
+template <Kind kind>
+__global__ __launch_bounds__(512) void muon_few_kernel(ProductArgs a) {
+  constexpr int kWaves = 8, kAhead = 4;  // steps whose loads a wave has in flight
+  __shared__ __align__(16) float sums[kWaves][256];
+  __shared__ half_t turn[16][17];
+  if (a.skip && *a.skip) return;
+  const Source<half_t>& q = a.src[0];
+  const int lane = threadIdx.x & 63, lr = lane & 15, lj = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  uint32_t tm = blockIdx.y, tn = blockIdx.x;
+  if (kind != Kind::kNext) place_lower(blockIdx.x, tm, tn);
+  const int64_t m0 = (int64_t)tm * 16, n0 = (int64_t)tn * 16;
+  const half_t* const row[2] = {q.B + (n0 + lr) * q.ldb + 8 * lj, q.A + (m0 + lr) * q.lda + 8 * lj};
+  f4 acc = {};
+  for (int s0 = w; s0 < q.steps; s0 += kAhead * kWaves) {
+    tile::u4 f[kAhead][2][2] = {};
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s)
+      if (s0 + s * kWaves < q.steps) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            f[s][h][i] = *reinterpret_cast<const tile::u4*>(row[i] + (int64_t)(s0 + s * kWaves) * tile::kTK + 32 * h);
+      }
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) acc = tile::mfma(half_t(0), f[s][h][0], f[s][h][1], acc);
+  }
+  *reinterpret_cast<f4*>(&sums[w][lane * 4]) = acc;
+  __syncthreads();
+  // thread 16 m + n: D's lane 16 (n / 4) + m holds column n in element n % 4
+  const int r = threadIdx.x >> 4 & 15, c = threadIdx.x & 15;
+  const bool mine = threadIdx.x < 256;
+  if (mine) {
+    float v = 0.f;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) v += sums[i][((c >> 2) * 16 + r) * 4 + (c & 3)];
+    const int64_t at = (m0 + r) * a.ld + n0 + c;
+    half_t o;
+    if constexpr (kind == Kind::kGram) {
+      o = (half_t)(v * (kScaleA / (kScaleX * kScaleX)));
+    } else if constexpr (kind == Kind::kPoly) {
+      o = (half_t)fmaf(kB * (kScaleB / kScaleA), (float)a.A[at], v * (kC * (kScaleB / (kScaleA * kScaleA))));
+    } else {
+      half_t lo;
+      split(fmaf(kA, (float)a.hi[at] + (float)a.lo[at], v * (1.f / kScaleB)), o, lo);
+      a.out_lo[at] = lo;
+    }
+    a.out[at] = o;
+    turn[r][c] = o;
+  }
+  if (!a.out_t || (kind != Kind::kNext && m0 == n0)) return;
+  __syncthreads();
+  if (mine) a.out_t[(n0 + r) * a.ld_t + m0 + c] = turn[c][r];
+}
+
 // ---------------------------------------------------------------------------------------------
 // the update
 // ---------------------------------------------------------------------------------------------
@@ -363,10 +427,14 @@ template <int kSize> struct Square;
 template <> struct Square<64> { typedef tile::Tile<half_t, 2, 2, 2, 2, 4, false, 0, 1, true> C; };
 template <> struct Square<128> { typedef tile::Tile<half_t, 2, 2, 4, 4, 3, false, 0, 1, true> C; };
 template <> struct Square<256> { typedef tile::Tile<half_t, 4, 2, 4, 8, 2, false, 0, 1, true> C; };
+// Small products go to muon_few_kernel where its estimate, kFewStep us a step of 64 for each round of 256 blocks, is below
+// the tiles'. Whole steps with it at 0.2 / 0.3 / 0.4 / 0.5, rounds not yet rounded up: 200 x 2000 90 / 90 / 100 / 100 us (all
+// on tiles 110), 512 x 512 116 / 105 / 105 / 100 (101); rounded up, at 0.3: 91 and 100.
 struct Choice {
-  int size;
+  int size;  // 0: muon_few_kernel
   tile::Lay lay;
 };
+constexpr double kFewStep = 0.3;
 Choice choose(int64_t M, int64_t N, int64_t steps, bool symmetric) {
   constexpr struct { int size; double step; } kinds[3] = {{64, 0.30}, {128, 0.60}, {256, 1.69}};
   Choice best{};
@@ -374,6 +442,11 @@ Choice choose(int64_t M, int64_t N, int64_t steps, bool symmetric) {
     const int64_t tm = (M + k.size - 1) / k.size, tn = (N + k.size - 1) / k.size;
     const tile::Lay l = tile::lay(symmetric ? 1 : tm, symmetric ? tm * (tm + 1) / 2 : tn, steps, k.step, (int64_t)k.size * k.size * 4);
     if (best.size == 0 || l.est < best.lay.est) best = Choice{k.size, l};
+  }
+  const int64_t m = M / 16, n = N / 16, blocks = symmetric ? m * (m + 1) / 2 : m * n;
+  if (2.6 + (double)((blocks + 255) / 256) * (double)steps * kFewStep < best.lay.est) {
+    best.size = 0;
+    best.lay.part_bytes = 0;
   }
   return best;
 }
@@ -421,6 +494,11 @@ hipError_t launch_size(const ProductArgs& a, hipStream_t s) {
 }
 template <Kind kind>
 hipError_t launch_product(const Choice& c, const ProductArgs& a, hipStream_t s) {
+  if (c.size == 0) {
+    const uint32_t m = (uint32_t)a.M / 16, n = (uint32_t)a.N / 16;
+    muon_few_kernel<kind><<<kind == Kind::kNext ? dim3(n, m) : dim3(m * (m + 1) / 2), 512, 0, s>>>(a);
+    return hipGetLastError();
+  }
   return c.size == 64 ? launch_size<64, kind>(a, s) : c.size == 128 ? launch_size<128, kind>(a, s) : launch_size<256, kind>(a, s);
 }
 

@@ -78,6 +78,12 @@ def test_step(N, K):
     step(N, K)
 
 
+@pytest.mark.parametrize("N,K", [(128, 1000), (200, 2000), (2000, 200), (512, 512), (600, 700), (260, 1500)])
+def test_products_of_several_forms(N, K):
+    """Sizes at which one step's products take different forms."""
+    step(N, K, 6)
+
+
 @pytest.mark.parametrize("gdt", [torch.float32, torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("pad,off", [(0, 0), (3, 1), (8, 8)])
 @pytest.mark.parametrize("nesterov", [True, False])
