@@ -404,7 +404,7 @@ rb_status rb_qat_matmul(const void* X, rb_dtype a_dtype, int64_t M, int64_t ldx,
 
 /* rb_qat_backward -- from the forward's X, What and planes and the incoming dY:
  *   dW   output [N][lddw] fp32 (lddw >= K), the shared weight's gradient
- *   dX   output [M][lddx] (lddx >= K), dx_dtype RB_F32 or a_dtype; NULL: not computed
+ *   dX   output [M][lddx] (lddx >= K), dx_dtype RB_F32 or a_dtype
  *   dg   output [k][N] fp32;  dh  output [k][K] fp32 (fixed-order fp32 sums: deterministic for
  *        a given dW)
  *   ws   rb_workspace_bytes(RB_OP_QAT_BACKWARD, k, N, K, M) bytes, 16-byte aligned, for the
@@ -414,6 +414,13 @@ rb_status rb_qat_backward(const void* dY, rb_dtype a_dtype, int64_t M, int64_t l
                           const float* h, int32_t k, int64_t N, int64_t K, float* dW, int64_t lddw, void* dX,
                           rb_dtype dx_dtype, int64_t lddx, float* dg, float* dh, void* ws, size_t ws_bytes,
                           void* stream);
+
+/* rb_qat_backward_weights -- rb_qat_backward without dX, for layers that share their input (rb_qat_glu_dx gives a gated
+ * pair's); the other outputs are the same. */
+rb_status rb_qat_backward_weights(const void* dY, rb_dtype a_dtype, int64_t M, int64_t lddy, const void* X, int64_t ldx,
+                                  const void* What, int64_t ldwh, const uint32_t* planes, int64_t ldp, const float* g,
+                                  const float* h, int32_t k, int64_t N, int64_t K, float* dW, int64_t lddw, float* dg,
+                                  float* dh, void* ws, size_t ws_bytes, void* stream);
 
 /* rb_qat_autotune -- choose the GEMM kernels of the training layer for one shape: for each of
  * the three products of rb_qat_forward / rb_qat_backward with these sizes, leading dimensions
@@ -480,7 +487,7 @@ rb_status rb_qat_linear_backward(const void* dY, rb_dtype dy_dtype, int64_t M, i
  *     dG = dH (.) U (.) act'(G);  dU = dH (.) act(G)  (slopes as in rb_qat_linear_backward)
  *   and the biases' gradients, the column sums of the unrounded dG and dU in fp32, in a fixed order.
  *   dH       [M][lddh] in dh_dtype, RB_F32 or a_dtype;  G [M][ldg], U [M][ldu] in a_dtype
- *   dG, dU   outputs [M][lddg], [M][lddu] in a_dtype: what rb_qat_glu_dx and rb_qat_backward take. Each may be any one of
+ *   dG, dU   outputs [M][lddg], [M][lddu] in a_dtype: what rb_qat_glu_dx and rb_qat_backward_weights take. Each may be any one of
  *            dH, G and U (same type and leading dimension), but not the same one.
  *   dbg, dbu outputs fp32 [N], each may be NULL
  *   ws       rb_workspace_bytes(RB_OP_QAT_GLU_BACKWARD, 1, N, 1, M) bytes, 16-byte aligned (NULL if that is 0
@@ -491,7 +498,7 @@ rb_status rb_qat_linear_backward(const void* dY, rb_dtype dy_dtype, int64_t M, i
  *   dG [M][lddg], dU [M][lddu], Wg [N][ldwg], Wu [N][ldwu] in a_dtype, any alignment (fast: 16 bytes, leading
  *   dimensions, N and K multiples of 8);  dX [M][lddx] in dx_dtype, RB_F32 or a_dtype; it overlaps no input
  *   ws       rb_workspace_bytes(RB_OP_QAT_GLU_DX, 1, N, K, M) bytes as for rb_qat_glu
- *   The weights' gradients, dWg = dG^T X and dWu = dU^T X, with those of their scales: rb_qat_backward with dX NULL.
+ *   The weights' gradients, dWg = dG^T X and dWu = dU^T X, with those of their scales: rb_qat_backward_weights.
  * --------------------------------------------------------------------------------------- */
 rb_status rb_qat_glu(const void* X, rb_dtype a_dtype, int64_t M, int64_t ldx, const void* Wg, int64_t ldwg, const void* Wu,
                      int64_t ldwu, int64_t N, int64_t K, const float* bg, const float* bu, int32_t act, void* G,

@@ -344,11 +344,13 @@ def qat_backward(dY: torch.Tensor, X: torch.Tensor, What: torch.Tensor, planes: 
     dh = torch.empty((k, K), dtype=torch.float32, device=dev) if dh is None else dh
     if ws is None:
         ws = torch.empty(max(16, workspace_bytes(RB_OP_QAT_BACKWARD, k, N, K, M)), dtype=torch.uint8, device=dev)
-    check("rb_qat_backward", lib.rb_qat_backward(_ptr_rows(dY), _dt(dY.dtype), M, dY.stride(0), _ptr_rows(X), X.stride(0),
-                                                 _ptr_rows(What), What.stride(0), _ptr_rows(planes), planes.stride(1),
-                                                 _ptr(g), _ptr(h), k, N, K, _ptr_rows(dW), dW.stride(0), _ptr_rows(dX),
-                                                 _dt((X if dX is None else dX).dtype), 0 if dX is None else dX.stride(0),
-                                                 _ptr(dg), _ptr(dh), _ptr(ws), ws.numel(), _stream()))
+    layer = (_ptr_rows(dY), _dt(dY.dtype), M, dY.stride(0), _ptr_rows(X), X.stride(0), _ptr_rows(What), What.stride(0),
+             _ptr_rows(planes), planes.stride(1), _ptr(g), _ptr(h), k, N, K, _ptr_rows(dW), dW.stride(0))
+    rest = (_ptr(dg), _ptr(dh), _ptr(ws), ws.numel(), _stream())
+    if dX is None:
+        check("rb_qat_backward_weights", lib.rb_qat_backward_weights(*layer, *rest))
+    else:
+        check("rb_qat_backward", lib.rb_qat_backward(*layer, _ptr_rows(dX), _dt(dX.dtype), dX.stride(0), *rest))
     return dW, dX, dg, dh
 
 

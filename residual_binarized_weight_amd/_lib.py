@@ -65,6 +65,8 @@ SIGNATURES = {
     "rb_qat_backward": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
                                        _vp, _i32, _i64, _i64, _vp, _i64, _vp, ctypes.c_int, _i64, _vp, _vp,
                                        _vp, _sz, _vp]),
+    "rb_qat_backward_weights": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
+                                               _vp, _i32, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _sz, _vp]),
     "rb_qat_autotune": (ctypes.c_int, [_vp, _vp, ctypes.c_int, _i64, _i64, _i64, _vp, _i64, _i64, _i64, _vp,
                                        ctypes.c_int, _i64, _vp, _i64, _vp, ctypes.c_int, _i64, _vp]),
     "rb_qat_linear": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _vp, _i64, _i64, _i64, _vp, _i32, _vp, _i64, _vp,

@@ -395,11 +395,12 @@ rb_status rb_qat_forward(const float* W, int64_t N, int64_t K, int64_t ldw, int3
   return from_hip(rb::launch_qat_forward_gemm(X, a_dtype, M, ldx, What, ldwh, N, K, Y, y_dtype, ldy, s));
 }
 
-rb_status rb_qat_backward(const void* dY, rb_dtype a_dtype, int64_t M, int64_t lddy, const void* X, int64_t ldx,
-                          const void* What, int64_t ldwh, const uint32_t* planes, int64_t ldp, const float* g,
-                          const float* h, int32_t k, int64_t N, int64_t K, float* dW, int64_t lddw, void* dX,
-                          rb_dtype dx_dtype, int64_t lddx, float* dg, float* dh, void* ws, size_t ws_bytes,
-                          void* stream) {
+// dX: NULL for rb_qat_backward_weights
+static rb_status qat_backward(const char* name, const void* dY, rb_dtype a_dtype, int64_t M, int64_t lddy,
+                              const void* X, int64_t ldx, const void* What, int64_t ldwh, const uint32_t* planes,
+                              int64_t ldp, const float* g, const float* h, int32_t k, int64_t N, int64_t K, float* dW,
+                              int64_t lddw, void* dX, rb_dtype dx_dtype, int64_t lddx, float* dg, float* dh, void* ws,
+                              size_t ws_bytes, void* stream) {
   if (!dY || !X || !dW || !dg || !dh) return RB_ERR_INVALID_ARG;
   rb_status st = check_qat_layer(N, K, k, g, h, planes, ldp, What, ldwh, a_dtype);
   if (st != RB_OK) return st;
@@ -414,11 +415,29 @@ rb_status rb_qat_backward(const void* dY, rb_dtype a_dtype, int64_t M, int64_t l
   const size_t need = rb::zero_region_bytes(N) + rb::qat_backward_workspace_bytes(k, N, K);
   if (!ws || ws_bytes < need) return RB_ERR_WORKSPACE;
   if (!aligned(ws, 16)) return RB_ERR_MISALIGNED;
-  log_call("rb_qat_backward", N, K, M, k);
+  log_call(name, N, K, M, k);
   return from_hip(rb::launch_qat_backward(dY, a_dtype, M, lddy, X, ldx, What, ldwh, planes, ldp, g, h, k, N, K, dW,
                                           lddw, dX, dx_dtype, lddx, dg, dh,
                                           static_cast<char*>(ws) + rb::zero_region_bytes(N),
                                           static_cast<hipStream_t>(stream)));
+}
+
+rb_status rb_qat_backward(const void* dY, rb_dtype a_dtype, int64_t M, int64_t lddy, const void* X, int64_t ldx,
+                          const void* What, int64_t ldwh, const uint32_t* planes, int64_t ldp, const float* g,
+                          const float* h, int32_t k, int64_t N, int64_t K, float* dW, int64_t lddw, void* dX,
+                          rb_dtype dx_dtype, int64_t lddx, float* dg, float* dh, void* ws, size_t ws_bytes,
+                          void* stream) {
+  if (!dX) return RB_ERR_INVALID_ARG;
+  return qat_backward("rb_qat_backward", dY, a_dtype, M, lddy, X, ldx, What, ldwh, planes, ldp, g, h, k, N, K, dW,
+                      lddw, dX, dx_dtype, lddx, dg, dh, ws, ws_bytes, stream);
+}
+
+rb_status rb_qat_backward_weights(const void* dY, rb_dtype a_dtype, int64_t M, int64_t lddy, const void* X,
+                                  int64_t ldx, const void* What, int64_t ldwh, const uint32_t* planes, int64_t ldp,
+                                  const float* g, const float* h, int32_t k, int64_t N, int64_t K, float* dW,
+                                  int64_t lddw, float* dg, float* dh, void* ws, size_t ws_bytes, void* stream) {
+  return qat_backward("rb_qat_backward_weights", dY, a_dtype, M, lddy, X, ldx, What, ldwh, planes, ldp, g, h, k, N,
+                      K, dW, lddw, nullptr, a_dtype, 0, dg, dh, ws, ws_bytes, stream);
 }
 
 rb_status rb_qat_matmul(const void* X, rb_dtype a_dtype, int64_t M, int64_t ldx, const void* What, int64_t ldwh,

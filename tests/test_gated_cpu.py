@@ -274,6 +274,10 @@ def test_wrappers_refuse_host_tensors_and_wrong_shapes():
 def test_backward_without_dx_still_refuses():
     a = dict(dY=P, dt=BF16, M=4, lddy=16, X=P, ldx=64, What=P, ldwh=64, planes=P, ldp=2, g=P, h=P, k=2, N=16, K=64, dW=P, lddw=64,
              dX=None, xdt=BF16, lddx=0, dg=P, dh=P, ws=None, wsb=0)
-    assert L.rb_qat_backward(*a.values(), None) == WORKSPACE      # past the checks of dX
+    assert L.rb_qat_backward(*a.values(), None) == INVALID        # this one needs a dX
     a.update(dX=P)
-    assert L.rb_qat_backward(*a.values(), None) == INVALID        # a dX needs its leading dimension
+    assert L.rb_qat_backward(*a.values(), None) == INVALID        # and its leading dimension
+    w = {n: v for n, v in a.items() if n not in ("dX", "xdt", "lddx")}
+    assert L.rb_qat_backward_weights(*w.values(), None) == WORKSPACE
+    for bad in (dict(dY=None), dict(X=None), dict(dW=None), dict(dg=None), dict(dh=None), dict(M=0), dict(lddw=63)):
+        assert L.rb_qat_backward_weights(*{**w, **bad}.values(), None) == INVALID
