@@ -28,6 +28,8 @@ struct PackArgs {
   int32_t* status;
 };
 
+// Bound by HBM: the codes and scales are an eighth of what is read (4096 x 11008 fp32: 42 to 74 us traced; with the reading back
+// into bf16, 22 us, 71 for both). Lanes of a row are 16 apart, so a group's extremes take two exchanges.
 template <typename TW, int kGroup>
 __global__ __launch_bounds__(256) void q4_pack_kernel(PackArgs a) {
   const int lane = threadIdx.x & 63, r = lane & 15, j = lane >> 4;
