@@ -88,7 +88,7 @@ struct GluArgs {
 
 // Half of a tile's columns are G's and half U's, so that a wave holds both sums of an output and H costs no further pass.
 // Bound by the matrix cores at the card's power limit and by the tiles' ends, which nothing overlaps: 2048 x 4096 over
-// 2 x 11008 in bf16 325 us (1.14 PFLOP/s) for both products, G, U and H; the library's product alone takes 426.
+// 2 x 11008 in bf16 323 to 349 us (1.06 to 1.14 PFLOP/s) for both products, G, U and H; the library's product alone takes 426.
 template <typename T, typename TH, typename C>
 __global__ __launch_bounds__(C::kThreads, 2) void glu_tile_kernel(GluArgs<T> a) {
   extern __shared__ __align__(16) uint8_t t_smem[];

@@ -66,7 +66,7 @@ __device__ __forceinline__ void blend8(const MomentArgs& a, float s, int64_t row
   for (int j = 0; j < 8; ++j) u[j] = a.mom ? fmaf(a.mu, m[j], s * u[j]) : s * u[j];
 }
 
-// Bound by HBM; with muon_start_kernel's second reading of m it makes 11008 x 4096's beginning.
+// Bound by HBM at large sizes, by its launch at small ones (256 x 512: 3.4 to 4.3 us traced).
 template <typename TG>
 __global__ __launch_bounds__(256) void muon_moment_kernel(MomentArgs a) {
   __shared__ double sums[4];
@@ -106,7 +106,8 @@ __device__ __forceinline__ void split(float x, half_t& hi, half_t& lo) {
   lo = (half_t)(x - (float)hi);
 }
 
-// A block owns 64 x 64 of X; bound by HBM (11008 x 4096: 126 to 140 us traced). The norm is summed from the partial sums by every block (8 KB from the cache), in one order.
+// A block owns 64 x 64 of X; bound by HBM (11008 x 4096: 126 to 140 us traced). The norm is summed from the partial sums
+// by every block (8 KB from the cache), in one order.
 template <typename TG>
 __global__ __launch_bounds__(256) void muon_start_kernel(MomentArgs a) {
   __shared__ double sums[4];
@@ -158,7 +159,7 @@ __global__ __launch_bounds__(256) void muon_start_kernel(MomentArgs a) {
 // tiles take 1.86 us a step with rows across the sum, read through the transposing LDS reads, and 1.69 with rows along it).
 // A symmetric product computes the lower triangle's tiles and writes each twice, the second time turned.
 // 11008 x 4096, traced: A 176 to 188 us (+ 35 for the split tiles' join), B 95 to 103 (+ 7), X' 378 to 446, which reads and
-// writes 450 MB of X after its sums; the whole step of 5 iterations 4050 us (0.77 PFLOP/s), the matrix cores' share of the
+// writes 450 MB of X after its sums; the whole step of 5 iterations 4010 to 4128 us (0.75 to 0.78 PFLOP/s), the matrix cores' share of the
 // card's power being the largest bound.
 // ---------------------------------------------------------------------------------------------
 enum class Kind { kGram, kPoly, kNext };  // A = X X^T; B = b A + c A A; X' = a X + B X
@@ -315,7 +316,7 @@ __global__ __launch_bounds__(2 * join_cols<C>()) void muon_join_kernel(ProductAr
 // Small matrices, whose steps are as many launches as products: a block owns 16 x 16 outputs; its 8 waves take the 64-term
 // steps in turn, each with its fragments straight from memory, and join in LDS in their order. Launches and
 // latency bound it (a wave has the loads of up to four of its steps in flight at once): 256 x 512, medians traced, 3.8 us for
-// A, 3.6 for B and 4.3 for the next X against 5.9, 5.9 and 5.6 on tiles of 64; the whole step 64 us against 85. From
+// A, 3.6 for B and 4.3 for the next X against 5.9, 5.9 and 5.6 on tiles of 64; the whole step 64 to 68 us against 85 to 90. From
 // 512 x 512 on the tiles are as fast or faster. Every size is a multiple of 64 here.
 template <Kind kind>
 __global__ __launch_bounds__(512) void muon_few_kernel(ProductArgs a) {

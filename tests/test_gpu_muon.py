@@ -205,10 +205,12 @@ def test_equal_steps_give_equal_results_whatever_the_workspace_held():
         assert torch.equal(W, first[0]) and torch.equal(m, first[1])
 
 
-def test_captured_and_replayed_beside_another_stream():
+@pytest.mark.parametrize("N,K", [(200, 456), (1000, 1800)])
+def test_captured_and_replayed_beside_another_stream(N, K):
+    """In one launch a product, and on tiles with split ones joined."""
     r = np.random.default_rng(998)
-    G, W, m = mat(r, 200, 456), mat(r, 200, 456), mat(r, 200, 456)
-    other = mat(r, 456, 200)
+    G, W, m = mat(r, N, K), mat(r, N, K), mat(r, N, K)
+    other = mat(r, K, N)
     want_other = rb.orthogonalize(other)
     W2, m2 = W.clone(), m.clone()
     rb.muon_step(W.clone(), G, m.clone(), 0.1)
