@@ -83,7 +83,7 @@ struct GluArgs {
   Work work;
   float* part;
   GluOut out;
-  uint32_t first;  // of the rows' form: its first block of weight rows
+  uint32_t first;  // of the forms without tiles: the launch's first block of weight rows
 };
 
 // Half of a tile's columns are G's and half U's, so that a wave holds both sums of an output and H costs no further pass.
@@ -204,7 +204,7 @@ __global__ __launch_bounds__(512) void glu_few_kernel(GluArgs<T> a) {
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int lr = lane & 15, lj = lane >> 4;
-  const int n0 = blockIdx.x * 16;
+  const int n0 = (int)(a.first + blockIdx.x) * 16;
   const int64_t m0 = (int64_t)blockIdx.y * 16;
   // rows past the last one repeat it: their outputs are not stored
   const int64_t n = n0 + lr < a.N ? n0 + lr : a.N - 1;
@@ -459,8 +459,10 @@ hipError_t launch_glu_product(GluArgs<T> a, void* ws, hipStream_t s) {
   switch (small_form(a.M, a.N, q.R, al)) {
     case Small::kRows: return launch_glu_rows<T, TH>(a, s);
     case Small::kFew:
-      glu_few_kernel<T, TH><<<dim3((uint32_t)((a.N + 15) / 16), (uint32_t)((a.M + 15) / 16)), 512, 0, s>>>(a);
-      return hipGetLastError();
+      return launch_in_parts(((int64_t)a.N + 15) / 16, [&](int64_t first, uint32_t blocks) {
+        a.first = (uint32_t)first;
+        glu_few_kernel<T, TH><<<dim3(blocks, (uint32_t)((a.M + 15) / 16)), 512, 0, s>>>(a);
+      });
     case Small::kNone: break;
   }
   const Choice c = choose(a.M, a.N, 128, q.steps, al, false);

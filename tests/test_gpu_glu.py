@@ -18,7 +18,7 @@ import torch
 
 import residual_binarized_weight_amd as rb
 from oracle import block_oracle as BO
-from tests.gpu_util import dev
+from tests.gpu_util import dev, long_buffer, pieces
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs the GPU")]
@@ -435,3 +435,19 @@ def test_weight_gradients_without_an_input_gradient():
     torch.cuda.synchronize()
     assert part[1] is None
     assert all(torch.equal(a, b) for a, b in zip((full[0], *full[2:]), (part[0], *part[2:])))
+
+
+@pytest.mark.parametrize("M,K", [(5, 8), (16, 9), (12, 64)])
+def test_weight_rows_past_one_launch(M, K):
+    """2^27 weight rows and more in the one-launch form, 512 threads for every 16: past 2^32 threads. Every output is
+    written, sampled ones are right."""
+    N = (1 << 27) + 37
+    X, Wg, Wu = long_buffer(M, K, DT["bf16"]), long_buffer(N, K, DT["bf16"]), long_buffer(N, K, DT["bf16"])
+    bg, bu = long_buffer(1, N, torch.float32)[0], long_buffer(1, N, torch.float32)[0]
+    H, G, Uu = (long_buffer(M, N, DT["bf16"], float("nan")) for _ in range(3))
+    rb.qat_glu(X, Wg, Wu, bias_g=bg, bias_u=bu, H=H, G=G, U=Uu)
+    assert not any(bool(torch.isnan(t).any()) for t in (H, G, Uu))
+    for p in pieces(N):
+        check(X, Wg[p], Wu[p], bg[p], bu[p], "silu", H[:, p], G[:, p], Uu[:, p])
+    del Wg, Wu, H, G, Uu
+    torch.cuda.empty_cache()
