@@ -34,8 +34,9 @@ __device__ __forceinline__ f4 mfma(__bf16, u4 a, u4 b, f4 c) {
 // range check sees all of it. Two forms of the same instruction: the compiler takes the transposing reads of LDS for
 // dependent on every load to LDS in flight and has them wait for all of these (2048 x 4096 over 2 x 11008 in 411 us
 // with the builtin), so where those reads are used the load is written out. It has no register outputs; its LDS writes
-// are ordered by the kernel's own waits and barriers, as with the builtin. m0 has no other user in those kernels. The waits in front: one state from the
-// write of m0, five from a descriptor word that comes from a vector register.
+// are ordered by the kernel's own waits and barriers, as with the builtin. m0, where the LDS address goes, is an input of
+// the statement, so that the compiler writes it and knows that it did (in the list of clobbers it is refused, being
+// reserved). The waits in front: one state from the write of m0, five from a descriptor word that comes from a vector register.
 template <bool kWritten> struct Rows {  // a buffer resource over [base, base + bytes)
   __amdgpu_buffer_rsrc_t r;
   Rows() = default;
@@ -55,7 +56,7 @@ template <> struct Rows<true> {
   }
   __device__ __forceinline__ void load(uint8_t* to, uint32_t off) const {
     const uint32_t m0 = __builtin_amdgcn_readfirstlane((uint32_t)(size_t)(lds_void*)to);
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(m0), "v"(off), "s"(r) : "memory");
+    asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"{m0}"(m0), "v"(off), "s"(r) : "memory");
   }
 };
 

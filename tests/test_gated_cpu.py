@@ -2,6 +2,8 @@
 refusals of their C entry points, and their workspaces."""
 import ctypes
 import math
+import os
+import re
 
 import numpy as np
 import pytest
@@ -281,3 +283,12 @@ def test_backward_without_dx_still_refuses():
     assert L.rb_qat_backward_weights(*w.values(), None) == WORKSPACE
     for bad in (dict(dY=None), dict(X=None), dict(dW=None), dict(dg=None), dict(dh=None), dict(M=0), dict(lddw=63)):
         assert L.rb_qat_backward_weights(*{**w, **bad}.values(), None) == INVALID
+
+
+def test_inline_assembly_leaves_m0_to_the_compiler():
+    """m0 is no register that a statement can list as clobbered: one that needs it takes it as an input."""
+    src = os.path.join(os.path.dirname(rb.__file__), "csrc")
+    for name in sorted(os.listdir(src)):
+        with open(os.path.join(src, name)) as f:
+            text = f.read()
+        assert not re.search(r"\bs_\w+\s+m0\s*,", text), name
