@@ -9,7 +9,7 @@ One step, all of it in the library's kernels but for the loss and the clip facto
               S1 = S0 + norm(O), X1 = norm(S1)                                     resnorm_forward
   backward    the same in reverse          resnorm_backward, qat_backward, qat_glu_backward, qat_glu_dx
   update      the three weights            muon_step;  scales and norms at once    adamw_step
-  decode      the trained shared weights in 4 bits, one token   q4_pack, q4_glu, q4_gemv
+  decode      the effective weights, which the block was trained through, in 4 bits   q4_pack, q4_glu, q4_gemv
 
 Usage: python examples/gated_block.py [--tokens 512] [--width 1024] [--hidden 2752] [--planes 2] [--steps 40]
 """
@@ -76,8 +76,11 @@ class GatedBlock:
         rb.adamw_step(self.plan, self.steps, self.lr, beta2=0.99, grad_scale=scale, skip=skip)
 
     def pack(self, group: int = 64):
-        """The shared weights in 4 bits, for decode."""
-        self.packed = [rb.q4_pack(y.W, group=group) for y in self.layers]
+        """The weights that the forward multiplies by, in 4 bits, for decode: those of the shared weights and scales
+        as they are now."""
+        for y in self.layers:
+            y.derive()
+        self.packed = [rb.q4_pack(y.What, group=group) for y in self.layers]
         self.group = group
 
     def decode(self, emb):

@@ -129,3 +129,24 @@ def test_training_and_decoding_run():
     assert len(losses) == 5 and all(np.isfinite(losses))
     block.pack()
     assert bool(torch.isfinite(block.decode(block.emb[:1])).all())
+
+
+def test_decoding_uses_the_weights_that_were_trained():
+    """What is packed is the weights that the forward multiplies by, after the last update: each within half a step of
+    its group's scale (W / s is rounded once before it is rounded to a code: 8 u more)."""
+    T = example()
+    torch.manual_seed(4)
+    b = T.GatedBlock(96, 160, planes=2, seed=6, lr=1e-2)
+    emb = torch.randn((48, 96), device="cuda").to(torch.bfloat16)
+    b.forward(emb)
+    b.backward(torch.randn_like(emb))
+    b.update()
+    b.pack(group=32)
+    want = []
+    for y in b.layers:
+        y.derive()
+        want.append(y.What.float().clone())
+    for p, w in zip(b.packed, want):
+        got = rb.q4_dequant(*p, *w.shape, group=32, dtype=torch.float32)
+        s = p[1].float().t().repeat_interleave(32, 1)[:, :w.shape[1]]
+        assert bool(((got - w).abs() <= s * (0.5 + 8 * 2.0 ** -24)).all())
