@@ -636,7 +636,8 @@ rb_status rb_adamw_step(const void* plan, int64_t chunks, int32_t state_bits, in
  *   mom      [N][ldm] fp32, updated in place, or NULL (momentum and nesterov are then not used)
  *   O        output [N][ldo] in o_dtype, RB_F16 or RB_BF16, or NULL; one of W and O at least. No buffer overlaps another.
  *   N, K     1 .. 2^21 - 1; leading dimensions >= K, below 2^31
- *   lr, scale, weight_decay   finite and >= 0; 0 <= momentum < 1; eps finite and > 0 as an fp32; steps 1 .. 16
+ *   lr, scale, weight_decay   finite and >= 0, with lr scale and lr weight_decay within fp32; 0 <= momentum < 1;
+ *            eps finite and > 0 as an fp32; steps 1 .. 16
  *   grad_scale  s: optional device fp32;  skip  optional device int32: the step changes nothing if it is not 0
  *   ws       rb_workspace_bytes(RB_OP_MUON_STEP, 1, N, K, 1) bytes, 16-byte aligned; no zero-filling needed.
  *            (0 for sizes out of range.) Equal inputs give equal results.

@@ -730,7 +730,10 @@ rb_status rb_muon_step(float* W, int64_t ldw, const void* G, rb_dtype g_dtype, i
   const auto factor = [](double x) { return std::isfinite(x) && x >= 0.0; };
   if (!factor(lr) || !factor(weight_decay) || !factor(scale) || !(momentum >= 0.0 && momentum < 1.0))
     return RB_ERR_INVALID_ARG;
-  if (!std::isfinite(eps) || !(static_cast<float>(eps) > 0.f)) return RB_ERR_INVALID_ARG;
+  // as the kernels take them: an infinite rate would make a NaN of X = 0
+  const auto fits = [](double x) { return std::isfinite(static_cast<float>(x)); };
+  if (!fits(lr * scale) || !fits(1.0 - lr * weight_decay) || !fits(eps) || !(static_cast<float>(eps) > 0.f))
+    return RB_ERR_INVALID_ARG;
   if (!valid_dtype(g_dtype) || (O && !valid_dtype(o_dtype))) return RB_ERR_INVALID_ARG;
   if (O && !act_dtype(o_dtype)) return RB_ERR_UNSUPPORTED;
   if (!elem_aligned(G, g_dtype) || !aligned(W, 4) || !aligned(mom, 4) || (O && !elem_aligned(O, o_dtype)) ||

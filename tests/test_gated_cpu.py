@@ -292,3 +292,15 @@ def test_inline_assembly_leaves_m0_to_the_compiler():
         with open(os.path.join(src, name)) as f:
             text = f.read()
         assert not re.search(r"\bs_\w+\s+m0\s*,", text), name
+
+
+@pytest.mark.parametrize("kw", [dict(lr=1e30, scale=1e30), dict(lr=1e30, wd=1e30), dict(lr=1e200, scale=1e200),
+                                dict(lr=1e200, wd=1e200), dict(eps=1e39)])
+def test_muon_rejects_factors_past_fp32(kw):
+    """With no gradient X is 0 and W has to stay: an infinite rate times X would be NaN."""
+    assert _muon(**kw) == INVALID
+
+
+@pytest.mark.parametrize("kw", [dict(lr=1e30, scale=1e8), dict(lr=1e30, wd=1e8), dict(eps=3e38)])
+def test_muon_takes_factors_within_fp32(kw):
+    assert _muon(**kw, ws=None) == WORKSPACE  # the next check
