@@ -743,6 +743,8 @@ def _q4_words(N: int, K: int) -> int:
 
 def _q4(name: str, codes: torch.Tensor, s: torch.Tensor, z: torch.Tensor | None, N: int, K: int, group: int):
     """Pointers of one 4-bit weight, its shapes checked."""
+    if group not in (32, 64, 128):
+        raise ValueError("group must be 32, 64 or 128")
     if codes.dtype is not torch.int32 or codes.numel() != _q4_words(N, K):
         raise ValueError(f"{name}: codes are int32 [ceil(N / 16)][ceil(K / 128)][64][4]")
     for t in (s, z):

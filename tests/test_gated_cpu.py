@@ -304,3 +304,13 @@ def test_muon_rejects_factors_past_fp32(kw):
 @pytest.mark.parametrize("kw", [dict(lr=1e30, scale=1e8), dict(lr=1e30, wd=1e8), dict(eps=3e38)])
 def test_muon_takes_factors_within_fp32(kw):
     assert _muon(**kw, ws=None) == WORKSPACE  # the next check
+
+
+@pytest.mark.parametrize("group", [0, -32, 48, 256])
+def test_q4_wrappers_refuse_other_groups(group):
+    w = (torch.zeros((1, 1, 64, 4), dtype=torch.int32), torch.zeros((1, 16), dtype=torch.float16), None)
+    x = torch.zeros((1, 128), dtype=torch.float16)
+    for call in (lambda: rb.q4_gemv(*w, x, 16, group=group), lambda: rb.q4_glu(w, w, x, 16, group=group),
+                 lambda: rb.q4_dequant(*w, 16, 128, group=group), lambda: rb.q4_pack(x, group=group)):
+        with pytest.raises(ValueError, match="group"):
+            call()
