@@ -663,14 +663,16 @@ rb_status rb_muon_step(float* W, int64_t ldw, const void* G, rb_dtype g_dtype, i
  *   over the group (W / s is taken as 0 where s is 0). d_status: optional device int32; the call ORs 1 into it if W
  *   holds a NaN or an infinity or a scale overflows (outputs of that group are then unspecified).
  *
- * rb_q4_dequant -- What [N][ldw] in w_dtype: s (q - 8) or s q + z, rounded once. What rb_qat_linear and rb_qat_glu take
- *   for larger batches.
+ * rb_q4_dequant -- What [N][ldw] in w_dtype: s (q - 8), exact in fp32, or s q + z, rounded to fp32 first; then rounded
+ *   to w_dtype. What rb_qat_linear and rb_qat_glu take for larger batches.
  *
  * rb_q4_gemv -- y [M][ldy] = x What^T for x [M][ldx] in x_dtype (RB_F16 or RB_BF16, any alignment), 1 <= M <= 16 (larger:
  *   RB_ERR_UNSUPPORTED), fp32 sums, y in y_dtype, RB_F32 or x_dtype. x must be finite: an infinity gives NaN in its row.
  * rb_q4_glu -- y = act(x Wg^T) (.) (x Wu^T) in one launch, both weights N x K with one group size; each with or
  *   without offsets.
- *   The calls need no workspace; sums are in a fixed order (deterministic).
+ *   The calls need no workspace; sums are in an order that M, N and K fix (deterministic: equal calls give equal bits). It
+ *   is not the same for every M: above 4096 weight rows a row's result may differ by fp32 rounding between batches of up
+ *   to 4 rows and of more.
  * --------------------------------------------------------------------------------------- */
 size_t rb_q4_codes_bytes(int64_t N, int64_t K); /* 0 for sizes out of range */
 rb_status rb_q4_pack(const void* W, rb_dtype w_dtype, int64_t N, int64_t K, int64_t ldw, int32_t group, uint32_t* codes,

@@ -249,3 +249,113 @@ def test_captured_and_replayed():
         want = go()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+# ------------------------------------------------------------------------------------------------
+# every form of the product: 1, 4 and 16 rows, blocks of 16 waves and (above 4096 weight rows, up to 4 rows) of 8, and
+# columns in one or several chunks of the loop
+# ------------------------------------------------------------------------------------------------
+def device_weight(gen, N, K, group, offset):
+    """Codes [N][K], and (codes, s, z) as the library takes them, made on the device."""
+    q = torch.randint(0, 16, (N, K), generator=gen, device=dev())
+    tn, tk = -(-N // 16), -(-K // 128)
+    full = torch.zeros((tn * 16, tk * 128), dtype=torch.int64, device=dev())
+    full[:N, :K] = q
+    t = full.view(tn, 16, tk, 4, 4, 4, 2).permute(0, 2, 4, 1, 3, 6, 5)  # tiles, lane / 16, row, word, column % 2, column / 2
+    w = (t << (4 * torch.arange(8, device=dev()).view(2, 4))).sum((-1, -2))
+    g = -(-K // group)
+    s = (torch.rand((g, N), generator=gen, device=dev()) * 0.8 + 0.2).mul_(0.01).half()
+    z = torch.randn((g, N), generator=gen, device=dev()).mul_(0.05).half() if offset else None
+    return q, (torch.where(w >= 1 << 31, w - (1 << 32), w).to(torch.int32).reshape(tn, tk, 64, 4).contiguous(), s, z)
+
+
+def some_rows(N):
+    return np.unique(np.clip(np.r_[0:20, N // 2:N // 2 + 20, 4080:4120, N - 20:N], 0, N - 1))
+
+
+def of_rows(q, w, at):
+    """Codes, s and z of some weight rows, on the host."""
+    i = torch.from_numpy(at).to(dev())
+    return q[i].cpu().numpy(), *(None if t is None else t[:, i].cpu().numpy() for t in w[1:])
+
+
+def form_case(M, N, K, group, offset, dt, pair, act="silu", ydt="f32"):
+    gen = torch.Generator(device=dev())
+    gen.manual_seed(M * 1000003 + N * 1009 + K)
+    x = rows(np.random.default_rng([1050, M, K]).standard_normal((M, K)), dt)
+    ws = [device_weight(gen, N, K, group, o) for o in ((offset, not offset) if pair else (offset,))]
+    y = torch.full((M, N), float("nan"), dtype=DT[ydt], device=dev())
+    if pair:
+        rb.q4_glu(ws[0][1], ws[1][1], x, N, group=group, act=act, y=y)
+    else:
+        rb.q4_gemv(*ws[0][1], x, N, group=group, y=y)
+    torch.cuda.synchronize()
+    assert not torch.isnan(y).any()
+    at, xs = some_rows(N), n64(x)
+    got = y[:, torch.from_numpy(at).to(dev())]
+    host = [of_rows(*w, at) for w in ws]
+    G = [xs @ BO.q4_values(*h, group).T for h in host]
+    L = [product_bound(xs, h[1], h[2], group, K) for h in host]
+    if not pair:
+        near(got, G[0], L[0], "y")
+        return
+    a = BO.activation(G[0], act)[0]
+    la = 1.13 * L[0] + 16 * U * (np.abs(G[0]) + np.abs(a))
+    near(got, a * G[1], la * (np.abs(G[1]) + L[1]) + np.abs(a) * L[1] + 2 * U * np.abs(a * G[1]), "y")
+
+
+def test_device_codes_are_the_oracles():
+    gen = torch.Generator(device=dev())
+    gen.manual_seed(1)
+    q, (codes, _, _) = device_weight(gen, 37, 300, 64, False)
+    assert np.array_equal(codes.cpu().numpy().view(np.uint32), BO.q4_codes(q.cpu().numpy()))
+
+
+@pytest.mark.parametrize("pair", [False, True])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("M", [1, 3, 4, 11, 16])
+def test_every_form(M, dt, group, pair):
+    for N in (70, 4096, 4100):
+        form_case(M, N, 515, group, N == 70, dt, pair, ydt="f32" if N != 4100 else dt)
+
+
+# a chunk holds 12288 columns (16 waves) or 8192 (8), of the pair 6144 or 4096: its end, one tile more, two and several
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("M", [1, 2, 4])
+@pytest.mark.parametrize("N,K", [(50, 12288), (50, 12289), (50, 12416), (50, 28672), (4100, 8192), (4100, 8200), (4100, 8320),
+                                 (4100, 16511)])
+def test_columns_in_several_chunks(N, K, M, group):
+    form_case(M, N, K, group, M == 1, "bf16" if K % 2 else "f16", False)
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("M", [1, 2, 4])
+@pytest.mark.parametrize("N,K", [(50, 6144), (50, 6145), (50, 6272), (50, 13824), (4100, 4096), (4100, 4104), (4100, 5120),
+                                 (4100, 8319)])
+def test_columns_of_a_pair_in_several_chunks(N, K, M, group):
+    form_case(M, N, K, group, M == 1, "bf16" if K % 2 else "f16", True)
+
+
+@pytest.mark.parametrize("pair", [False, True])
+def test_rows_across_batch_sizes(pair):
+    """Above 4096 weight rows the sums of up to 4 rows are split over 8 waves, those of more over 16: equal within both
+    sums' bounds. The same call gives the same bits."""
+    N, K, group = 4100, 5000, 64
+    gen = torch.Generator(device=dev())
+    gen.manual_seed(3)
+    ws = [device_weight(gen, N, K, group, True) for _ in range(2)]
+    x = rows(np.random.default_rng(1060).standard_normal((16, K)), "f16")
+    call = lambda t: (rb.q4_glu(ws[0][1], ws[1][1], t, N, group=group, act="none", y_dtype=torch.float32) if pair else  # noqa: E731
+                      rb.q4_gemv(*ws[0][1], t, N, group=group, y_dtype=torch.float32))
+    at = some_rows(N)
+    i, xs = torch.from_numpy(at).to(dev()), n64(x)
+    host = [of_rows(*w, at) for w in ws]
+    V, L = ([f(h) for h in host] for f in (lambda h: xs @ BO.q4_values(*h, group).T, lambda h: product_bound(xs, h[1], h[2], group, K)))
+    lim = 2 * (L[0] * (np.abs(V[1]) + L[1]) + np.abs(V[0]) * L[1] + 2 * U * np.abs(V[0] * V[1])) if pair else 2 * L[0]
+    full = call(x)
+    for m in (1, 2, 4, 7):
+        got, again = call(x[:m]), call(x[:m])
+        torch.cuda.synchronize()
+        assert torch.equal(got, again)
+        assert np.all(np.abs(n64(got[:, i]) - n64(full[:m, i])) <= lim[:m])
