@@ -229,3 +229,42 @@ def test_captured_and_replayed_beside_another_stream(N, K):
         rb.muon_step(W2, G, m2, 0.1)
         torch.cuda.synchronize()
         assert torch.equal(W, W2) and torch.equal(m, m2) and torch.equal(got, want_other), k
+
+
+def columns_near(O, G, axis):
+    """O against the products in 64 bits, vector by vector along the long axis: the file's bound for few rows counts every
+    rounding at its largest, relative to the vector that it falls on, so that it holds for each of them."""
+    X = G.double()
+    X = X / (X.norm() + 1e-7)
+    a, b, c = BO.NS_COEFFICIENTS
+    X = X.t() if axis == 0 else X
+    for _ in range(5):
+        A = X @ X.t().contiguous()
+        X = a * X + (b * A + c * (A @ A)) @ X
+    got = (O.t() if axis == 0 else O).double()
+    err, size = (got - X).norm(dim=0), X.norm(dim=0)
+    n = X.shape[0]
+    assert bool((err <= (bound(*G.shape) + 2.0 ** -11) * size + 2.0 ** -25 * n ** 0.5).all()), f"{float((err / size).max()):.3g}"
+    assert float(X.norm()) > 0.6  # its singular values end near 1
+
+
+@pytest.mark.parametrize("n", [1, 3, 7])
+@pytest.mark.parametrize("tall", [False, True])
+def test_every_vector_of_long_and_thin_ones(n, tall):
+    """Up to the largest length, 2^21 - 1: every column (row) against the definition."""
+    m = (1 << 21) - 1
+    gen = torch.Generator(device=dev())
+    gen.manual_seed(n)
+    G = torch.randn((m, n) if tall else (n, m), generator=gen, device=dev())
+    O = rb.orthogonalize(G, o_dtype=torch.float16)
+    torch.cuda.synchronize()
+    columns_near(O, G, 0 if tall else 1)
+
+
+def test_a_square_matrix_and_its_transpose():
+    """Both results are within the bound of one X."""
+    G = mat(np.random.default_rng(999), 1500, 1500)
+    O, T = (rb.orthogonalize(t, o_dtype=torch.float16) for t in (G, G.t().contiguous()))
+    torch.cuda.synchronize()
+    size = float(O.double().norm())
+    assert float((T.double() - O.t().double()).norm()) <= 2 * (4e-3 + 2.0 ** -11) * size * (1 + 5e-3)
