@@ -150,3 +150,33 @@ def test_decoding_uses_the_weights_that_were_trained():
         got = rb.q4_dequant(*p, *w.shape, group=32, dtype=torch.float32)
         s = p[1].float().t().repeat_interleave(32, 1)[:, :w.shape[1]]
         assert bool(((got - w).abs() <= s * (0.5 + 8 * 2.0 ** -24)).all())
+
+
+@pytest.mark.parametrize("along", ["dX", "gate", "up"])
+def test_input_gradient_against_differences(along):
+    """The forward, in fp32 outputs, with X moved by D and by -D: along the whole gradient, and along each of its two terms,
+    so that <dX, D> is a sum of terms of one sign. The moved X are rounded to fp16, and D is half of what then lies between
+    them. What the difference and <dX, D> are apart by, of the whole: the rest of third order, e^2 / 6 = 2^-10 / 6 times a third
+    derivative of the same order as the first (a part in a thousand); G, U, dG and dU rounded to fp16, 2^-11 each, over sums
+    of absolute terms up to a few times the whole (under one percent); the middle of the moved X, 2^-12 of X off (less than
+    that). So three percent; a dX without either term, or of the other sign, is off by about half or more."""
+    torch.manual_seed(1)
+    M, N, K = 64, 96, 80
+    X, Wg, Wu = (torch.randn(s, device="cuda").half() for s in ((M, K), (N, K), (N, K)))
+    Wg, Wu = Wg * 0.1, Wu * 0.1
+    dH = torch.randn((M, N), device="cuda")
+    H, G, U = rb.qat_glu(X, Wg, Wu, h_dtype=torch.float32, save=True)
+    dG, dU, _, _ = rb.qat_glu_backward(dH, G, U)
+    dX = rb.qat_glu_dx(dG, dU, Wg, Wu, dx_dtype=torch.float32).double()
+    gate, up = dG.double() @ Wg.double(), dU.double() @ Wu.double()
+    D = {"dX": gate + up, "gate": gate, "up": up}[along]
+    D = D / D.square().mean().sqrt() * 2.0 ** -5
+    hi, lo = ((X.double() + s * D).half() for s in (1, -1))
+    D = (hi.double() - lo.double()) / 2
+    Hh, Hl = (rb.qat_glu(t, Wg, Wu, h_dtype=torch.float32)[0].double() for t in (hi, lo))
+    torch.cuda.synchronize()
+    want = float(((Hh - Hl) * dH.double()).sum() / 2)
+    off = lambda d: abs(float((d * D).sum()) - want) / abs(want)  # noqa: E731
+    assert off(dX) <= 0.03
+    wrong = {"dX": (dX - gate, dX - up, -dX), "gate": (dX - gate, -dX), "up": (dX - up, -dX)}[along]
+    assert all(off(d) > 0.25 for d in wrong)
