@@ -708,7 +708,7 @@ def muon_step(W: torch.Tensor | None, G: torch.Tensor, mom: torch.Tensor | None,
     """One step of the matrix W [N][K] (fp32, in place) from its gradient G (fp32, fp16 or bf16): the momentum `mom`
     (fp32, in place) takes grad_scale G in, the update's singular values are brought near 1 by `steps` Newton-Schulz
     products, and W <- W (1 - lr weight_decay) - lr scale X. `scale` defaults to 0.2 sqrt(max(N, K)), which gives the
-    update AdamW's size. `grad_scale` (device fp32) and `skip` (device int32) as in adamw_step. O [N][K] (fp16 or
+    update AdamW's size (J. Liu and others, "Muon is scalable for LLM training", 2025). `grad_scale` (device fp32) and `skip` (device int32) as in adamw_step. O [N][K] (fp16 or
     bf16) receives X; W may be None where O is given. Rows may be strided."""
     N, K = G.shape
     if grad_scale is not None and grad_scale.dtype != torch.float32:

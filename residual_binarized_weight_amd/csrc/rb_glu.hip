@@ -89,6 +89,7 @@ struct GluArgs {
 // Half of a tile's columns are G's and half U's, so that a wave holds both sums of an output and H costs no further pass.
 // Bound by the matrix cores at the card's power limit and by the tiles' ends, which nothing overlaps: 2048 x 4096 over
 // 2 x 11008 in bf16 323 to 349 us (1.06 to 1.14 PFLOP/s) for both products, G, U and H; the library's product alone takes 426.
+// The 256-row tiles' registers are full: one vector register goes to scratch, 57 scalar ones to lanes of vector registers.
 template <typename T, typename TH, typename C>
 __global__ __launch_bounds__(C::kThreads, 2) void glu_tile_kernel(GluArgs<T> a) {
   extern __shared__ __align__(16) uint8_t t_smem[];
@@ -134,7 +135,8 @@ __global__ __launch_bounds__(256) void glu_join_kernel(GluArgs<T> a) {
 
 // Up to 4 batch rows: HBM's rate for the weights is the bound, and the vector units' products are far below it. A
 // wave owns a row of each weight, its lanes 8 columns each of a 512-column step; kSteps loads of 1 KB from each row
-// are in flight. One launch, no partial sums in memory. One row of 4096 over 2 x 11008 in fp16: 31.5 us, 5.7 TB/s.
+// are in flight. One launch, no partial sums in memory. One row of 4096 over 2 x 11008 in fp16: 31.5 us, 5.7 TB/s. Two to
+// four rows take one form, which does four rows' work (absent ones repeat the first): 39, 40 and 41 us in bf16.
 constexpr int kMaxRows = 4;
 
 template <typename T, typename TH, int MR, int kSteps>
@@ -255,7 +257,10 @@ __global__ __launch_bounds__(512) void glu_few_kernel(GluArgs<T> a) {
 // waves take in turn; each thread keeps its columns' sums in fp32. HBM bounds it.
 // ---------------------------------------------------------------------------------------------
 // A block walks down a strip of rows, 8 columns a thread, and keeps the column sums in registers; bound by HBM (2048 x
-// 11008 bf16, 225 MB: 51 us from warm caches, 78 from flushed ones, traced). Sums are joined in a fixed order.
+// 11008 bf16, 225 MB: 51 us from warm caches, 78 from flushed ones, traced). Sums are joined in a fixed order. Its stores
+// are streamed whatever the rows' alignment: a wave writes 1 KB of a row at once, so that few lines are written in two
+// parts (odd rows in bf16, us, streamed / only where rows start lines: 2048 x 11007 64 / 68, 2048 x 4095 24 / 26, 512 x 4095
+// 7.3 / 8.3, 4096 x 1411 19 / 21).
 struct GluGradArgs {
   const void *dH, *G, *U;
   void *dG, *dU;
@@ -342,7 +347,8 @@ struct DxArgs {
 };
 // dG and dU, and Wg and Wu, follow each other along the sum, so that dX is written once and no product waits for the other;
 // the weights' rows lie across the sum and are turned by the transposing LDS reads. 2048 x 4096 over 2 x 11008 bf16: 300 to
-// 324 us traced (1.14 to 1.23 PFLOP/s); the library's product of that shape takes 452.
+// 324 us traced (1.14 to 1.23 PFLOP/s); the library's product of that shape takes 452. The 256-row tiles keep 8 vector
+// registers in scratch. Up to 64 rows of it take 42 to 45 us, the weights' 35 at a copy's rate being the floor.
 template <typename T, typename TX, typename C>
 __global__ __launch_bounds__(C::kThreads, 2) void glu_dx_kernel(DxArgs<T> a) {
   extern __shared__ __align__(16) uint8_t t_smem[];
@@ -441,7 +447,9 @@ hipError_t launch_glu_rows(GluArgs<T> a, hipStream_t s) {
 // the weights. The one-launch form on the matrix cores is taken by its estimate against the tiles', up to the 256 rows
 // that the estimate holds for (us, one launch / tiles: 5 x 1000 x 1000 4.1 / 12.5, 16 x 2048 x 2048 8.5 / 15.3, 64 x 1408 x
 // 1024 8.6 / 13.3, 64 x 2048 x 2048 14.2 / 17.4, 64 x 4096 x 4096 53 / 27, 256 x 512 x 512 5.6 / 10.8; rows not aligned: 5 x
-// 1000 x 1001 7.3 / 15.7, 61 x 1411 x 1027 14.2 / 17.0, 16 x 2047 x 2047 21.4 / 19.4, 128 x 1023 x 1023 21.7 / 17.2).
+// 1000 x 1001 7.3 / 15.7, 61 x 1411 x 1027 14.2 / 17.0, 16 x 2047 x 2047 21.4 / 19.4, 128 x 1023 x 1023 21.7 / 17.2). Neither
+// estimate has a term for memory's rate, which is the floor where weights are large: 5 to 64 rows of 4096 over 2 x 11008 take
+// 49 to 53 us against the 35 that the weights need.
 enum class Small { kNone, kRows, kFew };
 Small small_form(int64_t M, int64_t N, int64_t K, bool aligned) {
   if (K < 8 || M > kFewRows) return Small::kNone;

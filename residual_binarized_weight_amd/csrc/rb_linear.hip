@@ -660,7 +660,7 @@ hipError_t launch_product(TileArgs a, void* ws, hipStream_t s) {
   const bool al = tile_aligned(a.X, a.ldx, a.W, a.ldw, a.K);
   switch (small_form(a.M, a.N, a.K, al)) {
     case Small::kRows: return launch_rows<TA, TY>(a, s);
-    case Small::kFew:
+    case Small::kFew:  // its estimate passes the tiles' long before N is 2^27 and the grid 2^32 threads
       linear_few_kernel<TA, TY><<<dim3((uint32_t)((a.N + 15) / 16), (uint32_t)((a.M + 15) / 16)), 512, 0, s>>>(a);
       return hipGetLastError();
     case Small::kNone: break;

@@ -2,6 +2,8 @@
 //
 //   m <- mu m + s g;  u = s g + mu m (nesterov) or m;  X = u / (|u|_F + eps), as its transpose where it is tall
 //   X <- a X + (b A + c A^2) X,  A = X X^T      a few times: the singular values go towards 1
+//   (a, b, c) are those published with the method: K. Jordan and others, "Muon: an optimizer for hidden layers in
+//   neural networks", 2024
 //   W <- W (1 - lr wd) - lr scale X
 //
 // With n = min(N, K) and m = max(N, K) an iteration is three products: A (symmetric, n x n over m), the polynomial
@@ -159,8 +161,9 @@ __global__ __launch_bounds__(256) void muon_start_kernel(MomentArgs a) {
 // tiles take 1.86 us a step with rows across the sum, read through the transposing LDS reads, and 1.69 with rows along it).
 // A symmetric product computes the lower triangle's tiles and writes each twice, the second time turned.
 // 11008 x 4096, traced: A 176 to 188 us (+ 35 for the split tiles' join), B 95 to 103 (+ 7), X' 378 to 446, which reads and
-// writes 450 MB of X after its sums; the whole step of 5 iterations 4010 to 4128 us (0.75 to 0.78 PFLOP/s), the matrix cores' share of the
-// card's power being the largest bound.
+// writes 450 MB of X after its sums; the whole step of 5 iterations 4010 to 4128 us (0.75 to 0.78 PFLOP/s). The same tiles reach 1.06 to
+// 1.23 PFLOP/s in the gated products; here A makes 0.82 to 0.88 with its join, B on 128-square tiles 0.62 to 0.67, X' 0.83 to
+// 0.98, with nothing over its reads and writes.
 // ---------------------------------------------------------------------------------------------
 enum class Kind { kGram, kPoly, kNext };  // A = X X^T; B = b A + c A A; X' = a X + B X
 

@@ -42,7 +42,12 @@ __device__ __forceinline__ u2 scales4(const _Float16* s, int64_t n, int64_t N) {
 // The columns are taken in chunks of kWaves kSteps tiles. x and the scales of a chunk go to LDS (the scales as fp32 s and
 // z - 16 s or -24 s); a wave's codes of a chunk, kSteps loads of 1 KB from each weight, are all in flight at once,
 // behind them (a wave's loads return in order). Up to kM batch rows. With 16 of them LDS holds a short chunk only, and
-// the next one's loads are in flight while a chunk is multiplied. Bound by the launch's ramp and one trip to memory:
+// the next one's loads are in flight while a chunk is multiplied (with groups of 32, and of 64 but for the pair, 2 to 4
+// registers go to scratch for that). Up to 4 rows a chunk is as long as the registers for its codes allow: 12288
+// columns for 16 waves and 8192 for 8, of a pair 6144 and 4096; the next one's loads start when a chunk is multiplied, so
+// that its first tile costs another trip to memory (us, one row, group 128, weights cold, a chunk's end / a tile more:
+// 4096 x 12288 9.3 / 10.3, 8192 x 8192 9.8 / 11.2, the pair of 4096 x 6144 8.9 / 9.7 and of 11008 x 4096 12.6 / 14.0; several
+// chunks: 8192 x 28672 28.0, 4.3 TB/s, the pair of 28672 x 8192 50.2, 4.8). Bound by the launch's ramp and one trip to memory:
 // 4096 x 11008, group 128, 23 MB: 7.6 us cold among other calls (3.1 TB/s); 16 rows, group 32 with offsets 18 us: four
 // times the groups, whose staging and sums were not timed apart.
 template <typename T, int kGroup, bool kPair, int kM, int kWaves>
@@ -235,7 +240,11 @@ hipError_t launch_one(Args a, hipStream_t s) {
   });
 }
 // A unit holds 16 waves of these: one block of 16, or two of 8 where there are more blocks than units, which then begin and
-// end at different times (us, 16 waves / 8: 4096 x 11008 7.9 / 10.1, the pair of 11008 x 4096 14.8 / 10.9).
+// end at different times (us, 16 waves / 8: 4096 x 11008 7.9 / 10.1, the pair of 11008 x 4096 14.8 / 10.9). Of 2 to 4
+// rows in groups of 32 and 64, not the pair, the 96 and 80 KB of LDS leave room for one block of 8; neither side
+// wins there (4 rows, group 32: 11008 x 4096 15.3 / 14.2, 13824 x 5120 21.3 / 22.1, 28672 x 8192 51.3 / 49.1; group 64: 13.5 / 12.6,
+// 18.5 / 19.9, 42.3 / 43.4; in chunks of 6144 columns, of which two blocks fit, 8 waves take 13.5, 20.0, 49.7 and 12.4,
+// 18.4, 46.0), so the rule is the same.
 template <typename T, int kGroup, bool kPair, int kM>
 hipError_t launch_waves(const Args& a, hipStream_t s) {
   return (a.N + kTileN - 1) / kTileN <= tile::kUnits ? launch_one<T, kGroup, kPair, kM, 16>(a, s)
