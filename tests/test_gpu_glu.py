@@ -451,3 +451,59 @@ def test_weight_rows_past_one_launch(M, K):
         check(X, Wg[p], Wu[p], bg[p], bu[p], "silu", H[:, p], G[:, p], Uu[:, p])
     del Wg, Wu, H, G, Uu
     torch.cuda.empty_cache()
+
+
+def test_many_batch_rows():
+    """2^24 batch rows and more, each direction: tiles along the batch, strips of many rows."""
+    M, N, K = (1 << 24) + 77, 24, 16
+    X, Wg, Wu = long_buffer(M, K, DT["bf16"]), long_buffer(N, K, DT["bf16"]), long_buffer(N, K, DT["bf16"])
+    H, G, Uu = (long_buffer(M, N, DT["bf16"], float("nan")) for _ in range(3))
+    rb.qat_glu(X, Wg, Wu, H=H, G=G, U=Uu)
+    assert not any(bool(torch.isnan(t).any()) for t in (H, G, Uu))
+    for p in pieces(M):
+        check(X[p], Wg, Wu, None, None, "silu", H[p], G[p], Uu[p])
+    dH = long_buffer(M, N, DT["bf16"])
+    dG, dU, _, _ = rb.qat_glu_backward(dH, G, Uu)
+    for p in pieces(M):
+        check_grad(dH[p], G[p], Uu[p], "silu", dG[p], dU[p], None, None)
+    # sums of M equal terms: 1024 strips, a thread's run of 4097 rows of one, their 1024 sums in 8 runs; a strip's part is 2^-10
+    one = torch.ones((M, N), dtype=torch.bfloat16, device=dev())
+    _, _, dbg, dbu = rb.qat_glu_backward(one, one, one, bias=True)
+    g = 1 / (1 + np.exp(-1.0))
+    for got, each in ((dbg, g + g * (1 - g)), (dbu, g)):
+        near(got, np.full(N, M * each), (4097 + 3 + 128 + 8 + 24 * 2) * U * M * each, "column sums")
+    del one
+    dX = rb.qat_glu_dx(dG, dU, Wg, Wu)
+    for p in pieces(M):
+        check_dx(dG[p], dU[p], Wg, Wu, dX[p])
+    del X, H, G, Uu, dH, dG, dU, dX
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("M", [3, 40, 300])
+def test_rows_far_apart(M):
+    """Leading dimensions of 2^21 and more, aligned: past what a tile's buffer loads reach."""
+    N, K, ld = 130, 200, (1 << 21) + 8
+    X, Wg, Wu, dG, dU = (long_buffer(n, ld, DT["f16"])[:, :k] for n, k in ((M, K), (N, K), (N, K), (M, N), (M, N)))
+    H, G, Uu = rb.qat_glu(X, Wg, Wu, act="gelu", h_dtype=torch.float32, save=True)
+    dX = rb.qat_glu_dx(dG, dU, Wg, Wu, dx_dtype=torch.float32)
+    torch.cuda.synchronize()
+    check(X, Wg, Wu, None, None, "gelu", H, G, Uu)
+    check_dx(dG, dU, Wg, Wu, dX)
+    del X, Wg, Wu, dG, dU
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("M,K", [(3, (1 << 24) + 5), (70, (1 << 21) + 8), (300, 1 << 21)])
+def test_dx_of_many_columns(M, K):
+    """dX of 2^21 columns and more, where its weights' rows are past the aligned tiles' reach."""
+    N = 24
+    dG, dU = long_buffer(M, N, DT["bf16"]), long_buffer(M, N, DT["bf16"])
+    Wg, Wu = long_buffer(N, K, DT["bf16"]), long_buffer(N, K, DT["bf16"])
+    dX = long_buffer(M, K, DT["bf16"], float("nan"))
+    rb.qat_glu_dx(dG, dU, Wg, Wu, dX=dX)
+    assert not torch.isnan(dX).any()
+    for p in pieces(K):
+        check_dx(dG, dU, Wg[:, p], Wu[:, p], dX[:, p])
+    del Wg, Wu, dX
+    torch.cuda.empty_cache()

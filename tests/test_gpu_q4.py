@@ -359,3 +359,41 @@ def test_rows_across_batch_sizes(pair):
         torch.cuda.synchronize()
         assert torch.equal(got, again)
         assert np.all(np.abs(n64(got[:, i]) - n64(full[:m, i])) <= lim[:m])
+
+
+@pytest.mark.parametrize("pair", [False, True])
+@pytest.mark.parametrize("M", [1, 3, 16])
+def test_weight_rows_past_one_part(M, pair):
+    """More than 2^20 blocks of 16 weight rows: launched in parts. Every output is written, sampled ones are right."""
+    N, K, group = (1 << 24) + 137, 96, 32
+    gen = torch.Generator(device=dev())
+    gen.manual_seed(M)
+    ws = []
+    for _ in range(1 + pair):
+        codes = torch.randint(-(1 << 31), (1 << 31) - 1, (-(-N // 16), 1, 64, 4), dtype=torch.int32, generator=gen, device=dev())
+        codes[..., 3] = 0  # columns 96 to 127
+        codes.view(-1, 4, 16, 4)[-1, :, N % 16:] = 0  # rows past the last
+        ws.append((codes, (torch.rand((3, N), generator=gen, device=dev()) * 0.01).half(), torch.randn((3, N), generator=gen, device=dev()).mul_(0.05).half()))
+    x = rows(np.random.default_rng(1070).standard_normal((M, K)), "f16")
+    y = torch.full((M, N), float("nan"), dtype=torch.float32, device=dev())
+    if pair:
+        rb.q4_glu(*ws, x, N, group=group, act="none", y=y)
+    else:
+        rb.q4_gemv(*ws[0], x, N, group=group, y=y)
+    assert not torch.isnan(y).any()
+    at = np.r_[0:20, (1 << 24) - 20:(1 << 24) + 20, N - 20:N]
+    i, c, xs = torch.from_numpy(at).to(dev()), np.arange(K), n64(x)
+    V, L = [], []
+    for codes, s, z in ws:
+        w = codes[i // 16, 0].cpu().numpy().view(np.uint32)  # [rows][lane][word]
+        q = w[np.arange(at.size)[:, None], 16 * (c % 32 // 8)[None] + (at % 16)[:, None], (c // 32)[None]]
+        q = q >> (16 * (c % 2) + 4 * (c % 8 // 2)).astype(np.uint32) & 15
+        h = q.astype(np.int64), s[:, i].cpu().numpy(), z[:, i].cpu().numpy()
+        V.append(xs @ BO.q4_values(*h, group).T)
+        L.append(product_bound(xs, h[1], h[2], group, K))
+    if pair:
+        near(y[:, i], V[0] * V[1], L[0] * (np.abs(V[1]) + L[1]) + np.abs(V[0]) * L[1] + 2 * U * np.abs(V[0] * V[1]), "y")
+    else:
+        near(y[:, i], V[0], L[0], "y")
+    del ws, y
+    torch.cuda.empty_cache()
